@@ -1,7 +1,8 @@
 /*
  * moe.h - C ABI of the GB300 (sm_103a) dropless mixture-of-experts expert
  * layer: router, permutation builder, grouped expert GEMMs (forward and
- * backward) and the MXFP8 quantiser.
+ * backward) and the MXFP8 quantiser; and of the operators around the layer in
+ * a training step: layer norm, vocabulary cross entropy, gradient clipping.
  *
  * Sources of the operations (web pages on the method, cited by title and
  * section):
@@ -57,9 +58,11 @@ typedef enum {
   MOE_ERR_UNSUPPORTED = 2,  /* valid request this build does not implement      */
   MOE_ERR_CUDA = 3,         /* a CUDA launch or driver call failed              */
   MOE_ERR_TIMEOUT = 4,      /* device: a bounded wait ran out (kernel returned) */
-  MOE_ERR_BAD_INDEX = 5,    /* device: an expert index outside [0, E) was seen  */
+  MOE_ERR_BAD_INDEX = 5,    /* device: an expert index outside [0, E), or a target
+                               outside [0, V), was seen                         */
   MOE_ERR_BAD_INPUT = 6     /* device: an input the operation is not defined for
-                               (a NaN logit; a token whose logits are all -inf) */
+                               (a NaN logit; a token whose logits are all -inf;
+                               gradients whose norm is not finite)              */
 } moe_status;
 
 typedef enum {
@@ -282,6 +285,134 @@ moe_status moe_quantize_mxfp8_dual(const void* src, int R, int C, int ld,
                                    const int32_t* rows_limit, uint8_t* q_row,
                                    uint8_t* s_row, uint8_t* q_col, uint8_t* s_col,
                                    int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The rest of a training step around the expert layer: the norm in front of
+ * it, the loss behind it, and the norm and clipping of the gradients.  The
+ * conventions above hold except where a call says otherwise.
+ * ---------------------------------------------------------------------- */
+
+typedef enum { MOE_TYPE_F32 = 0, MOE_TYPE_BF16 = 1 } moe_type;
+
+/* Layer normalisation of T rows of H elements.
+ *   x_type   of x, y, dy and dx;  w_type of gamma, beta, dgamma and dbeta.
+ *   ld_*     elements from one row to the next (>= H): x; y in the forward
+ *            and dy in the backward; dx.
+ *   eps      added to the variance, finite and >= 0.
+ * Limits: T >= 0, H >= 1.  Pointers need only the alignment of their element
+ * type; rows that all start on 16-byte boundaries (in x, y, dy, dx) run
+ * fastest. */
+typedef struct {
+  int T, H;
+  int64_t ld_x, ld_y, ld_dx;
+  moe_type x_type, w_type;
+  float eps;
+} moe_norm_dims;
+
+/* Layer norm:  mean = sum(x) / H,  rstd = 1 / sqrt(sum((x - mean)^2) / H + eps),
+ *   y = (x - mean) * rstd * gamma + beta.
+ *   gamma, beta [H], NULL for 1 and 0.
+ *   mean, rstd  float [T], written for the backward; NULL leaves them out.
+ * Statistics are fp32 (the variance from centred values); y is rounded once.
+ * y may be x (same ld).  A row with a NaN or an infinity gives NaN in that
+ * row only. */
+moe_status moe_layer_norm(const moe_norm_dims* dims, const void* x, const void* gamma,
+                          const void* beta, void* y, float* mean, float* rstd, void* stream);
+
+/* Bytes of the backward's workspace; 0 on invalid dims. */
+size_t moe_layer_norm_workspace_size(const moe_norm_dims* dims);
+
+/* Backward of moe_layer_norm, with h = (x - mean) * rstd and g = gamma * dy:
+ *   dx = rstd * (g - sum(g) / H - h * sum(g * h) / H),
+ *   dgamma = sum over rows of dy * h,  dbeta = sum over rows of dy.
+ *   mean, rstd  from the forward.   dgamma, dbeta [H], NULL leaves one out.
+ *   dx may be dy or x (same ld).  With T = 0 dgamma and dbeta are zero.
+ *   ws  moe_layer_norm_workspace_size bytes, 16-byte aligned (may be NULL
+ *       when dgamma and dbeta are).
+ * Sums over rows are fp32 in a fixed order (same results in every run). */
+moe_status moe_layer_norm_backward(const moe_norm_dims* dims, const void* dy, const void* x,
+                                   const void* gamma, const float* mean, const float* rstd,
+                                   void* dx, void* dgamma, void* dbeta, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+typedef enum { MOE_INDEX_I32 = 0, MOE_INDEX_I64 = 1 } moe_index_type;
+typedef enum { MOE_REDUCE_NONE = 0, MOE_REDUCE_SUM = 1, MOE_REDUCE_MEAN = 2 } moe_reduction;
+
+/* Softmax cross entropy of T hidden states of width H against a vocabulary
+ * of V output rows, bf16 storage with fp32 accumulation.
+ *   ld_x, ld_w    elements from one row to the next of X [T, H] and W [V, H]
+ *                 (>= H, multiples of 8).
+ *   ignore_index  targets with this value do not count (loss 0, gradient 0).
+ *   index_type    of targets.
+ * Limits: T >= 0, V >= 1, H a positive multiple of 8; other H return
+ * MOE_ERR_UNSUPPORTED (TMA rows start on 16-byte boundaries). */
+typedef struct {
+  int T, H, V;
+  int64_t ld_x, ld_w;
+  int ignore_index;
+  moe_index_type index_type;
+} moe_xent_dims;
+
+/* Bytes of the workspace of one call kind (MOE_WS_FORWARD, MOE_WS_BACKWARD);
+ * 0 on invalid dims. */
+size_t moe_cross_entropy_workspace_size(const moe_xent_dims* dims, int which);
+
+/* z = X W^T (formed tile by tile, never stored),
+ *   lse[t]  = log(sum_v exp(z[t, v])),  loss[t] = lse[t] - z[t, targets[t]]
+ * (0 for rows that do not count).
+ *   targets  int32 or int64 [T].  A target outside [0, V) that is not
+ *            ignore_index is reported (MOE_ERR_BAD_INDEX) and not counted.
+ *   loss, lse  float [T].
+ *   total      float [3]: sum of the losses, their mean over the rows that
+ *              count (0 if none does), the number of those rows. */
+moe_status moe_cross_entropy(const moe_xent_dims* dims, const void* X, const void* W,
+                             const void* targets, float* loss, float* lse, float* total, void* ws,
+                             size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Gradients of moe_cross_entropy: with dz[t, v] = s_t (exp(z[t, v] - lse[t])
+ * - [v = targets[t]]) for rows that count, 0 for the others,
+ *   dX = dz W,  dW = dz^T X.
+ * The vocabulary is gone through in pieces: a piece's logits are formed
+ * again, its dz is held in bf16, the products accumulate in fp32.
+ *   reduction  s_t: MOE_REDUCE_NONE dloss[t] (dloss float [T]),
+ *              MOE_REDUCE_SUM dloss[0], MOE_REDUCE_MEAN dloss[0] / total[2].
+ *   lse, total from the forward (total may be NULL unless MEAN).
+ *   dX [T, H], dW [V, H] bf16, contiguous; NULL leaves one out. */
+moe_status moe_cross_entropy_backward(const moe_xent_dims* dims, const void* X, const void* W,
+                                      const void* targets, const float* lse, const float* total,
+                                      const float* dloss, moe_reduction reduction, void* dX,
+                                      void* dW, void* ws, size_t ws_bytes, int32_t* dev_status,
+                                      void* stream);
+
+/* One gradient tensor of n contiguous elements; dst (same type) is used by
+ * moe_clip_grads and may be src, else it must not overlap any src.  Pointers
+ * need only the alignment of their element type; src and dst with the same
+ * offset from a 16-byte boundary run fastest. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t n;
+  moe_type type;
+} moe_grad_tensor;
+
+/* Bytes of the workspace of the two calls below for `count` tensors. */
+size_t moe_grad_workspace_size(int count);
+
+/* Global L2 norm: *norm = sqrt(sum over all tensors of g^2).  `tensors` is
+ * HOST memory, read before the call returns.  Sums are fp32 over a few dozen
+ * elements, double above that; gradients whose squares leave the range of
+ * fp32 are summed in double.  A norm that is not finite is written as it is
+ * and reported (MOE_ERR_BAD_INPUT).  No tensor (or only empty ones): 0.
+ *   norm  float [1] (device).   ws  16-byte aligned. */
+moe_status moe_grad_norm(const moe_grad_tensor* tensors, int count, float* norm, void* ws,
+                         size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* moe_grad_norm, then dst = src * (norm > max_norm ? max_norm / norm : 1),
+ * rounded once.  max_norm is finite and >= 0.  Where the norm is not finite
+ * (reported as above) the gradients are copied unscaled, for the caller to
+ * skip the step. */
+moe_status moe_clip_grads(const moe_grad_tensor* tensors, int count, float max_norm, float* norm,
+                          void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* moe_status_string(moe_status s);

@@ -20,6 +20,11 @@ __all__ = [
     "MOE_DEBUG_NEVER_READY", "MOE_DEBUG_SINGLE_CTA", "MOE_DEBUG_SPLIT_BACKWARD", "MOE_DEBUG_ONE_LAUNCH_BACKWARD", "moe_dims", "moe_route_out", "moe_saved_layout",
     "lib", "header_functions", "moe_max_rows", "moe_workspace_size",
     "moe_saved_layout_of", "moe_route", "moe_route_noalloc", "moe_route_backward", "moe_forward", "moe_backward",
+    "MOE_TYPE_F32", "MOE_TYPE_BF16", "MOE_INDEX_I32", "MOE_INDEX_I64", "MOE_REDUCE_NONE", "MOE_REDUCE_SUM",
+    "MOE_REDUCE_MEAN", "moe_norm_dims", "moe_xent_dims", "moe_grad_tensor", "moe_layer_norm",
+    "moe_layer_norm_workspace_size", "moe_layer_norm_backward", "moe_cross_entropy",
+    "moe_cross_entropy_workspace_size", "moe_cross_entropy_backward", "moe_grad_workspace_size",
+    "moe_grad_norm", "moe_clip_grads",
     "moe_quantize_mxfp8", "moe_quantize_mxfp8_dual", "moe_status_string", "moe_set_debug", "moe_set_gemm_events", "moe_set_gemm_launch_events", "moe_debug_occupy",
     "MoEError",
 ]
@@ -28,6 +33,9 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA = 0, 1, 2, 3
 MOE_ERR_TIMEOUT, MOE_ERR_BAD_INDEX, MOE_ERR_BAD_INPUT = 4, 5, 6
 MOE_F32, MOE_BF16, MOE_MXFP8, MOE_FP8_BWD = 0, 1, 2, 3
 MOE_WS_ROUTE, MOE_WS_FORWARD, MOE_WS_BACKWARD = 0, 1, 2
+MOE_TYPE_F32, MOE_TYPE_BF16 = 0, 1
+MOE_INDEX_I32, MOE_INDEX_I64 = 0, 1
+MOE_REDUCE_NONE, MOE_REDUCE_SUM, MOE_REDUCE_MEAN = 0, 1, 2
 MOE_DEBUG_NEVER_READY = 1
 MOE_DEBUG_SINGLE_CTA = 2
 MOE_DEBUG_SPLIT_BACKWARD = 4
@@ -37,6 +45,7 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
                       "include", "moe.h")
 
 _c_int, _c_size, _vp, _i64 = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int64
+_f32 = ctypes.c_float
 
 
 class moe_dims(ctypes.Structure):
@@ -56,6 +65,20 @@ class moe_saved_layout(ctypes.Structure):
                 ("w2_row_q", _c_size), ("w2_row_sf", _c_size), ("total", _c_size)]
 
 
+class moe_norm_dims(ctypes.Structure):
+    _fields_ = [("T", _c_int), ("H", _c_int), ("ld_x", _i64), ("ld_y", _i64), ("ld_dx", _i64),
+                ("x_type", _c_int), ("w_type", _c_int), ("eps", _f32)]
+
+
+class moe_xent_dims(ctypes.Structure):
+    _fields_ = [("T", _c_int), ("H", _c_int), ("V", _c_int), ("ld_x", _i64), ("ld_w", _i64),
+                ("ignore_index", _c_int), ("index_type", _c_int)]
+
+
+class moe_grad_tensor(ctypes.Structure):
+    _fields_ = [("src", _vp), ("dst", _vp), ("n", _i64), ("type", _c_int)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, code: int, what: str = ""):
         self.code = code
@@ -64,6 +87,9 @@ class MoEError(RuntimeError):
 
 _PD = ctypes.POINTER(moe_dims)
 _PR = ctypes.POINTER(moe_route_out)
+_PN = ctypes.POINTER(moe_norm_dims)
+_PX = ctypes.POINTER(moe_xent_dims)
+_PG = ctypes.POINTER(moe_grad_tensor)
 _SIGS = {
     "moe_max_rows": (_i64, [_PD]),
     "moe_workspace_size": (_c_size, [_PD, _c_int]),
@@ -78,6 +104,17 @@ _SIGS = {
                                     _vp, _vp]),
     "moe_quantize_mxfp8_dual": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp,
                                          _vp, _vp]),
+    "moe_layer_norm": (_c_int, [_PN, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_layer_norm_workspace_size": (_c_size, [_PN]),
+    "moe_layer_norm_backward": (_c_int, [_PN, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_size,
+                                         _vp]),
+    "moe_cross_entropy_workspace_size": (_c_size, [_PX, _c_int]),
+    "moe_cross_entropy": (_c_int, [_PX, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _vp, _vp]),
+    "moe_cross_entropy_backward": (_c_int, [_PX, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp,
+                                            _c_size, _vp, _vp]),
+    "moe_grad_workspace_size": (_c_size, [_c_int]),
+    "moe_grad_norm": (_c_int, [_PG, _c_int, _vp, _vp, _c_size, _vp, _vp]),
+    "moe_clip_grads": (_c_int, [_PG, _c_int, _f32, _vp, _vp, _c_size, _vp, _vp]),
     "moe_status_string": (ctypes.c_char_p, [_c_int]),
     "moe_set_debug": (None, [_c_int, _i64]),
     "moe_set_gemm_events": (None, [_c_int, _vp, _vp]),
@@ -162,6 +199,49 @@ def moe_quantize_mxfp8_dual(src, R, C, ld, rows_limit, q_row, s_row, q_col, s_co
                             stream) -> int:
     return lib().moe_quantize_mxfp8_dual(src, R, C, ld, rows_limit, q_row, s_row, q_col, s_col,
                                          dev_status, stream)
+
+
+def moe_layer_norm(d, x, gamma, beta, y, mean, rstd, stream) -> int:
+    return lib().moe_layer_norm(ctypes.byref(d), x, gamma, beta, y, mean, rstd, stream)
+
+
+def moe_layer_norm_workspace_size(d: moe_norm_dims) -> int:
+    return lib().moe_layer_norm_workspace_size(ctypes.byref(d))
+
+
+def moe_layer_norm_backward(d, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, ws_bytes,
+                            stream) -> int:
+    return lib().moe_layer_norm_backward(ctypes.byref(d), dy, x, gamma, mean, rstd, dx, dgamma,
+                                         dbeta, ws, ws_bytes, stream)
+
+
+def moe_cross_entropy_workspace_size(d: moe_xent_dims, which: int) -> int:
+    return lib().moe_cross_entropy_workspace_size(ctypes.byref(d), which)
+
+
+def moe_cross_entropy(d, X, W, targets, loss, lse, total, ws, ws_bytes, dev_status, stream) -> int:
+    return lib().moe_cross_entropy(ctypes.byref(d), X, W, targets, loss, lse, total, ws, ws_bytes,
+                                   dev_status, stream)
+
+
+def moe_cross_entropy_backward(d, X, W, targets, lse, total, dloss, reduction, dX, dW, ws, ws_bytes,
+                               dev_status, stream) -> int:
+    return lib().moe_cross_entropy_backward(ctypes.byref(d), X, W, targets, lse, total, dloss,
+                                            reduction, dX, dW, ws, ws_bytes, dev_status, stream)
+
+
+def moe_grad_workspace_size(count: int) -> int:
+    return lib().moe_grad_workspace_size(count)
+
+
+def moe_grad_norm(tensors, count, norm, ws, ws_bytes, dev_status, stream) -> int:
+    """tensors: a ctypes array of moe_grad_tensor (host memory)."""
+    return lib().moe_grad_norm(tensors, count, norm, ws, ws_bytes, dev_status, stream)
+
+
+def moe_clip_grads(tensors, count, max_norm, norm, ws, ws_bytes, dev_status, stream) -> int:
+    """tensors: a ctypes array of moe_grad_tensor (host memory)."""
+    return lib().moe_clip_grads(tensors, count, max_norm, norm, ws, ws_bytes, dev_status, stream)
 
 
 def moe_status_string(code: int) -> str:

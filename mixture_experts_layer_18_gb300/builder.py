@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
 
-SOURCES = ["moe_api.cu", "route.cu", "gather.cu", "gemm.cu", "quant.cu"]
+SOURCES = ["moe_api.cu", "route.cu", "gather.cu", "gemm.cu", "quant.cu", "training_api.cu", "norm.cu",
+           "xent.cu", "clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -280,37 +280,12 @@ __device__ __forceinline__ bool wait_counter(const int32_t* ctr, int target, con
   }
 }
 
-// Bounded wait on a barrier that also receives arrivals from the peer CTA.
-__device__ __forceinline__ bool wait_bar_cluster(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 63) == 0) {
-      if (*c.abort) return false;
-      if (global_ns() - t0 > c.limit_ns) {
-        report(c.status, MOE_ERR_TIMEOUT);
-        *c.abort = 1;
-        return false;
-      }
-    }
-  }
-}
-
 // Barriers of a CTA pair also receive arrivals / byte counts from the peer
 // CTA and from 2-CTA commits, so pair kernels wait with cluster scope.
 template <class C>
 __device__ __forceinline__ bool wait_bar_p(uint64_t* bar, uint32_t parity, const WaitCtl& c) {
   if constexpr (C::PAIR == 2) return wait_bar_cluster(bar, parity, c);
   else return wait_bar(bar, parity, c);
-}
-
-// Wait whose only exit besides success is the time limit (teardown drains).
-__device__ __forceinline__ bool wait_bar_drain(uint64_t* bar, uint32_t parity, uint64_t limit) {
-  const uint64_t t0 = global_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (global_ns() - t0 > limit) return false;
-  return true;
 }
 
 template <class C>
@@ -665,44 +640,6 @@ __device__ __forceinline__ void encode_mx_block(float (&v)[32], int64_t row, int
   dc[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-template <typename Elt>
-__device__ __forceinline__ void store32(Elt* dst, const float (&v)[32]) {
-  uint4* d = reinterpret_cast<uint4*>(dst);
-  if constexpr (sizeof(Elt) == 2) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      d[q] = make_uint4(pack_bf16(v[8 * q + 0], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
-                        pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      d[q] = make_uint4(__float_as_uint(v[4 * q + 0]), __float_as_uint(v[4 * q + 1]),
-                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-  }
-}
-
-template <typename Elt>
-__device__ __forceinline__ void load32(const Elt* src, float (&v)[32]) {
-  const uint4* s = reinterpret_cast<const uint4*>(src);
-  if constexpr (sizeof(Elt) == 2) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 w = s[q];
-      v[8 * q + 0] = bf16_lo(w.x); v[8 * q + 1] = bf16_hi(w.x);
-      v[8 * q + 2] = bf16_lo(w.y); v[8 * q + 3] = bf16_hi(w.y);
-      v[8 * q + 4] = bf16_lo(w.z); v[8 * q + 5] = bf16_hi(w.z);
-      v[8 * q + 6] = bf16_lo(w.w); v[8 * q + 7] = bf16_hi(w.w);
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint4 w = s[q];
-      v[4 * q + 0] = __uint_as_float(w.x); v[4 * q + 1] = __uint_as_float(w.y);
-      v[4 * q + 2] = __uint_as_float(w.z); v[4 * q + 3] = __uint_as_float(w.w);
-    }
-  }
-}
-
 // SiLU pieces for the epilogues, with the fast reciprocal (2 ulp): the
 // results are rounded to bf16 right after, so fp32 division rounding is
 // irrelevant.  For u below about -88, exp(-u) is +inf and both give 0.
@@ -713,17 +650,6 @@ __device__ __forceinline__ float silu_f(float u) { return __fdividef(u, 1.f + __
 template <int NTHREADS>
 __device__ __forceinline__ void epi_bar(int group) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NTHREADS) : "memory");
-}
-
-// Staging of bf16 results (per epilogue warp: two 2 KB buffers of 32 rows x
-// 64 bytes, 64-byte swizzle: 16-byte chunk c of row r sits at chunk
-// c ^ ((r >> 1) & 3)), drained by TMA tensor stores.
-__device__ __forceinline__ void stage_bf16_row(uint8_t* buf, int r, const float (&v)[32]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4*>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)) =
-        make_uint4(pack_bf16(v[8 * c + 0], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                   pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
 }
 
 template <typename Elt, int NV>
@@ -1205,17 +1131,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // Row-major [rows, cols] tensor, 128-byte swizzled boxes of
 // box_cols x box_rows elements.
 bool make_tmap(CUtensorMap* m, const void* base, int elem_bytes, int64_t rows, int64_t cols,
-               int box_cols, int box_rows) {
+               int box_cols, int box_rows, int64_t ld) {
   auto enc = encode_fn();
   if (!enc) return false;
   const CUtensorMapDataType dt =
       elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                       : (elem_bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8);
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * elem_bytes};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : cols) * elem_bytes};
   cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t es[2] = {1, 1};
   return enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, es,
@@ -1225,17 +1153,31 @@ bool make_tmap(CUtensorMap* m, const void* base, int elem_bytes, int64_t rows, i
 
 // bf16 output views for the epilogue's bulk stores: 32 x 32 boxes, 64-byte
 // swizzle (matching the staging layout).  2-D [rows, cols] or 3-D [E, M, N].
-bool make_tmap_out(CUtensorMap* m, void* base, int64_t rows, int64_t cols) {
+bool make_tmap_out(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : cols) * 2};
   cuuint32_t box[2] = {32, 32};
   cuuint32_t es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+int sm_count() {
+  static CtxCache<int> cache;
+  int n = 0;
+  cache.get(&n, [](int* v) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+    return e;
+  });
+  return n > 0 ? n : 1;
+}
+
+namespace {
 
 // MXFP8 scale atoms as a [bytes / 128, 128] uint8 tensor, boxes of one
 // 512-byte atom (4 x 128), no swizzle.
@@ -1261,18 +1203,6 @@ bool make_tmap_out3(CUtensorMap* m, void* base, int64_t E, int64_t M, int64_t N)
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count() {
-  static CtxCache<int> cache;
-  int n = 0;
-  cache.get(&n, [](int* v) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
-    return e;
-  });
-  return n > 0 ? n : 1;
 }
 
 // `gang`: tiles of this launch wait on tiles of other CTAs, so it is made a

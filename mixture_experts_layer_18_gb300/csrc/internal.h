@@ -142,6 +142,54 @@ struct EngineLaunch {
 
 cudaError_t launch_engine(const EngineLaunch& L, cudaStream_t s, moe_status* st);
 
+// Tensor maps of row-major [rows, cols] tensors whose rows are `ld` elements
+// apart (0: cols): operand tiles (128-byte swizzle), and 32 x 32 boxes of
+// bf16 results (64-byte swizzle, the layout of stage_bf16_row).
+bool make_tmap(CUtensorMap* m, const void* base, int elem_bytes, int64_t rows, int64_t cols,
+               int box_cols, int box_rows, int64_t ld = 0);
+bool make_tmap_out(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld = 0);
+
+// SMs of the current device.
+int sm_count();
+
+// norm.cu
+struct NormDesc {
+  int T, H;
+  int64_t ld_x, ld_y, ld_dx;   // rows of x; of y (forward) or dy (backward); of dx
+  int xtype, wtype;            // moe_type
+  float eps;
+};
+cudaError_t launch_layer_norm(const NormDesc& d, const void* x, const void* gamma, const void* beta,
+                              void* y, float* mean, float* rstd, cudaStream_t s);
+// Blocks whose column sums `partial` ([blocks][2][H] floats) has to hold.
+int64_t norm_partial_blocks(int T);
+cudaError_t launch_layer_norm_backward(const NormDesc& d, const void* dy, const void* x,
+                                       const void* gamma, const float* mean, const float* rstd,
+                                       void* dx, void* dgamma, void* dbeta, float* partial,
+                                       cudaStream_t s);
+
+// clip.cu
+size_t grad_workspace_bytes(int count);
+cudaError_t launch_grad_clip(const moe_grad_tensor* t, int count, bool clip, float max_norm,
+                             double* partial, float* norm, int32_t* status, cudaStream_t s);
+
+// xent.cu
+struct XentDesc {
+  int T, H, V;
+  int64_t ld_x, ld_w;
+  int ignore_index, index_type;
+  uint64_t wait_ns;
+};
+size_t xent_forward_bytes(const XentDesc& d);
+size_t xent_backward_bytes(const XentDesc& d);
+cudaError_t launch_xent_forward(const XentDesc& d, const void* X, const void* W, const void* targets,
+                                float* loss, float* lse, float* total, char* ws, int32_t* status,
+                                cudaStream_t s, moe_status* st);
+cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W, const void* targets,
+                                 const float* lse, const float* total, const float* dloss,
+                                 int reduction, void* dX, void* dW, char* ws, int32_t* status,
+                                 cudaStream_t s, moe_status* st);
+
 // debug / limits (api.cu)
 uint64_t wait_limit_ns();
 int debug_flags();

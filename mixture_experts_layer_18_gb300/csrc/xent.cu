@@ -1,0 +1,770 @@
+// xent.cu - softmax cross entropy over a large vocabulary, straight from the
+// hidden states, forward and backward.
+//
+//   z = X W^T                          X [T, H], W [V, H], z never stored
+//   lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target
+//   dz = s_t (exp(z - lse_t) - onehot(target)),  dX = dz W,  dW = dz^T X
+//
+// The forward is one GEMM whose epilogue reduces each 256 x 256 logit tile to
+// a maximum and a sum per row (an online softmax, 8 bytes per row and 128
+// columns instead of 512 bytes of logits); a second kernel joins the pieces.
+// The backward goes through the vocabulary in pieces: it forms the piece's
+// logits again, turns them into dz in the epilogue (bf16, [T, piece]) and
+// multiplies that by the piece's weights (added to dX's fp32 sums) and by X
+// (the piece's rows of dW).  Products: 2 T V H flops forward, 6 T V H
+// backward, which is what bounds it for T in the hundreds and more; for a few
+// tokens the bound is reading W.
+//
+// GEMM structure (as the expert engine in gemm.cu): persistent SM pairs
+// (clusters of two CTAs, cta_group::2 tcgen05 MMAs of 256 x 256 x 16), TMA
+// loads into a ring of 64-element K stages, two TMEM accumulators so that one
+// tile's epilogue runs under the next tile's MMAs.  Warp 0 loads A, warp 1
+// issues the MMAs, warps 2..9 are the epilogue (two per TMEM lane quarter,
+// 128 columns each: an exponential per logit is too much for four warps),
+// warp 10 loads B.  Every wait is bounded, as there.
+#include <climits>
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kBK = 64;                         // K elements per stage
+constexpr int kABytes = 128 * 128;              // 128 rows x 64 bf16
+constexpr int kStageBytes = 2 * kABytes;        // a CTA's A rows and its half of B
+constexpr int kAtomBytes = kBK * 128;           // 64 K rows x 64 MN elements (MN-major box)
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
+constexpr int kStgBytes = kEpiWarps * 4096;     // two 32 x 32 bf16 boxes per epilogue warp
+constexpr int kSmemBytes = kStages * kStageBytes + kStgBytes + 1024 + 256;
+constexpr int kTile = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+enum : int { XK_STATS = 0, XK_DZ = 1, XK_DX = 2, XK_DW = 3 };
+
+// One GEMM of a launch.  Operand coordinates are the tile's plus an origin.
+struct XJob {
+  CUtensorMap tmA, tmB, tmO;
+  int kind;
+  int a_mn, b_mn;        // operand stored M-/N-major (1) or K-major (0)
+  int mt, nt, ks;        // 256-row tiles, 256-column tiles, slices of K
+  int kblocks;           // 64-element K blocks of the whole K
+  int group;             // m-tiles that share one sweep over the n-tiles
+  int b_n0, b_k0;        // origins of B (a piece of the vocabulary)
+  int out_m0;            // first output row (DW)
+};
+
+struct XParams {
+  XJob job[3];
+  int njob;
+  int T, H, V;
+  // targets and statistics
+  const void* targets;
+  int index64, ignore_index;
+  const float* lse;
+  const float* dloss;
+  const float* total;    // {sum, mean, count}
+  int reduction;
+  // outputs
+  float2* part;          // STATS: [2 nt][T] {max, sum} in the log2 domain
+  float* zt;             // STATS: [T] target logits
+  float* acc;            // DX: fp32 sums [ks][T][Hp]
+  int Hp;
+  int add, last;         // DX: add to acc; write bf16 results
+  int32_t* status;
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Target of a row: its column, -1 if the row is ignored, -2 if it is outside
+// [0, V) (the caller reports it and treats the row as ignored).
+__device__ __forceinline__ int target_of(const void* targets, int index64, int ignore, int V, int row) {
+  const long long t = index64 ? static_cast<const long long*>(targets)[row]
+                              : (long long)static_cast<const int32_t*>(targets)[row];
+  if (t == ignore) return -1;
+  return t >= 0 && t < V ? (int)t : -2;
+}
+
+struct XTile {
+  int p, kind, m0, n0, ntile, slice, kb0, kb1;
+};
+
+__device__ __forceinline__ XTile decode(const XParams& P, const int (&cum)[4], int t, int rank) {
+  int p = 0;
+  while (p + 1 < P.njob && t >= cum[p + 1]) ++p;
+  const XJob& g = P.job[p];
+  int lt = t - cum[p];
+  XTile ti;
+  ti.p = p;
+  ti.kind = g.kind;
+  ti.slice = lt / (g.mt * g.nt);
+  lt -= ti.slice * g.mt * g.nt;
+  const int gi = lt / (g.group * g.nt);
+  const int r = lt - gi * g.group * g.nt;
+  const int gm = min(g.group, g.mt - gi * g.group);
+  ti.ntile = r / gm;
+  ti.m0 = (gi * g.group + (r - ti.ntile * gm)) * kTile + rank * 128;
+  ti.n0 = ti.ntile * kTile;
+  ti.kb0 = (int)((int64_t)g.kblocks * ti.slice / g.ks);
+  ti.kb1 = (int)((int64_t)g.kblocks * (ti.slice + 1) / g.ks);
+  return ti;
+}
+
+// Loads A (part 0, which also arms the leader's full barrier) or B (part 1)
+// of every stage: this CTA's 128 rows of A, its 128 of the tile's 256 B columns.
+__device__ void load_role(const XParams& P, const int (&cum)[4], int rank, uint8_t* stages,
+                          uint64_t* full, uint64_t* empty, const WaitCtl& wc, int part) {
+  int it = 0;
+  const int cl = blockIdx.x / 2, ncl = gridDim.x / 2;
+  bool ok = true;
+  for (int t = cl; ok && t < cum[P.njob]; t += ncl) {
+    const XTile ti = decode(P, cum, t, rank);
+    const XJob& g = P.job[ti.p];
+    const int n0 = ti.n0 + rank * 128 + g.b_n0;
+    for (int kb = ti.kb0; kb < ti.kb1; ++kb, ++it) {
+      const int s = it % kStages;
+      if (!wait_bar_cluster(&empty[s], ((it / kStages) & 1) ^ 1, wc)) { ok = false; break; }
+      const uint32_t fbar = mapa_shared(smem_u32(&full[s]), 0);
+      uint8_t* sA = stages + s * kStageBytes;
+      const int k0 = kb * kBK;
+      if (part == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+        if (g.a_mn) {
+          tma_load_2d_pair(sA, &g.tmA, ti.m0, k0, fbar);
+          tma_load_2d_pair(sA + kAtomBytes, &g.tmA, ti.m0 + 64, k0, fbar);
+        } else {
+          tma_load_2d_pair(sA, &g.tmA, k0, ti.m0, fbar);
+        }
+      } else {
+        uint8_t* sB = sA + kABytes;
+        if (g.b_mn) {
+          tma_load_2d_pair(sB, &g.tmB, n0, k0 + g.b_k0, fbar);
+          tma_load_2d_pair(sB + kAtomBytes, &g.tmB, n0 + 64, k0 + g.b_k0, fbar);
+        } else {
+          tma_load_2d_pair(sB, &g.tmB, k0 + g.b_k0, n0, fbar);
+        }
+      }
+    }
+  }
+  // the latest use of every stage has landed before the CTA leaves
+  if (rank == 0 && part == 0) {
+    const int n = it < kStages ? it : kStages;
+    for (int q = 1; q <= n; ++q) {
+      const int u = it - q;
+      wait_bar_drain(&full[u % kStages], (u / kStages) & 1, wc.limit_ns);
+    }
+  }
+}
+
+// One thread of the leader CTA issues every MMA of the pair.
+__device__ void mma_role(const XParams& P, const int (&cum)[4], uint8_t* stages, uint64_t* full,
+                         uint64_t* empty, uint64_t* tfull, uint64_t* tempty, uint64_t* drain,
+                         uint32_t tmem_base, const WaitCtl& wc) {
+  int acc = 0, s = 0;
+  uint32_t ph = 0, soff = 0;
+  const uint32_t sbase = smem_u32(stages);
+  const int cl = blockIdx.x / 2, ncl = gridDim.x / 2;
+  bool ok = true;
+  for (int t = cl; ok && t < cum[P.njob]; t += ncl, ++acc) {
+    const XTile ti = decode(P, cum, t, 0);
+    const XJob& g = P.job[ti.p];
+    const int buf = acc & 1;
+    if (!wait_bar_cluster(&tempty[buf], ((acc >> 1) & 1) ^ 1, wc)) break;
+    tc_fence_after();
+    const uint32_t d = tmem_base + buf * kTile;
+    const uint32_t a_mn = g.a_mn ? 1u : 0u, b_mn = g.b_mn ? 1u : 0u;
+    // D fp32, A and B bf16, their majors, N = 256, M = 256
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) |
+                           ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+    const uint64_t a0 = smem_desc_sw128(sbase, a_mn ? kAtomBytes : 16, 1024);
+    const uint64_t b0 = smem_desc_sw128(sbase + kABytes, b_mn ? kAtomBytes : 16, 1024);
+    // an MMA's K step: 16 rows of an MN-major block, or 32 bytes of a row
+    const uint32_t ak = a_mn ? (16 * 128) >> 4 : 2, bk = b_mn ? (16 * 128) >> 4 : 2;
+    for (int kb = ti.kb0; kb < ti.kb1; ++kb) {
+      if (!wait_bar_cluster(&full[s], ph, wc)) { ok = false; break; }
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_f16_pair(d, a0 + soff + kk * ak, b0 + soff + kk * bk, idesc, kb != ti.kb0 || kk != 0);
+      tc_commit_pair(&empty[s], 3);
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1;
+        soff = 0;
+      } else {
+        soff += kStageBytes >> 4;
+      }
+    }
+    if (ok) tc_commit_pair(&tfull[buf], 3);
+  }
+  tc_commit_pair(drain, 1);
+  wait_bar_drain(drain, 0, wc.limit_ns);
+}
+
+// Scale of a row's dz: the gradient that reaches its loss.
+__device__ __forceinline__ float row_scale(const XParams& P, int row) {
+  if (P.reduction == MOE_REDUCE_NONE) return P.dloss[row];
+  if (P.reduction == MOE_REDUCE_SUM) return P.dloss[0];
+  return P.dloss[0] / fmaxf(P.total[2], 1.f);   // total[2]: rows that count
+}
+
+template <bool BWD>
+__device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, uint64_t* tfull,
+                              uint64_t* tempty, uint32_t tmem_base, uint8_t* stg, const WaitCtl& wc) {
+  const int ew = (threadIdx.x >> 5) - 2;
+  const int q = (threadIdx.x >> 5) & 3;          // TMEM lane quarter of this warp
+  const int half = ew >> 2;                      // columns [128 half, 128 half + 128)
+  const int lane = threadIdx.x & 31;
+  const int cl = blockIdx.x / 2, ncl = gridDim.x / 2;
+  uint8_t* sb0 = stg + ew * 4096;
+  uint8_t* sb1 = sb0 + 2048;
+  const uint32_t te0 = mapa_shared(smem_u32(&tempty[0]), 0);
+  const uint32_t te1 = mapa_shared(smem_u32(&tempty[1]), 0);
+  // two 32-column boxes of bf16 results; columns at or past `cols` are left out
+  auto store_boxes = [&](const CUtensorMap* m, const float (&a)[32], const float (&b)[32], int x, int y,
+                         int cols) {
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+    stage_bf16_row(sb0, lane, a);
+    stage_bf16_row(sb1, lane, b);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (x < cols) tma_store_2d(m, sb0, x, y);
+      if (x + 32 < cols) tma_store_2d(m, sb1, x + 32, y);
+      bulk_commit();
+    }
+  };
+  int acc = 0;
+  for (int t = cl; t < cum[P.njob]; t += ncl, ++acc) {
+    const XTile ti = decode(P, cum, t, rank);
+    const XJob& g = P.job[ti.p];
+    const int buf = acc & 1;
+    const int y0 = ti.m0 + q * 32;               // first row of this warp
+    const int row = y0 + lane;
+    const int c0 = half * 128;
+    const bool rows = ti.kind != XK_DW;          // output rows are tokens
+    const bool live = !rows || row < P.T;
+    int tgt = -1;
+    float lse2 = 0.f, scale = 0.f;
+    if (ti.kind <= XK_DZ && live) {
+      tgt = target_of(P.targets, P.index64, P.ignore_index, P.V, row);
+      if (BWD && tgt == -2 && ti.n0 == 0) report(P.status, MOE_ERR_BAD_INDEX);
+      if (BWD && tgt >= 0) {
+        lse2 = P.lse[row] * kLog2e;
+        scale = row_scale(P, row);
+      }
+    }
+    const bool got = wait_bar_cluster(&tfull[buf], (acc >> 1) & 1, wc);
+    if (!__all_sync(0xffffffffu, got)) break;
+    tc_fence_after();
+    const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * kTile + c0;
+    if (!BWD) {
+      const int v0 = ti.n0 + c0;                 // first vocabulary entry of this warp
+      float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        float v[32];
+        tmem_ld32(taddr + c, v);
+        if (v0 + c + 32 > P.V) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (v0 + c + i >= P.V) v[i] = -INFINITY;
+        }
+        const int rel = tgt - (v0 + c);
+        if (__any_sync(0xffffffffu, tgt >= 0 && rel >= 0 && rel < 32)) {
+          float z = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) z = rel == i ? v[i] : z;
+          if (tgt >= 0 && rel >= 0 && rel < 32) P.zt[row] = z;
+        }
+        float cm = v[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) cm = fmaxf(cm, v[i]);
+        const float mn = fmaxf(m, cm * kLog2e);
+        const float ref = mn == -INFINITY ? 0.f : mn;   // nothing finite so far: every term is 0
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          a += ex2(fmaf(v[i], kLog2e, -ref));
+          b += ex2(fmaf(v[i + 1], kLog2e, -ref));
+        }
+        s = s * ex2(m - ref) + (a + b);
+        m = mn;
+      }
+      if (live) P.part[(size_t)(2 * ti.ntile + half) * P.T + row] = make_float2(m, s);
+    } else if (ti.kind == XK_DZ) {
+      const int v0 = g.b_n0 + ti.n0 + c0;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        float a[32], b[32];
+        tmem_ld32x2(taddr + c, taddr + c + 32, a, b);
+        const int rel = tgt - (v0 + c);
+        const bool here = __any_sync(0xffffffffu, tgt >= 0 && rel >= 0 && rel < 64);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          a[i] = ex2(fmaf(a[i], kLog2e, -lse2));
+          b[i] = ex2(fmaf(b[i], kLog2e, -lse2));
+        }
+        if (here) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            a[i] -= rel == i ? 1.f : 0.f;
+            b[i] -= rel == i + 32 ? 1.f : 0.f;
+          }
+        }
+        // an ignored row is exactly zero, whatever its logits; so are the
+        // columns past the vocabulary that pad the last piece
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          a[i] = tgt >= 0 ? a[i] * scale : 0.f;
+          b[i] = tgt >= 0 ? b[i] * scale : 0.f;
+        }
+        if (v0 + c + 64 > P.V) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (v0 + c + i >= P.V) a[i] = 0.f;
+            if (v0 + c + 32 + i >= P.V) b[i] = 0.f;
+          }
+        }
+        if (y0 < P.T) store_boxes(&g.tmO, a, b, ti.n0 + c0 + c, y0, INT_MAX);
+      }
+    } else if (ti.kind == XK_DX) {
+      float* sums = P.acc + ((size_t)ti.slice * P.T + (live ? row : 0)) * P.Hp + ti.n0 + c0;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        float a[32], b[32];
+        tmem_ld32x2(taddr + c, taddr + c + 32, a, b);
+        if (ti.kb0 == ti.kb1) {                  // a slice with no K: nothing was multiplied
+#pragma unroll
+          for (int i = 0; i < 32; ++i) a[i] = b[i] = 0.f;
+        }
+        if (P.add && live) {
+          float u[32];
+          load32<float>(sums + c, u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) a[i] += u[i];
+          load32<float>(sums + c + 32, u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) b[i] += u[i];
+        }
+        if (P.last) {
+          if (y0 < P.T) store_boxes(&g.tmO, a, b, ti.n0 + c0 + c, y0, P.H);
+        } else if (live) {
+          store32<float>(sums + c, a);
+          store32<float>(sums + c + 32, b);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        float a[32], b[32];
+        tmem_ld32x2(taddr + c, taddr + c + 32, a, b);
+        if (g.out_m0 + y0 < P.V) store_boxes(&g.tmO, a, b, ti.n0 + c0 + c, g.out_m0 + y0, P.H);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(buf ? te1 : te0);
+  }
+  if (lane == 0) bulk_wait_all();
+  __syncwarp();
+}
+
+template <bool BWD>
+__global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* stages = smem;
+  uint8_t* stg = smem + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg + kStgBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int rank = (int)cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    for (int p = 0; p < P.njob; ++p) {
+      tma_prefetch_desc(&P.job[p].tmA);
+      tma_prefetch_desc(&P.job[p].tmB);
+    }
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_holder, 2 * kTile);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();                            // the peer's barriers exist
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  int cum[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int p = 0; p < 3; ++p)
+    cum[p + 1] = cum[p] + (p < P.njob ? P.job[p].mt * P.job[p].nt * P.job[p].ks : 0);
+  const WaitCtl wc{abort_flag, P.status, P.wait_ns};
+  if (warp == 0) {
+    if ((threadIdx.x & 31) == 0) load_role(P, cum, rank, stages, full, empty, wc, 0);
+    __syncwarp();
+  } else if (warp == 1) {
+    if ((threadIdx.x & 31) == 0 && rank == 0)
+      mma_role(P, cum, stages, full, empty, tfull, tempty, drain, tmem_base, wc);
+    __syncwarp();
+  } else if (warp < 2 + kEpiWarps) {
+    epilogue_role<BWD>(P, cum, rank, tfull, tempty, tmem_base, stg, wc);
+  } else {
+    if ((threadIdx.x & 31) == 0) load_role(P, cum, rank, stages, full, empty, wc, 1);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  // after an abort, copies that either CTA issued may still be on their way
+  // to the other: they land within microseconds
+  if (threadIdx.x == 0 && *abort_flag) {
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 200000) __nanosleep(1000);
+  }
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 2 * kTile);
+}
+
+// Joins the pieces of each row: 32 rows per block, a warp per slice of the
+// pieces (a lane per row, so reads are coalesced), then a tree over warps.
+__global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int np, const float* zt,
+                                                         const void* targets, int index64, int ignore,
+                                                         int T, int V, float* loss, float* lse,
+                                                         int32_t* status) {
+  __shared__ float2 sm[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.f;
+  auto join = [](float& m, float& s, float m2, float s2) {
+    const float mn = fmaxf(m, m2);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    s = s * ex2(m - ref) + s2 * ex2(m2 - ref);
+    m = mn;
+  };
+  if (row < T)
+    for (int i = w; i < np; i += 32) {
+      const float2 p = part[(size_t)i * T + row];
+      join(m, s, p.x, p.y);
+    }
+  sm[lane][w] = make_float2(m, s);
+  __syncthreads();
+  // warp w joins the 32 slices of row w
+  const float2 mine = sm[w][lane];
+  m = mine.x;
+  s = mine.y;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    join(m, s, m2, s2);
+  }
+  const int r = blockIdx.x * 32 + w;
+  if (lane == 0 && r < T) {
+    const float l = (m + log2f(s)) * 0.6931471805599453f;
+    const int t = target_of(targets, index64, ignore, V, r);
+    if (t == -2) report(status, MOE_ERR_BAD_INDEX);
+    lse[r] = l;
+    loss[r] = t >= 0 ? l - zt[r] : 0.f;
+  }
+}
+
+// {sum, mean, number} of the losses of the rows that count.
+__global__ void __launch_bounds__(1024) xent_total_kernel(const float* loss, const void* targets,
+                                                          int index64, int ignore, int T, int V,
+                                                          float* total) {
+  __shared__ double ss[32];
+  __shared__ int sc[32];
+  double s = 0.0;
+  int n = 0;
+  for (int r = threadIdx.x; r < T; r += 1024)
+    if (target_of(targets, index64, ignore, V, r) >= 0) {
+      s += (double)loss[r];
+      ++n;
+    }
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if (lane == 0) {
+    ss[w] = s;
+    sc[w] = n;
+  }
+  __syncthreads();
+  if (w) return;
+  s = ss[lane];
+  n = sc[lane];
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if (lane == 0) {
+    total[0] = (float)s;
+    total[1] = n ? (float)(s / n) : 0.f;
+    total[2] = (float)n;
+  }
+}
+
+// dX from the slices' fp32 sums (H a multiple of 8).
+__global__ void __launch_bounds__(256) xent_dx_kernel(const float* acc, int ks, int T, int H, int Hp,
+                                                      __nv_bfloat16* dX) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = H / 8;
+  if (i >= (int64_t)T * per) return;
+  const int64_t row = i / per;
+  const int c = (int)(i - row * per) * 8;
+  float v[8] = {};
+  for (int k = 0; k < ks; ++k) {
+    const float4* p = reinterpret_cast<const float4*>(acc + ((size_t)k * T + row) * Hp + c);
+    const float4 a = p[0], b = p[1];
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+  *reinterpret_cast<uint4*>(dX + row * H + c) =
+      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                 pack_bf16(v[6], v[7]));
+}
+
+// ------------------------------------------------------------------ host
+int up(int64_t a, int b) { return (int)((a + b - 1) / b); }
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// m-tiles that keep their rows of A in L2 (48 MB) through one sweep over N.
+int group_for(int64_t row_bytes) {
+  const int64_t g = (48LL << 20) / (kTile * row_bytes);
+  return g < 1 ? 1 : (int)(g < 4096 ? g : 4096);
+}
+
+template <bool BWD>
+cudaError_t launch(const XParams& P, cudaStream_t s) {
+  auto kern = xent_gemm_kernel<BWD>;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static CtxCache<int> resident;   // pairs that run at once, per context
+  int pairs = 0;
+  cudaError_t e = resident.get(&pairs, [&](int* v) {
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (r != cudaSuccess) return r;
+    cudaLaunchConfig_t c = cfg;
+    c.gridDim = dim3(2 * (sm_count() / 2), 1, 1);
+    int n = 0;
+    r = cudaOccupancyMaxActiveClusters(&n, kern, &c);
+    if (r == cudaSuccess && n < 1) r = cudaErrorInvalidConfiguration;
+    *v = n;
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  int64_t tiles = 0;
+  for (int p = 0; p < P.njob; ++p) tiles += (int64_t)P.job[p].mt * P.job[p].nt * P.job[p].ks;
+  if (tiles < pairs) pairs = (int)tiles;
+  cfg.gridDim = dim3(2 * pairs, 1, 1);
+  return cudaLaunchKernelEx(&cfg, kern, P);
+}
+
+struct FwdWs {
+  size_t part, zt, total;
+  int np;
+};
+FwdWs fwd_ws(const XentDesc& d) {
+  FwdWs w;
+  w.np = 2 * up(d.V, kTile);
+  size_t o = 0;
+  w.part = o; o += align256((size_t)w.np * d.T * sizeof(float2));
+  w.zt = o; o += align256((size_t)d.T * sizeof(float));
+  w.total = o ? o : 256;
+  return w;
+}
+
+// The backward's pieces of the vocabulary: [T, piece] of dz in bf16 is held
+// to about 256 MB, and a piece to whole tiles.
+struct BwdWs {
+  size_t dz, acc, total;
+  int piece, slices, Hp;
+};
+BwdWs bwd_ws(const XentDesc& d) {
+  BwdWs w;
+  const int vp = up(d.V, kTile) * kTile;
+  int64_t piece = (256LL << 20) / (2 * (d.T < 1 ? 1 : (int64_t)d.T)) / kTile * kTile;
+  if (piece < 4096) piece = 4096;
+  w.piece = piece < vp ? (int)piece : vp;
+  w.Hp = up(d.H, kTile) * kTile;
+  // few dX tiles: their K (the piece) is cut into slices until every SM pair
+  // has two tiles; a slice keeps at least 512 columns
+  const int tiles = up(d.T < 1 ? 1 : d.T, kTile) * up(d.H, kTile);
+  int ks = up(152, tiles);
+  if (ks > w.piece / 512) ks = w.piece / 512;
+  w.slices = ks < 1 ? 1 : ks;
+  size_t o = 0;
+  w.dz = o; o += align256((size_t)d.T * w.piece * 2);
+  w.acc = o; o += align256((size_t)w.slices * d.T * w.Hp * sizeof(float));
+  w.total = o ? o : 256;
+  return w;
+}
+
+XParams params_of(const XentDesc& d, const void* targets, int32_t* status) {
+  XParams P;
+  memset(&P, 0, sizeof(P));
+  P.T = d.T;
+  P.H = d.H;
+  P.V = d.V;
+  P.targets = targets;
+  P.index64 = d.index_type == MOE_INDEX_I64;
+  P.ignore_index = d.ignore_index;
+  P.status = status;
+  P.wait_ns = d.wait_ns;
+  return P;
+}
+
+bool logits_job(XJob& g, const XentDesc& d, const void* X, const void* W, int v0, int cols) {
+  g.mt = up(d.T, kTile);
+  g.nt = up(cols, kTile);
+  g.ks = 1;
+  g.kblocks = up(d.H, kBK);
+  g.group = group_for(2 * (int64_t)d.H);
+  g.b_n0 = v0;
+  return make_tmap(&g.tmA, X, 2, d.T, d.H, kBK, 128, d.ld_x) &&
+         make_tmap(&g.tmB, W, 2, d.V, d.H, kBK, 128, d.ld_w);
+}
+
+}  // namespace
+
+size_t xent_forward_bytes(const XentDesc& d) { return fwd_ws(d).total; }
+size_t xent_backward_bytes(const XentDesc& d) { return bwd_ws(d).total; }
+
+#define XENT_TRY(expr)                       \
+  do {                                       \
+    const cudaError_t e_ = (expr);           \
+    if (e_ != cudaSuccess) return e_;        \
+  } while (0)
+
+cudaError_t launch_xent_forward(const XentDesc& d, const void* X, const void* W, const void* targets,
+                                float* loss, float* lse, float* total, char* ws, int32_t* status,
+                                cudaStream_t s, moe_status* st) {
+  *st = MOE_OK;
+  const FwdWs w = fwd_ws(d);
+  const int i64 = d.index_type == MOE_INDEX_I64;
+  if (d.T > 0) {
+    XParams P = params_of(d, targets, status);
+    P.part = reinterpret_cast<float2*>(ws + w.part);
+    P.zt = reinterpret_cast<float*>(ws + w.zt);
+    P.njob = 1;
+    P.job[0].kind = XK_STATS;
+    if (!logits_job(P.job[0], d, X, W, 0, d.V)) {
+      *st = MOE_ERR_CUDA;
+      return cudaSuccess;
+    }
+    XENT_TRY(launch<false>(P, s));
+    xent_join_kernel<<<up(d.T, 32), 1024, 0, s>>>(P.part, w.np, P.zt, targets, i64, d.ignore_index, d.T,
+                                                 d.V, loss, lse, status);
+    XENT_TRY(cudaGetLastError());
+  }
+  xent_total_kernel<<<1, 1024, 0, s>>>(loss, targets, i64, d.ignore_index, d.T, d.V, total);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W, const void* targets,
+                                 const float* lse, const float* total, const float* dloss,
+                                 int reduction, void* dX, void* dW, char* ws, int32_t* status,
+                                 cudaStream_t s, moe_status* st) {
+  *st = MOE_OK;
+  if (d.T == 0)   // no token: dW is zero
+    return dW ? cudaMemsetAsync(dW, 0, (size_t)d.V * d.H * 2, s) : cudaSuccess;
+  if (!dX && !dW) return cudaSuccess;
+  const BwdWs w = bwd_ws(d);
+  void* dz = ws + w.dz;
+  for (int v0 = 0; v0 < d.V; v0 += w.piece) {
+    const int cols = d.V - v0 < w.piece ? d.V - v0 : w.piece;
+    const bool last = v0 + cols == d.V;
+    // dz of the piece
+    XParams P = params_of(d, targets, status);
+    P.lse = lse;
+    P.dloss = dloss;
+    P.total = total;
+    P.reduction = reduction;
+    P.njob = 1;
+    P.job[0].kind = XK_DZ;
+    bool ok = logits_job(P.job[0], d, X, W, v0, cols) &&
+              make_tmap_out(&P.job[0].tmO, dz, d.T, w.piece, w.piece);
+    if (ok) XENT_TRY(launch<true>(P, s));
+    // dX (+)= dz W[piece], dW[piece] = dz^T X
+    XParams Q = params_of(d, targets, status);
+    Q.acc = reinterpret_cast<float*>(ws + w.acc);
+    Q.Hp = w.Hp;
+    Q.add = v0 > 0;
+    Q.last = last && w.slices == 1;
+    if (ok && dX) {
+      XJob& g = Q.job[Q.njob++];
+      g.kind = XK_DX;
+      g.b_mn = 1;
+      g.mt = up(d.T, kTile);
+      g.nt = up(d.H, kTile);
+      g.kblocks = up(cols, kBK);
+      g.ks = w.slices;
+      g.group = 8;
+      g.b_k0 = v0;
+      ok = make_tmap(&g.tmA, dz, 2, d.T, w.piece, kBK, 128, w.piece) &&
+           make_tmap(&g.tmB, W, 2, d.V, d.H, 64, kBK, d.ld_w) && make_tmap_out(&g.tmO, dX, d.T, d.H);
+    }
+    if (ok && dW) {
+      XJob& g = Q.job[Q.njob++];
+      g.kind = XK_DW;
+      g.a_mn = g.b_mn = 1;
+      g.mt = up(cols, kTile);
+      g.nt = up(d.H, kTile);
+      g.kblocks = up(d.T, kBK);
+      g.ks = 1;
+      g.group = 8;
+      g.out_m0 = v0;
+      ok = make_tmap(&g.tmA, dz, 2, d.T, w.piece, 64, kBK, w.piece) &&
+           make_tmap(&g.tmB, X, 2, d.T, d.H, 64, kBK, d.ld_x) && make_tmap_out(&g.tmO, dW, d.V, d.H);
+    }
+    if (!ok) {
+      *st = MOE_ERR_CUDA;
+      return cudaSuccess;
+    }
+    XENT_TRY(launch<true>(Q, s));
+  }
+  if (dX && w.slices > 1) {
+    const int64_t n = (int64_t)d.T * (d.H / 8);
+    xent_dx_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
+        reinterpret_cast<const float*>(ws + w.acc), w.slices, d.T, d.H, w.Hp,
+        static_cast<__nv_bfloat16*>(dX));
+    return cudaGetLastError();
+  }
+  return cudaSuccess;
+}
+
+}  // namespace moe
