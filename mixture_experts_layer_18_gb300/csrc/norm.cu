@@ -566,15 +566,10 @@ cudaError_t fwd_typed(FwdArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-struct BwdPlan {
-  bool fused;
-  int L, cpt, rows, smem, blocks;
+// Resident blocks per SM of one form of the backward, by warps per block.
+struct Occupancy {
+  int per_sm[kBwdThreads / 32 + 1];
 };
-
-template <typename X, int VEC, int CPT, int S>
-constexpr int ring_bytes(int threads) {
-  return VEC > 1 ? threads * S * 2 * (CPT / VEC) * 16 : 0;
-}
 
 template <typename X, int VEC, int CPT, int S>
 cudaError_t run_bwd(BwdArgs& a, int64_t max_blocks, int* blocks_out, cudaStream_t s) {
@@ -583,19 +578,21 @@ cudaError_t run_bwd(BwdArgs& a, int64_t max_blocks, int* blocks_out, cudaStream_
   a.L = L;
   const int rows = L >= 256 ? 1 : 256 / L;
   const int threads = rows * L;
+  constexpr int kRing = VEC > 1 ? S * 2 * (CPT / VEC) * 16 : 0;    // bytes per thread
   const int sums = rows > 1 ? rows * 2 * a.H * 4 : 0;
-  const int ring = ring_bytes<X, VEC, CPT, S>(threads);
-  const int smem = ring > sums ? ring : sums;
-  static CtxCache<int> opt_in;
-  int ok = 0;
-  cudaError_t e = opt_in.get(&ok, [&](int* v) {
-    *v = 1;
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+  const int smem = kRing * threads > sums ? kRing * threads : sums;
+  static CtxCache<Occupancy> cache;
+  Occupancy occ;
+  cudaError_t e = cache.get(&occ, [&](Occupancy* o) {
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kRing * kBwdThreads > 65536 ? kRing * kBwdThreads : 65536);
+    o->per_sm[0] = 1;
+    for (int w = 1; w <= kBwdThreads / 32 && r == cudaSuccess; ++w)
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o->per_sm[w], kern, 32 * w, kRing * 32 * w);
+    return r;
   });
   if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
-  if (e != cudaSuccess) return e;
+  const int per_sm = occ.per_sm[threads / 32];
   int64_t blocks = (int64_t)sm_count() * (per_sm < 1 ? 1 : per_sm);
   const int64_t need = ((int64_t)a.T + rows - 1) / rows;
   if (blocks > need) blocks = need;

@@ -3,7 +3,7 @@
 //
 //   z = X W^T                          X [T, H], W [V, H], z never stored
 //   lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target
-//   dz = s_t (exp(z - lse_t) - onehot(target)),  dX = dz W,  dW = dz^T X
+//   dz = exp(z - lse_t) - onehot(target),  dX = s dz W,  dW = s dz^T X
 //
 // The forward is one GEMM whose epilogue reduces each 256 x 256 logit tile to
 // a maximum and a sum per row (an online softmax, 8 bytes per row and 128
@@ -210,11 +210,15 @@ __device__ void mma_role(const XParams& P, const int (&cum)[4], uint8_t* stages,
   wait_bar_drain(drain, 0, wc.limit_ns);
 }
 
-// Scale of a row's dz: the gradient that reaches its loss.
-__device__ __forceinline__ float row_scale(const XParams& P, int row) {
-  if (P.reduction == MOE_REDUCE_NONE) return P.dloss[row];
-  if (P.reduction == MOE_REDUCE_SUM) return P.dloss[0];
-  return P.dloss[0] / fmaxf(P.total[2], 1.f);   // total[2]: rows that count
+// The gradient that reaches the losses: one factor for all rows (SUM, MEAN)
+// multiplies dX and dW in fp32, so dz = exp(z - lse) - onehot is rounded to
+// bf16 without it (at a target that is not predicted dz is about -1, which
+// bf16 holds; a factor such as 1/1000 would put the same rounding error into
+// every such row).  A factor per row (NONE) goes into dz.
+__device__ __forceinline__ float common_scale(const float* dloss, const float* total, int reduction) {
+  if (reduction == MOE_REDUCE_NONE) return 1.f;
+  if (reduction == MOE_REDUCE_SUM) return dloss[0];
+  return dloss[0] / fmaxf(total[2], 1.f);   // total[2]: rows that count
 }
 
 template <bool BWD>
@@ -244,6 +248,7 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
       bulk_commit();
     }
   };
+  const float gs = BWD ? common_scale(P.dloss, P.total, P.reduction) : 1.f;
   int acc = 0;
   for (int t = cl; t < cum[P.njob]; t += ncl, ++acc) {
     const XTile ti = decode(P, cum, t, rank);
@@ -261,7 +266,7 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
       if (BWD && tgt == -2 && ti.n0 == 0) report(P.status, MOE_ERR_BAD_INDEX);
       if (BWD && tgt >= 0) {
         lse2 = P.lse[row] * kLog2e;
-        scale = row_scale(P, row);
+        scale = P.reduction == MOE_REDUCE_NONE ? P.dloss[row] : 1.f;
       }
     }
     const bool got = wait_bar_cluster(&tfull[buf], (acc >> 1) & 1, wc);
@@ -358,6 +363,11 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
           for (int i = 0; i < 32; ++i) b[i] += u[i];
         }
         if (P.last) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            a[i] *= gs;
+            b[i] *= gs;
+          }
           if (y0 < P.T) store_boxes(&g.tmO, a, b, ti.n0 + c0 + c, y0, P.H);
         } else if (live) {
           store32<float>(sums + c, a);
@@ -369,6 +379,11 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
       for (int c = 0; c < 128; c += 64) {
         float a[32], b[32];
         tmem_ld32x2(taddr + c, taddr + c + 32, a, b);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          a[i] *= gs;
+          b[i] *= gs;
+        }
         if (g.out_m0 + y0 < P.V) store_boxes(&g.tmO, a, b, ti.n0 + c0 + c, g.out_m0 + y0, P.H);
       }
     }
@@ -531,7 +546,8 @@ __global__ void __launch_bounds__(1024) xent_total_kernel(const float* loss, con
 
 // dX from the slices' fp32 sums (H a multiple of 8).
 __global__ void __launch_bounds__(256) xent_dx_kernel(const float* acc, int ks, int T, int H, int Hp,
-                                                      __nv_bfloat16* dX) {
+                                                      const float* dloss, const float* total,
+                                                      int reduction, __nv_bfloat16* dX) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = H / 8;
   if (i >= (int64_t)T * per) return;
@@ -544,6 +560,9 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float* acc, int ks, 
     v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
     v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
   }
+  const float gs = common_scale(dloss, total, reduction);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= gs;
   *reinterpret_cast<uint4*>(dX + row * H + c) =
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                  pack_bf16(v[6], v[7]));
@@ -710,10 +729,10 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
     const bool last = v0 + cols == d.V;
     // dz of the piece
     XParams P = params_of(d, targets, status);
-    P.lse = lse;
     P.dloss = dloss;
     P.total = total;
     P.reduction = reduction;
+    P.lse = lse;
     P.njob = 1;
     P.job[0].kind = XK_DZ;
     bool ok = logits_job(P.job[0], d, X, W, v0, cols) &&
@@ -721,6 +740,9 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
     if (ok) XENT_TRY(launch<true>(P, s));
     // dX (+)= dz W[piece], dW[piece] = dz^T X
     XParams Q = params_of(d, targets, status);
+    Q.dloss = dloss;
+    Q.total = total;
+    Q.reduction = reduction;
     Q.acc = reinterpret_cast<float*>(ws + w.acc);
     Q.Hp = w.Hp;
     Q.add = v0 > 0;
@@ -760,7 +782,7 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
   if (dX && w.slices > 1) {
     const int64_t n = (int64_t)d.T * (d.H / 8);
     xent_dx_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
-        reinterpret_cast<const float*>(ws + w.acc), w.slices, d.T, d.H, w.Hp,
+        reinterpret_cast<const float*>(ws + w.acc), w.slices, d.T, d.H, w.Hp, dloss, total, reduction,
         static_cast<__nv_bfloat16*>(dX));
     return cudaGetLastError();
   }

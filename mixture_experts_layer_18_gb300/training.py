@@ -17,11 +17,15 @@ from . import (MOE_ERR_INVALID_ARG, MOE_INDEX_I32, MOE_INDEX_I64, MOE_OK, MOE_RE
                moe_cross_entropy_backward, moe_cross_entropy_workspace_size, moe_grad_norm,
                moe_grad_tensor, moe_grad_workspace_size, moe_layer_norm, moe_layer_norm_backward,
                moe_layer_norm_workspace_size, moe_norm_dims, moe_xent_dims)
-from .layer import _ptr, _stream
+from .layer import _ptr
 
 TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
 INDEX_TYPES = {torch.int32: MOE_INDEX_I32, torch.int64: MOE_INDEX_I64}
 REDUCTIONS = {"none": MOE_REDUCE_NONE, "sum": MOE_REDUCE_SUM, "mean": MOE_REDUCE_MEAN}
+
+
+# torch.cuda.current_stream(index).cuda_stream without the Stream object (3 us)
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _require(ok, what):
@@ -29,34 +33,54 @@ def _require(ok, what):
         raise MoEError(MOE_ERR_INVALID_ARG, what)
 
 
-def _call(rc, what):
-    if rc != MOE_OK:
-        raise MoEError(rc, what)
-
-
 class _Op:
-    def _fits(self, name, t, shape, dtype, strided=False, optional=False):
-        """`t` has this shape and type on this device, contiguous or (strided)
-        with rows of adjacent elements."""
-        if t is None and optional:
-            return
-        _require(isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape)
-                 and t.device == self.device, f"{name}: expected {dtype} {tuple(shape)} on {self.device}")
-        if strided:
-            _require(t.numel() == 0 or t.shape[1] == 1 or t.stride(1) == 1,
-                     f"{name}: rows of adjacent elements are expected")
-            _require(self._ld(t) >= t.shape[1], f"{name}: overlapping rows")
-        else:
-            _require(t.is_contiguous(), f"{name}: a contiguous tensor is expected")
+    """The checks cost about as much as a small kernel, so they are a few
+    comparisons each and build no text unless something is wrong."""
 
-    @staticmethod
-    def _ld(t):
-        """Elements from one row of `t` to the next."""
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    def _fits(self, name, t, shape, dtype):
+        """`t` is a contiguous tensor of this shape and type on this device;
+        returns its address."""
+        try:
+            ok = (t.dtype is dtype and t.shape == shape and t.get_device() == self.index
+                  and t.is_contiguous())
+        except AttributeError:
+            ok = False
+        if not ok:
+            self._refuse(name, t, shape, dtype, "contiguous")
+        return t.data_ptr()
+
+    def _fits_or_none(self, name, t, shape, dtype):
+        return None if t is None else self._fits(name, t, shape, dtype)
+
+    def _rows(self, name, t, shape, dtype):
+        """As _fits, for rows of adjacent elements that may lie apart (a slice
+        of a wider buffer); returns the address and the distance of rows."""
+        try:
+            ok = t.dtype is dtype and t.shape == shape and t.get_device() == self.index
+            ld, step = t.stride()
+        except (AttributeError, ValueError):
+            ok = False
+        rows, cols = shape
+        if ok and rows <= 1:
+            ld = cols
+        if not ok or ld < cols or (step != 1 and cols > 1 and rows > 0):
+            self._refuse(name, t, shape, dtype, "adjacent elements in rows that do not overlap")
+        return t.data_ptr(), ld
+
+    def _refuse(self, name, t, shape, dtype, layout):
+        got = f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}" \
+            if isinstance(t, torch.Tensor) else repr(t)
+        raise MoEError(MOE_ERR_INVALID_ARG, f"{name}: expected {dtype} {tuple(shape)} on {self.device}, "
+                                            f"{layout}; got {got}")
+
+    def _current(self, stream):
+        """Handle of `stream`, or of the device's current stream."""
+        return stream.cuda_stream if stream is not None else _current_stream(self.index)
 
     def _device(self, device):
         d = torch.device(device)
-        self.device = torch.device("cuda", torch.cuda.current_device()) if d.index is None else d
+        self.index = torch.cuda.current_device() if d.index is None else d.index
+        self.device = torch.device("cuda", self.index)
 
     def device_status(self) -> int:
         return int(self.status[0].item())
@@ -75,40 +99,41 @@ class LayerNorm(_Op):
         _require(dtype in TYPES and weight_dtype in TYPES, "LayerNorm: float32 or bfloat16")
         self.T, self.H, self.dtype, self.weight_dtype, self.eps = T, H, dtype, weight_dtype, eps
         self._device(device)
-        need = moe_layer_norm_workspace_size(self._dims(H, H, H))
+        self.shape = torch.Size((T, H))
+        self.dims = moe_norm_dims(T, H, H, H, H, TYPES[dtype], TYPES[weight_dtype], eps)
+        need = moe_layer_norm_workspace_size(self.dims)
         _require(need > 0, "LayerNorm: invalid sizes")
         f32 = dict(dtype=torch.float32, device=self.device)
         self.mean = torch.empty(T, **f32) if backward else None
         self.rstd = torch.empty(T, **f32) if backward else None
+        self._stats = (_ptr(self.mean), _ptr(self.rstd))
         self.ws = torch.empty(need if backward else 0, dtype=torch.uint8, device=self.device)
-
-    def _dims(self, ld_x, ld_y, ld_dx):
-        return moe_norm_dims(self.T, self.H, ld_x, ld_y, ld_dx, TYPES[self.dtype],
-                             TYPES[self.weight_dtype], self.eps)
 
     def forward(self, x, gamma, beta, y, stream=None):
         """y = layer norm of x; gamma and beta may be None (1 and 0)."""
-        T, H = self.T, self.H
-        for n, t in (("x", x), ("y", y)):
-            self._fits(n, t, (T, H), self.dtype, strided=True)
-        for n, t in (("gamma", gamma), ("beta", beta)):
-            self._fits(n, t, (H,), self.weight_dtype, optional=True)
-        _call(moe_layer_norm(self._dims(self._ld(x), self._ld(y), H), _ptr(x), _ptr(gamma), _ptr(beta),
-                             _ptr(y), _ptr(self.mean), _ptr(self.rstd), _stream(stream)),
-              "moe_layer_norm")
+        d, shape, dt, wt, w = self.dims, self.shape, self.dtype, self.weight_dtype, self.shape[1:]
+        x, d.ld_x = self._rows("x", x, shape, dt)
+        y, d.ld_y = self._rows("y", y, shape, dt)
+        gamma = self._fits_or_none("gamma", gamma, w, wt)
+        beta = self._fits_or_none("beta", beta, w, wt)
+        rc = moe_layer_norm(d, x, gamma, beta, y, *self._stats, self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_layer_norm")
 
     def backward(self, dy, x, gamma, dx, dgamma=None, dbeta=None, stream=None):
         """dx, dgamma and dbeta (None leaves one out) of the last forward's x."""
-        T, H = self.T, self.H
+        d, shape, dt, wt, w = self.dims, self.shape, self.dtype, self.weight_dtype, self.shape[1:]
         _require(self.mean is not None, "LayerNorm: built with backward=False")
-        for n, t in (("dy", dy), ("x", x), ("dx", dx)):
-            self._fits(n, t, (T, H), self.dtype, strided=True)
-        for n, t in (("gamma", gamma), ("dgamma", dgamma), ("dbeta", dbeta)):
-            self._fits(n, t, (H,), self.weight_dtype, optional=True)
-        _call(moe_layer_norm_backward(self._dims(self._ld(x), self._ld(dy), self._ld(dx)), _ptr(dy),
-                                      _ptr(x), _ptr(gamma), _ptr(self.mean), _ptr(self.rstd), _ptr(dx),
-                                      _ptr(dgamma), _ptr(dbeta), _ptr(self.ws), self.ws.numel(),
-                                      _stream(stream)), "moe_layer_norm_backward")
+        dy, d.ld_y = self._rows("dy", dy, shape, dt)
+        x, d.ld_x = self._rows("x", x, shape, dt)
+        dx, d.ld_dx = self._rows("dx", dx, shape, dt)
+        gamma = self._fits_or_none("gamma", gamma, w, wt)
+        dgamma = self._fits_or_none("dgamma", dgamma, w, wt)
+        dbeta = self._fits_or_none("dbeta", dbeta, w, wt)
+        rc = moe_layer_norm_backward(d, dy, x, gamma, *self._stats, dx, dgamma, dbeta,
+                                     self.ws.data_ptr(), self.ws.numel(), self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_layer_norm_backward")
 
     def empty_io(self):
         """Output tensors: y, dx, dgamma, dbeta."""
@@ -130,12 +155,12 @@ class CrossEntropy(_Op):
         self.T, self.H, self.V, self.ignore_index = T, H, V, ignore_index
         self.index_dtype = index_dtype
         self._device(device)
-        dims = self._dims(H, H)
-        need = moe_cross_entropy_workspace_size(dims, MOE_WS_FORWARD)
+        self.dims = moe_xent_dims(T, H, V, H, H, ignore_index, INDEX_TYPES[index_dtype])
+        need = moe_cross_entropy_workspace_size(self.dims, MOE_WS_FORWARD)
         _require(need > 0, "CrossEntropy: invalid sizes (H has to be a multiple of 8)")
         if backward:
             # the two calls of a step run one after the other: one workspace
-            need = max(need, moe_cross_entropy_workspace_size(dims, MOE_WS_BACKWARD))
+            need = max(need, moe_cross_entropy_workspace_size(self.dims, MOE_WS_BACKWARD))
         f32 = dict(dtype=torch.float32, device=self.device)
         self.loss = torch.empty(T, **f32)
         self.lse = torch.empty(T, **f32)
@@ -144,37 +169,38 @@ class CrossEntropy(_Op):
         self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
         self.with_backward = backward
-
-    def _dims(self, ld_x, ld_w):
-        return moe_xent_dims(self.T, self.H, self.V, ld_x, ld_w, self.ignore_index,
-                             INDEX_TYPES[self.index_dtype])
+        self._out = (self.loss.data_ptr(), self.lse.data_ptr(), self.total.data_ptr())
 
     def _inputs(self, X, W, targets):
-        self._fits("X", X, (self.T, self.H), torch.bfloat16, strided=True)
-        self._fits("W", W, (self.V, self.H), torch.bfloat16, strided=True)
-        self._fits("targets", targets, (self.T,), self.index_dtype)
-        return self._dims(self._ld(X), self._ld(W))
+        d = self.dims
+        X, d.ld_x = self._rows("X", X, (self.T, self.H), torch.bfloat16)
+        W, d.ld_w = self._rows("W", W, (self.V, self.H), torch.bfloat16)
+        return d, X, W, self._fits("targets", targets, (self.T,), self.index_dtype)
 
     def forward(self, X, W, targets, stream=None):
-        dims = self._inputs(X, W, targets)
-        _call(moe_cross_entropy(dims, _ptr(X), _ptr(W), _ptr(targets), _ptr(self.loss), _ptr(self.lse),
-                                _ptr(self.total), _ptr(self.ws), self.ws.numel(), _ptr(self.status),
-                                _stream(stream)), "moe_cross_entropy")
+        d, X, W, targets = self._inputs(X, W, targets)
+        rc = moe_cross_entropy(d, X, W, targets, *self._out, self.ws.data_ptr(), self.ws.numel(),
+                               self.status.data_ptr(), self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_cross_entropy")
 
     def backward(self, X, W, targets, dloss, dX, dW, reduction="mean", stream=None):
         """dX and dW (None leaves one out) after ``forward`` on the same inputs.
         dloss: the gradient of each row's loss [T] (reduction "none"), or of
         their sum or mean [1]."""
-        dims = self._inputs(X, W, targets)
         _require(self.with_backward, "CrossEntropy: built with backward=False")
         _require(reduction in REDUCTIONS, "CrossEntropy: reduction is none, sum or mean")
-        self._fits("dloss", dloss, (self.T if reduction == "none" else 1,), torch.float32)
-        self._fits("dX", dX, (self.T, self.H), torch.bfloat16, optional=True)
-        self._fits("dW", dW, (self.V, self.H), torch.bfloat16, optional=True)
-        _call(moe_cross_entropy_backward(dims, _ptr(X), _ptr(W), _ptr(targets), _ptr(self.lse),
-                                         _ptr(self.total), _ptr(dloss), REDUCTIONS[reduction], _ptr(dX),
-                                         _ptr(dW), _ptr(self.ws), self.ws.numel(), _ptr(self.status),
-                                         _stream(stream)), "moe_cross_entropy_backward")
+        d, X, W, targets = self._inputs(X, W, targets)
+        n = self.T if reduction == "none" else 1
+        dloss = self._fits("dloss", dloss, (n,), torch.float32)
+        dX = self._fits_or_none("dX", dX, (self.T, self.H), torch.bfloat16)
+        dW = self._fits_or_none("dW", dW, (self.V, self.H), torch.bfloat16)
+        _, lse, total = self._out
+        rc = moe_cross_entropy_backward(d, X, W, targets, lse, total, dloss, REDUCTIONS[reduction], dX,
+                                        dW, self.ws.data_ptr(), self.ws.numel(),
+                                        self.status.data_ptr(), self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_cross_entropy_backward")
 
     def empty_io(self):
         """Output tensors of the backward: dX, dW."""
@@ -203,13 +229,17 @@ class GradClip(_Op):
         self.ws = torch.empty(moe_grad_workspace_size(len(self.grads)), dtype=torch.uint8,
                               device=self.device)
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self._buffers = (self.norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
+                         self.status.data_ptr())
 
     def measure(self, stream=None):
         """The norm alone."""
-        _call(moe_grad_norm(self.list, len(self.grads), _ptr(self.norm), _ptr(self.ws),
-                            self.ws.numel(), _ptr(self.status), _stream(stream)), "moe_grad_norm")
+        rc = moe_grad_norm(self.list, len(self.grads), *self._buffers, self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_grad_norm")
 
     def clip(self, max_norm, stream=None):
         """out = grads * min(1, max_norm / norm)."""
-        _call(moe_clip_grads(self.list, len(self.grads), max_norm, _ptr(self.norm), _ptr(self.ws),
-                             self.ws.numel(), _ptr(self.status), _stream(stream)), "moe_clip_grads")
+        rc = moe_clip_grads(self.list, len(self.grads), max_norm, *self._buffers, self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_clip_grads")
