@@ -30,6 +30,18 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31; }
 
+// ------------------------------------------------------------- launch order
+// For kernels launched with launch_after(): returns once the kernel before
+// this one has completed and its writes are visible.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Allows the blocks of a kernel launched after this one to start (they still
+// wait for all of this kernel's work).
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // --------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
@@ -204,6 +216,16 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* s
                                              int y, int z) {
   asm volatile(
       "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+          reinterpret_cast<uint64_t>(m)),
+      "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem_src))
+      : "memory");
+}
+// Bulk tensor add shared -> global (fp32 maps): each element of the box is
+// added to the one in memory.
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, const void* smem_src, int x, int y,
+                                           int z) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
           reinterpret_cast<uint64_t>(m)),
       "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem_src))
       : "memory");
@@ -546,6 +568,15 @@ __device__ __forceinline__ void stage_bf16_row(uint8_t* buf, int r, const float 
     *reinterpret_cast<uint4*>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)) =
         make_uint4(pack_bf16(v[8 * c + 0], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
                    pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+}
+
+// Staging of fp32 results: 32 rows x 128 bytes, 128-byte swizzle (16-byte
+// chunk c of row r at chunk c ^ (r & 7)); the buffer is 1024-byte aligned.
+__device__ __forceinline__ void stage_f32_row(uint8_t* buf, int r, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4*>(buf + r * 128 + ((c ^ (r & 7)) << 4)) =
+        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
 
 }  // namespace moe

@@ -148,9 +148,31 @@ cudaError_t launch_engine(const EngineLaunch& L, cudaStream_t s, moe_status* st)
 bool make_tmap(CUtensorMap* m, const void* base, int elem_bytes, int64_t rows, int64_t cols,
                int box_cols, int box_rows, int64_t ld = 0);
 bool make_tmap_out(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld = 0);
+// fp32 results [n, rows, cols]: 32 x 32 boxes of one matrix (128-byte swizzle,
+// the layout of stage_f32_row); cols a multiple of 4.
+bool make_tmap_out_f32(CUtensorMap* m, void* base, int64_t n, int64_t rows, int64_t cols);
 
 // SMs of the current device.
 int sm_count();
+
+// Launch of a kernel that follows another one of the same call on the same
+// stream: its blocks may start while the last blocks of the first kernel run,
+// so every thread has to call wait_for_previous() (common.cuh) before it reads
+// what that kernel wrote, or writes what it may still read.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
 
 // norm.cu
 struct NormDesc {

@@ -22,7 +22,6 @@
 // issues the MMAs, warps 2..9 are the epilogue (two per TMEM lane quarter,
 // 128 columns each: an exponential per logit is too much for four warps),
 // warp 10 loads B.  Every wait is bounded, as there.
-#include <climits>
 #include <cstring>
 
 #include "common.cuh"
@@ -43,6 +42,8 @@ constexpr int kStgBytes = kEpiWarps * 4096;     // two 32 x 32 bf16 boxes per ep
 constexpr int kSmemBytes = kStages * kStageBytes + kStgBytes + 1024 + 256;
 constexpr int kTile = 256;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFewTokens = 16;                  // most tokens of the kernel for few tokens
+constexpr int kFewMaxBlocks = 512;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 enum : int { XK_STATS = 0, XK_DZ = 1, XK_DX = 2, XK_DW = 3 };
@@ -52,7 +53,8 @@ struct XJob {
   CUtensorMap tmA, tmB, tmO;
   int kind;
   int a_mn, b_mn;        // operand stored M-/N-major (1) or K-major (0)
-  int mt, nt, ks;        // 256-row tiles, 256-column tiles, slices of K
+  int tn;                // tile width (MMA N): 256, or 192 (K-major B)
+  int mt, nt, ks;        // 256-row tiles, tn-column tiles, slices of K
   int kblocks;           // 64-element K blocks of the whole K
   int group;             // m-tiles that share one sweep over the n-tiles
   int b_n0, b_k0;        // origins of B (a piece of the vocabulary)
@@ -73,7 +75,9 @@ struct XParams {
   // outputs
   float2* part;          // STATS: [2 nt][T] {max, sum} in the log2 domain
   float* zt;             // STATS: [T] target logits
+  unsigned* ticket;      // STATS: zeroed for the join kernel
   float* acc;            // DX: fp32 sums [ks][T][Hp]
+  int zcols;             // DZ: columns of the dz buffer
   int Hp;
   int add, last;         // DX: add to acc; write bf16 results
   int32_t* status;
@@ -114,14 +118,14 @@ __device__ __forceinline__ XTile decode(const XParams& P, const int (&cum)[4], i
   const int gm = min(g.group, g.mt - gi * g.group);
   ti.ntile = r / gm;
   ti.m0 = (gi * g.group + (r - ti.ntile * gm)) * kTile + rank * 128;
-  ti.n0 = ti.ntile * kTile;
+  ti.n0 = ti.ntile * g.tn;
   ti.kb0 = (int)((int64_t)g.kblocks * ti.slice / g.ks);
   ti.kb1 = (int)((int64_t)g.kblocks * (ti.slice + 1) / g.ks);
   return ti;
 }
 
 // Loads A (part 0, which also arms the leader's full barrier) or B (part 1)
-// of every stage: this CTA's 128 rows of A, its 128 of the tile's 256 B columns.
+// of every stage: this CTA's 128 rows of A and its half of the tile's B columns.
 __device__ void load_role(const XParams& P, const int (&cum)[4], int rank, uint8_t* stages,
                           uint64_t* full, uint64_t* empty, const WaitCtl& wc, int part) {
   int it = 0;
@@ -130,7 +134,8 @@ __device__ void load_role(const XParams& P, const int (&cum)[4], int rank, uint8
   for (int t = cl; ok && t < cum[P.njob]; t += ncl) {
     const XTile ti = decode(P, cum, t, rank);
     const XJob& g = P.job[ti.p];
-    const int n0 = ti.n0 + rank * 128 + g.b_n0;
+    const int n0 = ti.n0 + rank * (g.tn / 2) + g.b_n0;
+    const uint32_t bytes = 2 * (kABytes + g.tn * 64);   // both CTAs' A rows and halves of B
     for (int kb = ti.kb0; kb < ti.kb1; ++kb, ++it) {
       const int s = it % kStages;
       if (!wait_bar_cluster(&empty[s], ((it / kStages) & 1) ^ 1, wc)) { ok = false; break; }
@@ -138,7 +143,7 @@ __device__ void load_role(const XParams& P, const int (&cum)[4], int rank, uint8
       uint8_t* sA = stages + s * kStageBytes;
       const int k0 = kb * kBK;
       if (part == 0) {
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
         if (g.a_mn) {
           tma_load_2d_pair(sA, &g.tmA, ti.m0, k0, fbar);
           tma_load_2d_pair(sA + kAtomBytes, &g.tmA, ti.m0 + 64, k0, fbar);
@@ -183,9 +188,9 @@ __device__ void mma_role(const XParams& P, const int (&cum)[4], uint8_t* stages,
     tc_fence_after();
     const uint32_t d = tmem_base + buf * kTile;
     const uint32_t a_mn = g.a_mn ? 1u : 0u, b_mn = g.b_mn ? 1u : 0u;
-    // D fp32, A and B bf16, their majors, N = 256, M = 256
+    // D fp32, A and B bf16, their majors, N, M = 256
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) |
-                           ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+                           ((uint32_t)(g.tn >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
     const uint64_t a0 = smem_desc_sw128(sbase, a_mn ? kAtomBytes : 16, 1024);
     const uint64_t b0 = smem_desc_sw128(sbase + kABytes, b_mn ? kAtomBytes : 16, 1024);
     // an MMA's K step: 16 rows of an MN-major block, or 32 bytes of a row
@@ -226,7 +231,7 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
                               uint64_t* tempty, uint32_t tmem_base, uint8_t* stg, const WaitCtl& wc) {
   const int ew = (threadIdx.x >> 5) - 2;
   const int q = (threadIdx.x >> 5) & 3;          // TMEM lane quarter of this warp
-  const int half = ew >> 2;                      // columns [128 half, 128 half + 128)
+  const int half = ew >> 2;                      // which half of the tile's columns
   const int lane = threadIdx.x & 31;
   const int cl = blockIdx.x / 2, ncl = gridDim.x / 2;
   uint8_t* sb0 = stg + ew * 4096;
@@ -256,7 +261,7 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
     const int buf = acc & 1;
     const int y0 = ti.m0 + q * 32;               // first row of this warp
     const int row = y0 + lane;
-    const int c0 = half * 128;
+    const int cw = g.tn / 2, c0 = half * cw;     // this warp's columns
     const bool rows = ti.kind != XK_DW;          // output rows are tokens
     const bool live = !rows || row < P.T;
     int tgt = -1;
@@ -277,7 +282,7 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
       const int v0 = ti.n0 + c0;                 // first vocabulary entry of this warp
       float m = -INFINITY, s = 0.f;
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
+      for (int c = 0; c < cw; c += 32) {
         float v[32];
         tmem_ld32(taddr + c, v);
         if (v0 + c + 32 > P.V) {
@@ -310,9 +315,10 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
     } else if (ti.kind == XK_DZ) {
       const int v0 = g.b_n0 + ti.n0 + c0;
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 64) {
+      for (int c = 0; c < cw; c += 64) {         // (96 columns: the second box of the last turn is left out)
         float a[32], b[32];
-        tmem_ld32x2(taddr + c, taddr + c + 32, a, b);
+        const bool two = c + 32 < cw;
+        tmem_ld32x2(taddr + c, taddr + (two ? c + 32 : c), a, b);
         const int rel = tgt - (v0 + c);
         const bool here = __any_sync(0xffffffffu, tgt >= 0 && rel >= 0 && rel < 64);
 #pragma unroll
@@ -341,20 +347,16 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
             if (v0 + c + 32 + i >= P.V) b[i] = 0.f;
           }
         }
-        if (y0 < P.T) store_boxes(&g.tmO, a, b, ti.n0 + c0 + c, y0, INT_MAX);
+        const int x = ti.n0 + c0 + c;
+        if (y0 < P.T) store_boxes(&g.tmO, a, b, x, y0, two ? P.zcols : min(P.zcols, x + 32));
       }
-    } else if (ti.kind == XK_DX) {
-      float* sums = P.acc + ((size_t)ti.slice * P.T + (live ? row : 0)) * P.Hp + ti.n0 + c0;
+    } else if (ti.kind == XK_DX && P.last) {     // the sums of the pieces before + this one, to bf16
+      const float* sums = P.acc + ((size_t)ti.slice * P.T + (live ? row : 0)) * P.Hp + ti.n0 + c0;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 64) {
-        float a[32], b[32];
+        float a[32], b[32], u[32];
         tmem_ld32x2(taddr + c, taddr + c + 32, a, b);
-        if (ti.kb0 == ti.kb1) {                  // a slice with no K: nothing was multiplied
-#pragma unroll
-          for (int i = 0; i < 32; ++i) a[i] = b[i] = 0.f;
-        }
         if (P.add && live) {
-          float u[32];
           load32<float>(sums + c, u);
 #pragma unroll
           for (int i = 0; i < 32; ++i) a[i] += u[i];
@@ -362,16 +364,32 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
 #pragma unroll
           for (int i = 0; i < 32; ++i) b[i] += u[i];
         }
-        if (P.last) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            a[i] *= gs;
-            b[i] *= gs;
-          }
-          if (y0 < P.T) store_boxes(&g.tmO, a, b, ti.n0 + c0 + c, y0, P.H);
-        } else if (live) {
-          store32<float>(sums + c, a);
-          store32<float>(sums + c + 32, b);
+        for (int i = 0; i < 32; ++i) {
+          a[i] *= gs;
+          b[i] *= gs;
+        }
+        if (y0 < P.T) store_boxes(&g.tmO, a, b, ti.n0 + c0 + c, y0, P.H);
+      }
+    } else if (ti.kind == XK_DX) {               // fp32 sums, written or added to by bulk copies
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        float v[32];
+        tmem_ld32(taddr + c, v);
+        if (ti.kb0 == ti.kb1) {                  // a slice with no K: nothing was multiplied
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        if (y0 >= P.T) continue;
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+        stage_f32_row(sb0, lane, v);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (P.add) tma_add_3d(&g.tmO, sb0, ti.n0 + c0 + c, y0, ti.slice);
+          else tma_store_3d(&g.tmO, sb0, ti.n0 + c0 + c, y0, ti.slice);
+          bulk_commit();
         }
       }
     } else {
@@ -411,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
 
   const int warp = threadIdx.x >> 5;
   const int rank = (int)cluster_ctarank();
+  let_next_start();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -433,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
   __syncthreads();
   cluster_sync_all();                            // the peer's barriers exist
   tc_fence_after();
+  wait_for_previous();
+  if (!BWD && blockIdx.x == 0 && threadIdx.x == 0) *P.ticket = 0;   // of the join kernel
   const uint32_t tmem_base = *tmem_holder;
   int cum[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -466,22 +487,43 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
   if (warp == 1) tmem_dealloc_pair(tmem_base, 2 * kTile);
 }
 
-// Joins the pieces of each row: 32 rows per block, a warp per slice of the
-// pieces (a lane per row, so reads are coalesced), then a tree over warps.
+// Joins the pieces of each row (32 rows per block, a warp per slice of the
+// pieces with a lane per row, so reads are coalesced; then a tree over the
+// warps), and sums the losses up: each block its rows, the last block to
+// finish all blocks' sums, in their order.
+struct BlockSum {
+  double sum;
+  int count, pad;
+};
+
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+  const float mn = fmaxf(m, m2);
+  const float ref = mn == -INFINITY ? 0.f : mn;
+  s = s * ex2(m - ref) + s2 * ex2(m2 - ref);
+  m = mn;
+}
+
+__device__ __forceinline__ void warp_sum(double& s, int& n) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+}
+
 __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int np, const float* zt,
                                                          const void* targets, int index64, int ignore,
                                                          int T, int V, float* loss, float* lse,
-                                                         int32_t* status) {
+                                                         BlockSum* sums, unsigned* ticket,
+                                                         float* total, int32_t* status) {
   __shared__ float2 sm[32][33];
+  __shared__ double ss[32];
+  __shared__ int sc[32];
+  __shared__ bool last;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int row = blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.f;
-  auto join = [](float& m, float& s, float m2, float s2) {
-    const float mn = fmaxf(m, m2);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    s = s * ex2(m - ref) + s2 * ex2(m2 - ref);
-    m = mn;
-  };
+  wait_for_previous();
   if (row < T)
     for (int i = w; i < np; i += 32) {
       const float2 p = part[(size_t)i * T + row];
@@ -493,54 +535,189 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int
   const float2 mine = sm[w][lane];
   m = mine.x;
   s = mine.y;
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
     join(m, s, m2, s2);
   }
   const int r = blockIdx.x * 32 + w;
-  if (lane == 0 && r < T) {
-    const float l = (m + log2f(s)) * 0.6931471805599453f;
-    const int t = target_of(targets, index64, ignore, V, r);
-    if (t == -2) report(status, MOE_ERR_BAD_INDEX);
-    lse[r] = l;
-    loss[r] = t >= 0 ? l - zt[r] : 0.f;
-  }
-}
-
-// {sum, mean, number} of the losses of the rows that count.
-__global__ void __launch_bounds__(1024) xent_total_kernel(const float* loss, const void* targets,
-                                                          int index64, int ignore, int T, int V,
-                                                          float* total) {
-  __shared__ double ss[32];
-  __shared__ int sc[32];
-  double s = 0.0;
-  int n = 0;
-  for (int r = threadIdx.x; r < T; r += 1024)
-    if (target_of(targets, index64, ignore, V, r) >= 0) {
-      s += (double)loss[r];
-      ++n;
-    }
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (int o = 16; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    n += __shfl_xor_sync(0xffffffffu, n, o);
-  }
   if (lane == 0) {
-    ss[w] = s;
+    double mine_loss = 0.0;
+    int counts = 0;
+    if (r < T) {
+      const float l = (m + log2f(s)) * 0.6931471805599453f;
+      const int t = target_of(targets, index64, ignore, V, r);
+      if (t == -2) report(status, MOE_ERR_BAD_INDEX);
+      counts = t >= 0;
+      const float v = counts ? l - zt[r] : 0.f;
+      lse[r] = l;
+      loss[r] = v;
+      mine_loss = v;
+    }
+    ss[w] = mine_loss;
+    sc[w] = counts;
+  }
+  __syncthreads();
+  if (w == 0) {
+    double a = ss[lane];
+    int n = sc[lane];
+    warp_sum(a, n);
+    if (lane == 0) {
+      sums[blockIdx.x] = BlockSum{a, n, 0};
+      __threadfence();
+      last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double a = 0.0;
+  int n = 0;
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += 1024) {
+    a += __ldcg(&sums[i].sum);
+    n += __ldcg(&sums[i].count);
+  }
+  warp_sum(a, n);
+  if (lane == 0) {
+    ss[w] = a;
     sc[w] = n;
   }
   __syncthreads();
   if (w) return;
-  s = ss[lane];
+  a = ss[lane];
   n = sc[lane];
-  for (int o = 16; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    n += __shfl_xor_sync(0xffffffffu, n, o);
-  }
+  warp_sum(a, n);
   if (lane == 0) {
-    total[0] = (float)s;
-    total[1] = n ? (float)(s / n) : 0.f;
+    total[0] = (float)a;
+    total[1] = n ? (float)(a / n) : 0.f;
     total[2] = (float)n;
+  }
+}
+
+// ------------------------------------------------------------ few tokens
+// The forward for at most 16 tokens (scoring while generating): the bound is
+// reading W once, and a 256-row MMA tile would be nearly empty.  A warp takes
+// 16 vocabulary rows at a time straight from memory into the fragments of
+// m16n8k16 products (A: the rows, B: the tokens, from shared memory).  K may be
+// taken in any order as long as both operands agree, so a lane's four K
+// positions of two consecutive products are eight adjacent columns: one
+// 16-byte load per row.  Every lane keeps a running maximum and sum of its
+// tokens over all rows it sees; lanes, warps and blocks are joined at the end.
+// TOKMEASURE
+constexpr int kFewWarps = 8, kFewPerSm = 2, kFewAhead = 4;
+
+struct FewArgs {
+  const __nv_bfloat16* X;
+  const __nv_bfloat16* W;
+  const void* targets;
+  float2* part;
+  float* zt;
+  unsigned* ticket;
+  int64_t ld_x, ld_w;
+  int T, H, V, index64, ignore, pitch;   // pitch: bytes of a token's row in shared memory
+};
+
+__device__ __forceinline__ uint4 load_stream16(const void* p) {
+  uint4 u;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(p));
+  return u;
+}
+
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int NB>   // blocks of 8 tokens
+__global__ void __launch_bounds__(32 * kFewWarps, kFewPerSm) xent_few_kernel(const FewArgs a) {
+  extern __shared__ __align__(16) uint8_t xs[];          // [8 NB][pitch]
+  __shared__ float2 sm[kFewWarps][8 * NB];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  let_next_start();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  const int words = a.pitch / 16;
+  for (int i = threadIdx.x; i < 8 * NB * words; i += 32 * kFewWarps) {
+    const int n = i / words, c = (i - n * words) * 8;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (n < a.T && c < a.H) u = *reinterpret_cast<const uint4*>(a.X + n * a.ld_x + c);
+    *reinterpret_cast<uint4*>(xs + n * a.pitch + c * 2) = u;
+  }
+  int tgt[2 * NB];
+  float m[2 * NB], s[2 * NB];
+#pragma unroll
+  for (int j = 0; j < 2 * NB; ++j) {
+    const int n = (j >> 1) * 8 + 2 * t + (j & 1);
+    tgt[j] = n < a.T ? target_of(a.targets, a.index64, a.ignore, a.V, n) : -1;
+    m[j] = -INFINITY;
+    s[j] = 0.f;
+  }
+  __syncthreads();
+  const int tasks = (a.V + 15) / 16, chunks = (a.H + 31) / 32;
+  const uint8_t* xl = xs + g * a.pitch + t * 16;          // this lane's part of B
+  // consecutive tasks go to different blocks, so that the last, partial round
+  // is spread over all SMs
+  for (int task = w * gridDim.x + blockIdx.x; task < tasks; task += kFewWarps * gridDim.x) {
+    const int r0 = task * 16 + g, r1 = r0 + 8;
+    const __nv_bfloat16* p0 = a.W + (int64_t)r0 * a.ld_w + t * 8;
+    const __nv_bfloat16* p1 = a.W + (int64_t)r1 * a.ld_w + t * 8;
+    float c[NB][4] = {};
+    uint4 u0[kFewAhead], u1[kFewAhead];
+    auto load = [&](int q, uint4& x, uint4& y) {
+      const bool in = q * 32 + t * 8 < a.H;
+      x = in && r0 < a.V ? load_stream16(p0 + q * 32) : make_uint4(0, 0, 0, 0);
+      y = in && r1 < a.V ? load_stream16(p1 + q * 32) : make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < kFewAhead; ++i) load(i, u0[i], u1[i]);
+    for (int q = 0; q < chunks; q += kFewAhead) {
+#pragma unroll
+      for (int i = 0; i < kFewAhead; ++i) {
+        const uint4 x = u0[i], y = u1[i];
+        load(q + i + kFewAhead, u0[i], u1[i]);
+        if (q + i < chunks) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint4 v = *reinterpret_cast<const uint4*>(xl + b * 8 * a.pitch + (q + i) * 64);
+            mma_16x8x16(c[b], x.x, y.x, x.y, y.y, v.x, v.y);
+            mma_16x8x16(c[b], x.z, y.z, x.w, y.w, v.z, v.w);
+          }
+        }
+      }
+    }
+    // c[b][0], c[b][1]: row r0, tokens 8 b + 2 t, + 1;  c[b][2], c[b][3]: row r1
+#pragma unroll
+    for (int j = 0; j < 2 * NB; ++j) {
+      const float z0 = c[j >> 1][j & 1], z1 = c[j >> 1][2 + (j & 1)];
+      const int n = (j >> 1) * 8 + 2 * t + (j & 1);
+      if (tgt[j] >= 0 && tgt[j] == r0) a.zt[n] = z0;
+      if (tgt[j] >= 0 && tgt[j] == r1) a.zt[n] = z1;
+      if (r0 < a.V) join(m[j], s[j], z0 * kLog2e, 1.f);
+      if (r1 < a.V) join(m[j], s[j], z1 * kLog2e, 1.f);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2 * NB; ++j) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m[j], o), s2 = __shfl_xor_sync(0xffffffffu, s[j], o);
+      join(m[j], s[j], m2, s2);
+    }
+    if (g == 0) sm[w][(j >> 1) * 8 + 2 * t + (j & 1)] = make_float2(m[j], s[j]);
+  }
+  __syncthreads();
+  const int n = threadIdx.x;
+  if (n < a.T) {
+    float2 v = sm[0][n];
+#pragma unroll
+    for (int i = 1; i < kFewWarps; ++i) join(v.x, v.y, sm[i][n].x, sm[i][n].y);
+    a.part[(size_t)blockIdx.x * a.T + n] = v;
   }
 }
 
@@ -548,6 +725,7 @@ __global__ void __launch_bounds__(1024) xent_total_kernel(const float* loss, con
 __global__ void __launch_bounds__(256) xent_dx_kernel(const float* acc, int ks, int T, int H, int Hp,
                                                       const float* dloss, const float* total,
                                                       int reduction, __nv_bfloat16* dX) {
+  wait_for_previous();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = H / 8;
   if (i >= (int64_t)T * per) return;
@@ -578,15 +756,18 @@ int group_for(int64_t row_bytes) {
   return g < 1 ? 1 : (int)(g < 4096 ? g : 4096);
 }
 
+// `after`: another kernel of the same call comes before this one.
 template <bool BWD>
-cudaError_t launch(const XParams& P, cudaStream_t s) {
+cudaError_t launch(const XParams& P, bool after, cudaStream_t s) {
   auto kern = xent_gemm_kernel<BWD>;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
@@ -610,21 +791,60 @@ cudaError_t launch(const XParams& P, cudaStream_t s) {
   for (int p = 0; p < P.njob; ++p) tiles += (int64_t)P.job[p].mt * P.job[p].nt * P.job[p].ks;
   if (tiles < pairs) pairs = (int)tiles;
   cfg.gridDim = dim3(2 * pairs, 1, 1);
+  cfg.numAttrs = after ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
 struct FwdWs {
-  size_t part, zt, total;
-  int np;
+  size_t part, zt, sums, ticket, total;
 };
+// The size does not depend on the GPU (it is asked for without one): room for
+// the pieces of either kernel, at either tile width.
 FwdWs fwd_ws(const XentDesc& d) {
   FwdWs w;
-  w.np = 2 * up(d.V, kTile);
+  int64_t np = 2 * (int64_t)up(d.V, 192);
+  if (d.T <= kFewTokens && np < kFewMaxBlocks) np = kFewMaxBlocks;
   size_t o = 0;
-  w.part = o; o += align256((size_t)w.np * d.T * sizeof(float2));
+  w.part = o; o += align256((size_t)np * d.T * sizeof(float2));
   w.zt = o; o += align256((size_t)d.T * sizeof(float));
-  w.total = o ? o : 256;
+  w.sums = o; o += align256((size_t)up(d.T, 32) * sizeof(BlockSum));
+  w.ticket = o; o += 256;
+  w.total = o;
   return w;
+}
+
+// Bytes of a token's row in the shared memory of the kernel for few tokens:
+// whole 32-column chunks, and 64 bytes more than a multiple of 128, so that
+// the eight lanes of a quarter-warp read different banks.
+int few_pitch(int H) { return (H * 2 + 127) / 128 * 128 + 64; }
+bool few_tokens(const XentDesc& d) {
+  return d.T <= kFewTokens && (int64_t)(d.T <= 8 ? 8 : 16) * few_pitch(d.H) <= 110 * 1024;
+}
+
+template <int NB>
+cudaError_t run_few(const FewArgs& a, int* blocks, cudaStream_t s) {
+  static CtxCache<int> opt_in;
+  int ok = 0;
+  const cudaError_t e = opt_in.get(&ok, [](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(xent_few_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 110 * 1024);
+  });
+  if (e != cudaSuccess) return e;
+  const int tasks = (a.V + 15) / 16;
+  int n = kFewPerSm * sm_count();
+  if (n > kFewMaxBlocks) n = kFewMaxBlocks;
+  if (n > tasks) n = tasks;
+  *blocks = n;
+  xent_few_kernel<NB><<<n, 32 * kFewWarps, 8 * NB * a.pitch, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_few(const XentDesc& d, const void* X, const void* W, const void* targets, float2* part,
+                       float* zt, unsigned* ticket, int* np, cudaStream_t s) {
+  const FewArgs a{static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(W), targets, part,
+                  zt, ticket, d.ld_x, d.ld_w, d.T, d.H, d.V, d.index_type == MOE_INDEX_I64, d.ignore_index,
+                  few_pitch(d.H)};
+  return d.T <= 8 ? run_few<1>(a, np, s) : run_few<2>(a, np, s);
 }
 
 // The backward's pieces of the vocabulary: [T, piece] of dz in bf16 is held
@@ -667,15 +887,26 @@ XParams params_of(const XentDesc& d, const void* targets, int32_t* status) {
   return P;
 }
 
+// Width of the logit tiles: 256 columns, or 192 where that saves enough of the
+// last, partly filled round of tiles over the SM pairs to make up for moving
+// 8% more operand bytes per product (T = 1001, V = 10007: 3 rounds of either,
+// TNMEASURE).
+int tile_width(int T, int cols, int pairs) {
+  const int64_t mt = up(T, kTile);
+  const int64_t r256 = up(mt * up(cols, 256), pairs) * 256LL, r192 = up(mt * up(cols, 192), pairs) * 192LL;
+  return r192 * 108 < r256 * 100 ? 192 : 256;
+}
+
 bool logits_job(XJob& g, const XentDesc& d, const void* X, const void* W, int v0, int cols) {
+  g.tn = tile_width(d.T, cols, sm_count() / 2);
   g.mt = up(d.T, kTile);
-  g.nt = up(cols, kTile);
+  g.nt = up(cols, g.tn);
   g.ks = 1;
   g.kblocks = up(d.H, kBK);
   g.group = group_for(2 * (int64_t)d.H);
   g.b_n0 = v0;
   return make_tmap(&g.tmA, X, 2, d.T, d.H, kBK, 128, d.ld_x) &&
-         make_tmap(&g.tmB, W, 2, d.V, d.H, kBK, 128, d.ld_w);
+         make_tmap(&g.tmB, W, 2, d.V, d.H, kBK, g.tn / 2, d.ld_w);
 }
 
 }  // namespace
@@ -695,23 +926,30 @@ cudaError_t launch_xent_forward(const XentDesc& d, const void* X, const void* W,
   *st = MOE_OK;
   const FwdWs w = fwd_ws(d);
   const int i64 = d.index_type == MOE_INDEX_I64;
-  if (d.T > 0) {
+  if (d.T == 0) return cudaMemsetAsync(total, 0, 3 * sizeof(float), s);
+  float2* part = reinterpret_cast<float2*>(ws + w.part);
+  float* zt = reinterpret_cast<float*>(ws + w.zt);
+  unsigned* ticket = reinterpret_cast<unsigned*>(ws + w.ticket);
+  int np = 0;
+  if (few_tokens(d)) {
+    XENT_TRY(launch_few(d, X, W, targets, part, zt, ticket, &np, s));
+  } else {
     XParams P = params_of(d, targets, status);
-    P.part = reinterpret_cast<float2*>(ws + w.part);
-    P.zt = reinterpret_cast<float*>(ws + w.zt);
+    P.part = part;
+    P.zt = zt;
+    P.ticket = ticket;
     P.njob = 1;
     P.job[0].kind = XK_STATS;
     if (!logits_job(P.job[0], d, X, W, 0, d.V)) {
       *st = MOE_ERR_CUDA;
       return cudaSuccess;
     }
-    XENT_TRY(launch<false>(P, s));
-    xent_join_kernel<<<up(d.T, 32), 1024, 0, s>>>(P.part, w.np, P.zt, targets, i64, d.ignore_index, d.T,
-                                                 d.V, loss, lse, status);
-    XENT_TRY(cudaGetLastError());
+    np = 2 * P.job[0].nt;
+    XENT_TRY(launch<false>(P, false, s));
   }
-  xent_total_kernel<<<1, 1024, 0, s>>>(loss, targets, i64, d.ignore_index, d.T, d.V, total);
-  return cudaGetLastError();
+  return launch_after(xent_join_kernel, up(d.T, 32), 1024, 0, s, (const float2*)part, np, (const float*)zt,
+                      targets, i64, d.ignore_index, d.T, d.V, loss, lse,
+                      reinterpret_cast<BlockSum*>(ws + w.sums), ticket, total, status);
 }
 
 cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W, const void* targets,
@@ -733,11 +971,12 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
     P.total = total;
     P.reduction = reduction;
     P.lse = lse;
+    P.zcols = w.piece;
     P.njob = 1;
     P.job[0].kind = XK_DZ;
     bool ok = logits_job(P.job[0], d, X, W, v0, cols) &&
               make_tmap_out(&P.job[0].tmO, dz, d.T, w.piece, w.piece);
-    if (ok) XENT_TRY(launch<true>(P, s));
+    if (ok) XENT_TRY(launch<true>(P, v0 > 0, s));
     // dX (+)= dz W[piece], dW[piece] = dz^T X
     XParams Q = params_of(d, targets, status);
     Q.dloss = dloss;
@@ -751,6 +990,7 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
       XJob& g = Q.job[Q.njob++];
       g.kind = XK_DX;
       g.b_mn = 1;
+      g.tn = kTile;
       g.mt = up(d.T, kTile);
       g.nt = up(d.H, kTile);
       g.kblocks = up(cols, kBK);
@@ -758,12 +998,15 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
       g.group = 8;
       g.b_k0 = v0;
       ok = make_tmap(&g.tmA, dz, 2, d.T, w.piece, kBK, 128, w.piece) &&
-           make_tmap(&g.tmB, W, 2, d.V, d.H, 64, kBK, d.ld_w) && make_tmap_out(&g.tmO, dX, d.T, d.H);
+           make_tmap(&g.tmB, W, 2, d.V, d.H, 64, kBK, d.ld_w) &&
+           (Q.last ? make_tmap_out(&g.tmO, dX, d.T, d.H)
+                   : make_tmap_out_f32(&g.tmO, Q.acc, w.slices, d.T, w.Hp));
     }
     if (ok && dW) {
       XJob& g = Q.job[Q.njob++];
       g.kind = XK_DW;
       g.a_mn = g.b_mn = 1;
+      g.tn = kTile;
       g.mt = up(cols, kTile);
       g.nt = up(d.H, kTile);
       g.kblocks = up(d.T, kBK);
@@ -777,14 +1020,13 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
       *st = MOE_ERR_CUDA;
       return cudaSuccess;
     }
-    XENT_TRY(launch<true>(Q, s));
+    XENT_TRY(launch<true>(Q, true, s));
   }
   if (dX && w.slices > 1) {
     const int64_t n = (int64_t)d.T * (d.H / 8);
-    xent_dx_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(
-        reinterpret_cast<const float*>(ws + w.acc), w.slices, d.T, d.H, w.Hp, dloss, total, reduction,
-        static_cast<__nv_bfloat16*>(dX));
-    return cudaGetLastError();
+    return launch_after(xent_dx_kernel, (unsigned)((n + 255) / 256), 256, 0, s,
+                        reinterpret_cast<const float*>(ws + w.acc), w.slices, d.T, d.H, w.Hp, dloss, total,
+                        reduction, static_cast<__nv_bfloat16*>(dX));
   }
   return cudaSuccess;
 }

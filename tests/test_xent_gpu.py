@@ -93,7 +93,9 @@ def _check(X, W, t, out, s=None, backward=True):
 # one token, one entry; sizes around a tile (256) and a K block (64); odd
 # everything; enough tiles for several rounds; slices of the vocabulary
 SHAPES = [(1, 8, 1), (1, 64, 1000), (2, 72, 3), (7, 256, 32000), (128, 64, 256), (129, 128, 257), (255, 520, 511),
-          (256, 64, 255), (257, 192, 5003), (1001, 1032, 2007), (600, 2048, 1537), (33, 4096, 700), (3000, 264, 4111)]
+          (256, 64, 255), (257, 192, 5003), (1001, 1032, 2007), (600, 2048, 1537), (33, 4096, 700), (3000, 264, 4111),
+          # the kernel for few tokens: both its widths, vocabularies around its 16 rows, long and short K
+          (8, 1032, 15), (9, 40, 17), (16, 2056, 4999), (16, 8, 33), (5, 12000, 130), (16, 4096, 515)]
 
 
 @pytest.mark.parametrize("T,H,V", SHAPES)
