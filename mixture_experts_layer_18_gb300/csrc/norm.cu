@@ -15,11 +15,17 @@
 // all rows of a block.  All sums are fp32 trees in a fixed order; the results
 // do not depend on timing.
 //
-// Blocks are persistent.  Where every row starts on a 16-byte boundary, a
-// lane's vectors of the next rows travel to its own slots of shared memory
-// (asynchronous copies that only this lane reads, so no barrier orders them);
-// otherwise (odd widths or strides) lanes load single elements, the next
-// row's into registers.  L and the columns per lane are compile-time numbers:
+// Blocks are persistent.  A lane's vectors of the next rows travel to its own
+// slots of shared memory (asynchronous copies that only this lane reads, so no
+// barrier orders them).  Rows need not start on 16-byte boundaries (odd widths
+// or strides: SHIFT): lanes are then laid over the aligned vectors that
+// contain the row, whose first element sits m elements into its vector.  m
+// repeats with a period of at most 8 rows, and a group of lanes takes rows of
+// one m only (its stride over the rows is a multiple of the period), so its
+// columns stay the same.  The vectors at a row's ends hold elements of its
+// neighbours too: those are masked after the copy, and the stores there go by
+// elements (4097 x 2049 bf16, forward and backward: all moves by elements 14.3
+// and 22.7 us, SHIFTMEASURE).  L and the columns per lane are compile-time numbers:
 // a row's offsets are then part of the instructions, which with the arithmetic
 // in pairs (fp32x2) keeps a row's instructions below the time that HBM takes
 // for it (they were the bound of a first version with both at run time).
@@ -114,11 +120,14 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int group, float* sm) {
     x = lanes_sum<W>(x);
     if ((lane & (W - 1)) == 0) sm[(threadIdx.x >> 5) * N + lane / W] = x;
     group_bar<L>(group);
-    const int k = lane / W, w = lane & (W - 1);
+    // each half (N == 2) or the whole warp adds the warps' sums up, as often
+    // as they fit into its lanes
+    constexpr int P = WARPS > 16 ? 32 : WARPS > 8 ? 16 : WARPS > 4 ? 8 : WARPS > 2 ? 4 : 2;
+    const int k = lane / W, w = lane & ((P < W ? P : W) - 1);
     const float* g = sm + group * WARPS * N;
     x = w < WARPS ? g[w * N + k] : 0.f;
     if constexpr (WARPS > W) x += g[(w + W) * N + k];
-    x = lanes_sum<W>(x);
+    x = lanes_sum<(P < W ? P : W)>(x);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = N == 1 ? x : __shfl_sync(0xffffffffu, x, i * W);
   }
@@ -141,54 +150,76 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A lane's CPT columns of every row, V to a load: element i of load j is
-// column (j L + t) V + i.  V is the row's vector (16 bytes) or one element.
-template <typename X, int V, int CPT, int L>
+// Elements of a 16-byte vector.
+template <typename X>
+constexpr int kVec = 16 / (int)sizeof(X);
+
+// A lane's CPT columns of every row of its group: element i of its vector j is
+// column first() + j L V + i.  A vector lies wholly (full) or, at a row's ends
+// with SHIFT, partly inside the row, or past it.
+template <typename X, int CPT, int L, bool SHIFT>
 struct Lane {
-  int t, left;                           // `left`: columns from this lane's first to the row's end
-  __device__ __forceinline__ Lane(int H) : t(threadIdx.x & (L - 1)), left(H - t * V) {}
+  static constexpr int V = kVec<X>;
+  int t, c0, left;                       // c0: first column; left: columns from there to the row's end
+  bool ends;                             // a lane of this warp holds an end of the row (SHIFT)
+  __device__ __forceinline__ Lane(int H, int m)
+      : t(threadIdx.x % L), c0(t * V - (SHIFT ? m : 0)), left(H - c0), ends(false) {
+    if constexpr (SHIFT) {
+#pragma unroll
+      for (int j = 0; j < CPT / V; ++j) ends = ends || (valid(j) && !full(j));
+      ends = __any_sync(0xffffffffu, ends);
+    }
+  }
+  __device__ __forceinline__ int first() const { return c0; }
   __device__ __forceinline__ bool valid(int j) const { return left > j * L * V; }
-  __device__ __forceinline__ int first() const { return t * V; }
+  __device__ __forceinline__ bool full(int j) const {
+    return SHIFT ? c0 + j * L * V >= 0 && left >= (j * L + 1) * V : valid(j);
+  }
+  // element i of vector j is in the row (asked of partly filled vectors)
+  __device__ __forceinline__ bool inside(int j, int i) const {
+    return c0 + j * L * V + i >= 0 && left > j * L * V + i;
+  }
 };
 
-// Load j of a lane, as pairs, to its place in a row; a whole part of a row.
-template <typename X, int V, int CPT, int L>
-__device__ __forceinline__ void store_vec(const Lane<X, V, CPT, L>& l, X* row, int j, const F2* p) {
-  static_assert(V > 1, "vectors");
-  float e[V];
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i) split(p[i], e[2 * i], e[2 * i + 1]);
-  X* q = row + l.first() + j * L * V;
-  if (!l.valid(j)) return;
-  if constexpr (sizeof(X) == 2)
-    *reinterpret_cast<uint4*>(q) = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
-                                              pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
-  else
-    *reinterpret_cast<float4*>(q) = make_float4(e[0], e[1], e[2], e[3]);
+// A row's first element's place in its 16-byte vector.
+template <typename X>
+__device__ __forceinline__ int shift_of(const X* p) {
+  return (int)((uintptr_t)p & 15) / (int)sizeof(X);
 }
-template <typename X, int V, int CPT, int L>
-__device__ __forceinline__ void store_row(const Lane<X, V, CPT, L>& l, X* row, const F2 (&p)[CPT / 2]) {
-  if constexpr (V > 1) {
+
+template <typename X, int CPT, int L, bool SHIFT>
+__device__ __forceinline__ void store_row(const Lane<X, CPT, L, SHIFT>& l, X* row, const F2 (&p)[CPT / 2]) {
+  constexpr int V = kVec<X>;
+  row += l.first();
 #pragma unroll
-    for (int j = 0; j < CPT / V; ++j) store_vec(l, row, j, p + j * V / 2);
-  } else {
+  for (int j = 0; j < CPT / V; ++j) {
+    float e[V];
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      float e[2];
-      split(p[j / 2], e[0], e[1]);
-      if (l.valid(j)) put(row + l.first() + j * L, e[j & 1]);
+    for (int i = 0; i < V / 2; ++i) split(p[j * V / 2 + i], e[2 * i], e[2 * i + 1]);
+    X* q = row + j * L * V;
+    if (SHIFT && l.ends ? l.full(j) : l.valid(j)) {
+      if constexpr (sizeof(X) == 2)
+        *reinterpret_cast<uint4*>(q) = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
+                                                  pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
+      else
+        *reinterpret_cast<float4*>(q) = make_float4(e[0], e[1], e[2], e[3]);
+    } else if (SHIFT && l.ends && l.valid(j)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (l.inside(j, i)) put(q + i, e[i]);
     }
   }
 }
 
 // A lane's weights, read once per block (0 past the row's end): in registers
 // up to 16 columns, else in shared memory (each lane's own, 16 bytes apart).
-template <typename X, int V, int CPT, int L, int THREADS>
+template <typename X, int CPT, int L, bool SHIFT, int THREADS>
 struct Weights {
+  static constexpr int V = kVec<X>;
   static constexpr bool REGS = CPT <= 16;
   F2 r[REGS ? CPT / 2 : 1];
   float4* s;
-  __device__ __forceinline__ void load(const Lane<X, V, CPT, L>& l, const void* p, int type, float fill,
+  __device__ __forceinline__ void load(const Lane<X, CPT, L, SHIFT>& l, const void* p, int type, float fill,
                                        float4* smem) {
     s = smem + threadIdx.x;
     F2 v[CPT / 2];
@@ -197,12 +228,12 @@ struct Weights {
       float e[V] = {};
       const int c = l.first() + j * L * V;
       if (l.valid(j)) {
-        if (V == 8 && p && type == MOE_TYPE_BF16 && ((uintptr_t)p & 15) == 0) {
+        if (!SHIFT && V == 8 && p && type == MOE_TYPE_BF16 && ((uintptr_t)p & 15) == 0) {
           const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c);
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int i = 0; i < V; ++i) e[i] = i & 1 ? bf16_hi(w[(i / 2) & 3]) : bf16_lo(w[(i / 2) & 3]);
-        } else if (V >= 4 && p && type == MOE_TYPE_F32 && ((uintptr_t)p & 15) == 0) {
+        } else if (!SHIFT && p && type == MOE_TYPE_F32 && ((uintptr_t)p & 15) == 0) {
 #pragma unroll
           for (int i = 0; i + 3 < V; i += 4) {
             const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + i);
@@ -210,19 +241,12 @@ struct Weights {
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < V; ++i) e[i] = load_w1(p, type, c + i, fill);
+          for (int i = 0; i < V; ++i)
+            if (!SHIFT || l.inside(j, i)) e[i] = load_w1(p, type, c + i, fill);
         }
       }
-      if constexpr (V > 1) {
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) v[j * V / 2 + i] = f2(e[2 * i], e[2 * i + 1]);
-      } else if (j & 1) {
-        float a, b;
-        split(v[j / 2], a, b);
-        v[j / 2] = f2(a, e[0]);
-      } else {
-        v[j / 2] = f2(e[0], 0.f);
-      }
+      for (int i = 0; i < V / 2; ++i) v[j * V / 2 + i] = f2(e[2 * i], e[2 * i + 1]);
     }
     if constexpr (REGS) {
 #pragma unroll
@@ -252,66 +276,77 @@ struct Weights {
   }
 };
 
-// The rows of one tensor on their way to a lane.  Vectors: a ring of S rows
-// in shared memory, `at` the lane's first slot.  Elements: the next row in
-// registers.  Slots (registers) past the row's end are zero from the start
-// and never written.
-template <typename X, int V, int CPT, int L, int S, int THREADS>
+// The rows of one tensor on their way to a lane: a ring of S rows in shared
+// memory, `at` the lane's first slot.  What lies past the row's ends reads as
+// zero.
+template <typename X, int CPT, int L, bool SHIFT, int S, int THREADS>
 struct Stream {
-  static constexpr int NL = CPT / V;
-  static constexpr int RING = V == 1 ? 0 : S * NL * THREADS * 16;    // bytes per block
+  static constexpr int V = kVec<X>, NL = CPT / V;
+  static constexpr int RING = S * NL * THREADS * 16;    // bytes per block
+  using Lane_ = Lane<X, CPT, L, SHIFT>;
   const X* p;
   int64_t ld;
   uint8_t* at;
-  X next[V == 1 ? CPT : 1];
-  __device__ __forceinline__ Stream(const Lane<X, V, CPT, L>& l, const void* base, int64_t ld_, uint8_t* ring)
+  __device__ __forceinline__ Stream(const Lane_& l, const void* base, int64_t ld_, uint8_t* ring)
       : p(static_cast<const X*>(base) + l.first()), ld(ld_), at(ring + threadIdx.x * 16) {
-    if constexpr (V == 1) {
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) put(&next[i], 0.f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NL; ++j)
-        if (!l.valid(j))
-          for (int st = 0; st < S; ++st)
-            *reinterpret_cast<uint4*>(at + (st * NL + j) * THREADS * 16) = make_uint4(0, 0, 0, 0);
-    }
+    for (int j = 0; j < NL; ++j)
+      if (!l.valid(j))
+        for (int st = 0; st < S; ++st)
+          *reinterpret_cast<uint4*>(at + (st * NL + j) * THREADS * 16) = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void fetch(const Lane<X, V, CPT, L>& l, int64_t row, int T, int st) {
+  __device__ __forceinline__ void fetch(const Lane_& l, int64_t row, int T, int st) {
     if (row >= T) return;
     const X* q = p + row * ld;
-    if constexpr (V == 1) {
-#pragma unroll
-      for (int i = 0; i < CPT; ++i)
-        if (l.valid(i)) next[i] = q[i * L];
-    } else {
-      const uint32_t d = smem_u32(at) + st * (NL * THREADS * 16);
+    uint8_t* d = at + st * (NL * THREADS * 16);
+    if (!SHIFT || !l.ends) {
 #pragma unroll
       for (int j = 0; j < NL; ++j)
-        if (l.valid(j)) copy_async16(d + j * THREADS * 16, q + j * L * V);
+        if (l.valid(j)) copy_async16(smem_u32(d + j * THREADS * 16), q + j * L * V);
+      return;
     }
-  }
-  __device__ __forceinline__ void take(F2 (&x)[CPT / 2], int st) const {
-    if constexpr (V == 1) {
+    // elements from the tensor's first to this lane's, and to the tensor's end
+    const int64_t before = row * ld + l.first();
+    const int64_t after = (int64_t)(T - 1 - row) * ld + l.left;
 #pragma unroll
-      for (int i = 0; i < CPT / 2; ++i) x[i] = f2(to_f(next[2 * i]), to_f(next[2 * i + 1]));
-    } else {
+    for (int j = 0; j < NL; ++j) {
+      if (!l.valid(j)) continue;
+      if (before + j * L * V >= 0 && after >= (j * L + 1) * V) {
+        copy_async16(smem_u32(d + j * THREADS * 16), q + j * L * V);
+      } else {                                   // the vector sticks out of the tensor itself
 #pragma unroll
-      for (int j = 0; j < NL; ++j) {
-        const uint4 u = *reinterpret_cast<const uint4*>(at + (st * NL + j) * THREADS * 16);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i)
-          x[j * V / 2 + i] = sizeof(X) == 2
-                                 ? f2(bf16_lo(w[i]), bf16_hi(w[i]))
-                                 : f2(__uint_as_float(w[(2 * i) & 3]), __uint_as_float(w[(2 * i + 1) & 3]));
+        for (int i = 0; i < V; ++i)
+          if (l.inside(j, i)) reinterpret_cast<X*>(d + j * THREADS * 16)[i] = q[j * L * V + i];
       }
     }
+  }
+  __device__ __forceinline__ void take(const Lane_& l, F2 (&x)[CPT / 2], int st) const {
+    uint32_t w[NL][4];
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4*>(at + (st * NL + j) * THREADS * 16);
+      w[j][0] = u.x; w[j][1] = u.y; w[j][2] = u.z; w[j][3] = u.w;
+    }
+    if (SHIFT && l.ends) {                       // elements of the rows before and after this one
+#pragma unroll
+      for (int j = 0; j < NL; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (!l.inside(j, i))
+            w[j][i * (int)sizeof(X) / 4] &= sizeof(X) == 4 ? 0u : i & 1 ? 0x0000ffffu : 0xffff0000u;
+    }
+#pragma unroll
+    for (int j = 0; j < NL; ++j)
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        x[j * V / 2 + i] = sizeof(X) == 2
+                               ? f2(bf16_lo(w[j][i]), bf16_hi(w[j][i]))
+                               : f2(__uint_as_float(w[j][(2 * i) & 3]), __uint_as_float(w[j][(2 * i + 1) & 3]));
   }
 };
 
 template <int L>
-constexpr int kRows = L >= 256 ? 1 : 256 / L;     // rows of a block
+constexpr int kRows = L > 128 ? 1 : 256 / L;      // rows of a block
 template <int L>
 constexpr int kBlock = kRows<L>* L;
 
@@ -328,24 +363,25 @@ struct FwdArgs {
   float eps;
 };
 
-template <typename X, int V, int CPT, int L, int S>
-__global__ void __launch_bounds__(kBlock<L>, kBlock<L> == 256 && CPT <= 16 ? 3 : 1)
+template <typename X, bool SHIFT, int CPT, int L, int S>
+__global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 800 / kBlock<L> : 1)
     norm_fwd_kernel(const __grid_constant__ FwdArgs a) {
-  constexpr int TH = kBlock<L>, ROWS = kRows<L>;
-  using Str = Stream<X, V, CPT, L, S, TH>;
+  constexpr int TH = kBlock<L>, ROWS = kRows<L>, V = kVec<X>;
+  using Str = Stream<X, CPT, L, SHIFT, S, TH>;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ float sm[2][TH / 32];
   const int group = threadIdx.x / L;
-  const Lane<X, V, CPT, L> lane(a.H);
   const int64_t stride = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + group;
+  const Lane<X, CPT, L, SHIFT> lane(
+      a.H, SHIFT ? shift_of(static_cast<const X*>(a.x) + (row < a.T ? row : 0) * a.ld_x) : 0);
   Str xs(lane, a.x, a.ld_x, dyn);
 #pragma unroll
-  for (int st = 0; st < (V == 1 ? 1 : S - 1); ++st) {
+  for (int st = 0; st < S - 1; ++st) {
     xs.fetch(lane, row + st * stride, a.T, st);
     copy_commit();
   }
-  Weights<X, V, CPT, L, TH> gam, bet;
+  Weights<X, CPT, L, SHIFT, TH> gam, bet;
   float4* wsm = reinterpret_cast<float4*>(dyn + Str::RING);
   gam.load(lane, a.gamma, a.wtype, 1.f, wsm);
   bet.load(lane, a.beta, a.wtype, 0.f, wsm + CPT / 4 * TH);
@@ -353,13 +389,10 @@ __global__ void __launch_bounds__(kBlock<L>, kBlock<L> == 256 && CPT <= 16 ? 3 :
   int st = 0;
   for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.T; base += stride, row += stride) {
     F2 x[CPT / 2];
-    if constexpr (V > 1) {
-      xs.fetch(lane, row + (S - 1) * stride, a.T, st == 0 ? S - 1 : st - 1);
-      copy_commit();
-      copy_wait<S - 1>();
-    }
-    xs.take(x, st);
-    if constexpr (V == 1) xs.fetch(lane, row + stride, a.T, 0);
+    xs.fetch(lane, row + (S - 1) * stride, a.T, st == 0 ? S - 1 : st - 1);
+    copy_commit();
+    copy_wait<S - 1>();
+    xs.take(lane, x, st);
     if (++st == S) st = 0;
     F2 acc = f2(0.f, 0.f), acc2 = acc;
 #pragma unroll
@@ -373,13 +406,12 @@ __global__ void __launch_bounds__(kBlock<L>, kBlock<L> == 256 && CPT <= 16 ? 3 :
     const F2 neg = f2(-mu, -mu);
 #pragma unroll
     for (int i = 0; i < CPT / 2; ++i) x[i] = add2(x[i], neg);
-    if constexpr (V == 1) {
+    if (SHIFT && lane.ends) {            // the row's ends, by elements
 #pragma unroll
-      for (int i = 0; i < CPT / 2; ++i) {
-        float d, e;
-        split(x[i], d, e);
-        q[0] += lane.valid(2 * i) ? d * d : 0.f;
-        q[0] += lane.valid(2 * i + 1) ? e * e : 0.f;
+      for (int i = 0; i < CPT; ++i) {
+        float d[2];
+        split(x[i / 2], d[0], d[1]);
+        q[0] += lane.inside(i / V, i % V) ? d[i & 1] * d[i & 1] : 0.f;
       }
     } else {
 #pragma unroll
@@ -409,7 +441,8 @@ __global__ void __launch_bounds__(kBlock<L>, kBlock<L> == 256 && CPT <= 16 ? 3 :
   copy_wait<0>();
 }
 
-// Rows too long for the kernel above: a block per row, three passes over it
+// Rows that the kernel above does not take (too long, or x and y at different
+// offsets from 16-byte boundaries): a block per row, three passes over it
 // (the second and third find most of it in L1 or L2).
 template <typename X>
 __global__ void __launch_bounds__(1024) norm_fwd_rows_kernel(const FwdArgs a) {
@@ -452,28 +485,29 @@ struct BwdArgs {
 //   dx = r g + x A + B,  A = -r r mean(g h),  B = -r mean(g) - b r mean(g h).
 // (Three blocks per SM instead of two, with gamma in shared memory and the row
 // read from the ring a second time, measured no faster: 79 against 76 us.)
-template <typename X, int V, int CPT, int L, int S>
-__global__ void __launch_bounds__(kBlock<L>, kBlock<L> == 256 && CPT <= 16 ? 2 : 1)
+template <typename X, bool SHIFT, int CPT, int L, int S>
+__global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
     norm_bwd_kernel(const __grid_constant__ BwdArgs a) {
-  constexpr int TH = kBlock<L>, ROWS = kRows<L>;
-  using Str = Stream<X, V, CPT, L, S, TH>;
+  constexpr int TH = kBlock<L>, ROWS = kRows<L>, V = kVec<X>;
+  using Str = Stream<X, CPT, L, SHIFT, S, TH>;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ float sm[2][TH / 16];
   let_next_start();
   const int group = threadIdx.x / L;
-  const Lane<X, V, CPT, L> lane(a.H);
   const int64_t stride = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + group;
+  const Lane<X, CPT, L, SHIFT> lane(
+      a.H, SHIFT ? shift_of(static_cast<const X*>(a.x) + (row < a.T ? row : 0) * a.ld_x) : 0);
   Str xs(lane, a.x, a.ld_x, dyn), ds(lane, a.dy, a.ld_dy, dyn + Str::RING);
 #pragma unroll
-  for (int st = 0; st < (V == 1 ? 1 : S - 1); ++st) {
+  for (int st = 0; st < S - 1; ++st) {
     xs.fetch(lane, row + st * stride, a.T, st);
     ds.fetch(lane, row + st * stride, a.T, st);
     copy_commit();
   }
   auto at = [&](int64_t q) { return q < a.T ? q : a.T - 1; };
   float mu = a.mean[at(row)], r = a.rstd[at(row)];
-  Weights<X, V, CPT, L, TH> gam;
+  Weights<X, CPT, L, SHIFT, TH> gam;
   gam.load(lane, a.gamma, a.wtype, 1.f, reinterpret_cast<float4*>(dyn + 2 * Str::RING));
   F2 dg[CPT / 2], db[CPT / 2];
 #pragma unroll
@@ -485,24 +519,18 @@ __global__ void __launch_bounds__(kBlock<L>, kBlock<L> == 256 && CPT <= 16 ? 2 :
     const bool live = row < a.T;
     mu = a.mean[at(row + stride)];
     r = a.rstd[at(row + stride)];
-    if constexpr (V > 1) {
-      const int to = st == 0 ? S - 1 : st - 1;
-      xs.fetch(lane, row + (S - 1) * stride, a.T, to);
-      ds.fetch(lane, row + (S - 1) * stride, a.T, to);
-      copy_commit();
-      copy_wait<S - 1>();
-    }
+    const int to = st == 0 ? S - 1 : st - 1;
+    xs.fetch(lane, row + (S - 1) * stride, a.T, to);
+    ds.fetch(lane, row + (S - 1) * stride, a.T, to);
+    copy_commit();
+    copy_wait<S - 1>();
     const F2 rr = f2(rc, rc), bb = f2(bc, bc);
     F2 s1 = f2(0.f, 0.f), s2 = s1;
     F2 x[CPT / 2], d[CPT / 2], g[CPT / 2];
-    xs.take(x, st);
-    ds.take(d, st);
+    xs.take(lane, x, st);
+    ds.take(lane, d, st);
     if (++st == S) st = 0;
     gam.get(g);
-    if constexpr (V == 1) {
-      xs.fetch(lane, row + stride, a.T, 0);
-      ds.fetch(lane, row + stride, a.T, 0);
-    }
 #pragma unroll
     for (int i = 0; i < CPT / 2; ++i) {
       const F2 h = fma2(x[i], rr, bb);
@@ -527,10 +555,11 @@ __global__ void __launch_bounds__(kBlock<L>, kBlock<L> == 256 && CPT <= 16 ? 2 :
   }
   copy_wait<0>();
   if (!a.partial) return;
-  // the block's column sums: groups of one block are added in order
+  // the block's column sums, through shared memory: groups of one block are
+  // added in order, and the stores are coalesced
   float* out = a.partial + (size_t)blockIdx.x * 2 * a.H;
   float* acc = reinterpret_cast<float*>(dyn) + (size_t)group * 2 * a.H;   // [ROWS][2][H]
-  if (ROWS > 1) __syncthreads();         // the ring is no longer read
+  __syncthreads();                       // the ring is no longer read
 #pragma unroll
   for (int i = 0; i < CPT / 2; ++i) {
     float gs[2], bs[2];
@@ -538,25 +567,19 @@ __global__ void __launch_bounds__(kBlock<L>, kBlock<L> == 256 && CPT <= 16 ? 2 :
     split(db[i], bs[0], bs[1]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int j = (2 * i + k) / V, c = lane.first() + j * L * V + (2 * i + k) % V;
-      if (!lane.valid(j)) continue;
-      if constexpr (ROWS == 1) {
-        out[c] = gs[k];
-        out[a.H + c] = bs[k];
-      } else {
-        acc[c] = gs[k];
-        acc[a.H + c] = bs[k];
-      }
+      const int j = (2 * i + k) / V, e = (2 * i + k) % V, c = lane.first() + j * L * V + e;
+      if (!(SHIFT ? lane.inside(j, e) : lane.valid(j))) continue;
+      acc[c] = gs[k];
+      acc[a.H + c] = bs[k];
     }
   }
-  if constexpr (ROWS > 1) {
-    __syncthreads();
-    const float* all = reinterpret_cast<const float*>(dyn);
-    for (int c = threadIdx.x; c < 2 * a.H; c += TH) {
-      float v = 0.f;
-      for (int g = 0; g < ROWS; ++g) v += all[(size_t)2 * g * a.H + c];
-      out[c] = v;
-    }
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(dyn);
+  for (int c = threadIdx.x; c < 2 * a.H; c += TH) {
+    float v = all[c];
+#pragma unroll
+    for (int g = 1; g < ROWS; ++g) v += all[(size_t)2 * g * a.H + c];
+    out[c] = v;
   }
 }
 
@@ -570,6 +593,7 @@ __global__ void __launch_bounds__(1024) norm_param_grad_kernel(const float* part
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
   if (c < H)
+#pragma unroll 8
     for (int b = w; b < blocks; b += 32) v += partial[((size_t)b * 2 + blockIdx.y) * H + c];
   sm[w][lane] = v;
   __syncthreads();
@@ -582,8 +606,8 @@ __global__ void __launch_bounds__(1024) norm_param_grad_kernel(const float* part
   }
 }
 
-// Rows too long for the kernel above: dx with a block per row (two passes),
-// the column sums from a second read with a thread per column.
+// Rows that the kernel above does not take: dx with a block per row (two
+// passes), the column sums from a second read with a thread per column.
 template <typename X>
 __global__ void __launch_bounds__(1024) norm_bwd_rows_kernel(const BwdArgs a) {
   __shared__ float sm[64];
@@ -624,81 +648,8 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const BwdArgs a) {
 }
 
 // ------------------------------------------------------------------ host
-// Launches one form: blocks that fill the GPU once, but no more than there
-// are rows.
-template <typename Args, typename K>
-cudaError_t run(K kern, CtxCache<int>& cache, const Args& a, int rows, int threads, int smem,
-                int64_t max_blocks, int* blocks_out, cudaStream_t s) {
-  int per_sm = 0;
-  const cudaError_t e = cache.get(&per_sm, [&](int* v) {
-    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, threads, smem);
-    return r == cudaSuccess && *v < 1 ? cudaErrorInvalidConfiguration : r;
-  });
-  if (e != cudaSuccess) return e;
-  int64_t blocks = (int64_t)sm_count() * per_sm;
-  const int64_t need = ((int64_t)a.T + rows - 1) / rows;
-  if (blocks > need) blocks = need;
-  if (blocks > max_blocks) blocks = max_blocks;
-  kern<<<(unsigned)blocks, threads, smem, s>>>(a);
-  *blocks_out = (int)blocks;
-  return cudaGetLastError();
-}
-
-template <typename X, int V, int CPT, int L, int S>
-cudaError_t run_fwd(const FwdArgs& a, cudaStream_t s) {
-  static CtxCache<int> cache;
-  constexpr int TH = kBlock<L>;
-  constexpr int kBytes = Stream<X, V, CPT, L, S, TH>::RING + (CPT > 16 ? 2 * CPT * 4 * TH : 0);
-  int blocks;
-  return run(norm_fwd_kernel<X, V, CPT, L, S>, cache, a, kRows<L>, TH, kBytes, INT64_MAX, &blocks, s);
-}
-
-template <typename X, int V, int CPT, int L, int S>
-cudaError_t run_bwd(const BwdArgs& a, int64_t max_blocks, int* blocks, cudaStream_t s) {
-  static CtxCache<int> cache;
-  constexpr int TH = kBlock<L>;
-  constexpr int kRing = 2 * Stream<X, V, CPT, L, S, TH>::RING + (CPT > 16 ? CPT * 4 * TH : 0);
-  constexpr int kSums = kRows<L> > 1 ? kRows<L> * 2 * L * CPT * 4 : 0;    // H <= L CPT
-  return run(norm_bwd_kernel<X, V, CPT, L, S>, cache, a, kRows<L>, TH, kRing > kSums ? kRing : kSums,
-             max_blocks, blocks, s);
-}
-
-// The fewest lanes that hold a row at 16 columns each (8 in rows up to 128 and
-// where lanes load single elements, whose next row sits in registers), 512
-// lanes of 32 columns (vectors only) for rows over 8192.
-template <typename X, int V>
-cudaError_t forward(const FwdArgs& a, cudaStream_t s) {
-  constexpr bool B = sizeof(X) == 2;
-  constexpr int C = V == 1 ? 8 : 16;
-  if (a.H <= 128) return run_fwd<X, V, 8, 16, 4>(a, s);
-  if (a.H <= 32 * C) return run_fwd<X, V, C, 32, 4>(a, s);
-  if (a.H <= 64 * C) return run_fwd<X, V, C, 64, 4>(a, s);
-  if (a.H <= 128 * C) return run_fwd<X, V, C, 128, 4>(a, s);
-  if (a.H <= 256 * C) return run_fwd<X, V, C, 256, 4>(a, s);
-  if (a.H <= 4096) return run_fwd<X, V, 16, 256, 4>(a, s);
-  if (a.H <= 8192) return run_fwd<X, V, 16, 512, 3>(a, s);
-  if constexpr (V > 1)
-    if (a.H <= 16384) return run_fwd<X, V, 32, 512, B ? 2 : 1>(a, s);
-  norm_fwd_rows_kernel<X><<<(unsigned)a.T, 1024, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-// As the forward; fp32 rows over 8192 would not fit the ring with two tensors.
-template <typename X, int V>
-cudaError_t backward(const BwdArgs& a, int64_t max_blocks, int* blocks, cudaStream_t s) {
-  constexpr bool B = sizeof(X) == 2;
-  constexpr int S = B ? 4 : 3;
-  constexpr int C = V == 1 ? 8 : 16;
-  if (a.H <= 128) return run_bwd<X, V, 8, 16, S>(a, max_blocks, blocks, s);
-  if (a.H <= 32 * C) return run_bwd<X, V, C, 32, S>(a, max_blocks, blocks, s);
-  if (a.H <= 64 * C) return run_bwd<X, V, C, 64, S>(a, max_blocks, blocks, s);
-  if (a.H <= 128 * C) return run_bwd<X, V, C, 128, S>(a, max_blocks, blocks, s);
-  if (a.H <= 256 * C) return run_bwd<X, V, C, 256, S>(a, max_blocks, blocks, s);
-  if (a.H <= 512 * C && C == 8) return run_bwd<X, V, C, 512, S>(a, max_blocks, blocks, s);
-  if (a.H <= 8192) return run_bwd<X, V, 16, 512, 3>(a, max_blocks, blocks, s);
-  if constexpr (B && (V > 1))
-    if (a.H <= 16384) return run_bwd<X, V, 32, 512, 2>(a, max_blocks, blocks, s);
+template <typename X>
+cudaError_t backward_rows(const BwdArgs& a, int64_t max_blocks, int* blocks, cudaStream_t s) {
   if (a.partial) {
     int64_t slabs = 64;
     if (slabs > a.T) slabs = a.T;
@@ -712,19 +663,140 @@ cudaError_t backward(const BwdArgs& a, int64_t max_blocks, int* blocks, cudaStre
   return cudaGetLastError();
 }
 
-bool rows16(const void* p, int64_t ld, int T, int es) {
-  return ((uintptr_t)p & 15) == 0 && (T <= 1 || (ld * es) % 16 == 0);
+// Where the rows of a call's tensors start relative to 16-byte boundaries.
+struct Offsets {
+  bool vectors;   // all on boundaries, and rows are whole vectors
+  bool same;      // at the same offset in every tensor, row by row
+  int period;     // rows after which the offset repeats (1 .. 8)
+};
+Offsets offsets_of(const void* const* p, const int64_t* ld, int n, int es, int T, int H) {
+  Offsets o{(int64_t)H * es % 16 == 0, true, 1};
+  for (int i = 0; i < n; ++i) {
+    o.vectors = o.vectors && ((uintptr_t)p[i] & 15) == 0 && (T <= 1 || ld[i] * es % 16 == 0);
+    o.same = o.same && (((uintptr_t)p[i] ^ (uintptr_t)p[0]) & 15) == 0 &&
+             (T <= 1 || (ld[i] - ld[0]) * es % 16 == 0);
+  }
+  if (T > 1)
+    while (ld[0] * es * o.period % 16) o.period *= 2;
+  return o;
+}
+
+// Launches one form: blocks that fill the GPU once, but no more than there
+// are rows; where a group takes several rows, their distance is a multiple of
+// `period`.
+template <typename Args, typename K>
+cudaError_t run(K kern, CtxCache<int>& cache, const Args& a, int rows, int threads, int smem, int period,
+                int64_t max_blocks, int* blocks_out, cudaStream_t s) {
+  int per_sm = 0;
+  const cudaError_t e = cache.get(&per_sm, [&](int* v) {
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r == cudaSuccess) r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, threads, smem);
+    return r == cudaSuccess && *v < 1 ? cudaErrorInvalidConfiguration : r;
+  });
+  if (e != cudaSuccess) return e;
+  int64_t blocks = (int64_t)sm_count() * per_sm;
+  const int64_t need = ((int64_t)a.T + rows - 1) / rows;
+  if (blocks > max_blocks) blocks = max_blocks;
+  if (blocks >= need) {
+    blocks = need;                       // a row per group
+  } else {
+    int unit = 1;                        // blocks in which whole periods of rows fit
+    while (unit * rows % period) ++unit;
+    blocks = blocks > unit ? blocks / unit * unit : unit;
+  }
+  kern<<<(unsigned)blocks, threads, smem, s>>>(a);
+  *blocks_out = (int)blocks;
+  return cudaGetLastError();
+}
+
+template <typename X, bool SHIFT, int CPT, int L, int S>
+cudaError_t run_fwd(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
+  static CtxCache<int> cache;
+  constexpr int TH = kBlock<L>;
+  constexpr int kBytes = Stream<X, CPT, L, SHIFT, S, TH>::RING + (CPT > 16 ? 2 * CPT * 4 * TH : 0);
+  int blocks;
+  return run(norm_fwd_kernel<X, SHIFT, CPT, L, S>, cache, a, kRows<L>, TH, kBytes, SHIFT ? o.period : 1,
+             INT64_MAX, &blocks, s);
+}
+
+template <typename X, bool SHIFT, int CPT, int L, int S>
+cudaError_t run_bwd(const BwdArgs& a, const Offsets& o, int64_t max_blocks, int* blocks, cudaStream_t s) {
+  static CtxCache<int> cache;
+  constexpr int TH = kBlock<L>;
+  constexpr int kRing = 2 * Stream<X, CPT, L, SHIFT, S, TH>::RING + (CPT > 16 ? CPT * 4 * TH : 0);
+  constexpr int kSums = kRows<L> * 2 * L * CPT * 4;    // H <= L CPT
+  return run(norm_bwd_kernel<X, SHIFT, CPT, L, S>, cache, a, kRows<L>, TH, kRing > kSums ? kRing : kSums,
+             SHIFT ? o.period : 1, max_blocks, blocks, s);
+}
+
+// The fewest lanes that hold a row (with SHIFT, one from any place in its
+// first vector) at 16 columns each, 8 in short rows; 512 lanes of 32 columns
+// for aligned rows over 8192.
+template <typename X, bool SHIFT>
+cudaError_t forward(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
+  const int n = SHIFT ? a.H + kVec<X> - 1 : a.H;
+  if (n <= 128) return run_fwd<X, SHIFT, 8, 16, 4>(a, o, s);
+  if (n <= 512) return run_fwd<X, SHIFT, 16, 32, 4>(a, o, s);
+  if (n <= 1024) return run_fwd<X, SHIFT, 16, 64, 4>(a, o, s);
+  if (n <= 1536) return run_fwd<X, SHIFT, 16, 96, 4>(a, o, s);
+  if (n <= 2048) return run_fwd<X, SHIFT, 16, 128, 4>(a, o, s);
+  if (n <= 2560) return run_fwd<X, SHIFT, 16, 160, 4>(a, o, s);
+  if (n <= 3584) return run_fwd<X, SHIFT, 16, 224, 4>(a, o, s);
+  if (n <= 4096) return run_fwd<X, SHIFT, 16, 256, 4>(a, o, s);
+  if (n <= 5632) return run_fwd<X, SHIFT, 16, 352, 3>(a, o, s);
+  if (n <= 8192) return run_fwd<X, SHIFT, 16, 512, 3>(a, o, s);
+  if constexpr (!SHIFT)
+    if (n <= 16384) return run_fwd<X, SHIFT, 32, 512, sizeof(X) == 2 ? 2 : 1>(a, o, s);
+  norm_fwd_rows_kernel<X><<<(unsigned)a.T, 1024, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// As the forward; fp32 rows over 8192 would not fit the ring with two tensors.
+template <typename X, bool SHIFT>
+cudaError_t backward(const BwdArgs& a, const Offsets& o, int64_t max_blocks, int* blocks, cudaStream_t s) {
+  constexpr bool B = sizeof(X) == 2;
+  constexpr int S = B ? 4 : 3;
+  const int n = SHIFT ? a.H + kVec<X> - 1 : a.H;
+  if (n <= 128) return run_bwd<X, SHIFT, 8, 16, S>(a, o, max_blocks, blocks, s);
+  if (n <= 512) return run_bwd<X, SHIFT, 16, 32, S>(a, o, max_blocks, blocks, s);
+  if (n <= 1024) return run_bwd<X, SHIFT, 16, 64, S>(a, o, max_blocks, blocks, s);
+  if (n <= 1536) return run_bwd<X, SHIFT, 16, 96, S>(a, o, max_blocks, blocks, s);
+  if (n <= 2048) return run_bwd<X, SHIFT, 16, 128, S>(a, o, max_blocks, blocks, s);
+  if (n <= 2560) return run_bwd<X, SHIFT, 16, 160, S>(a, o, max_blocks, blocks, s);
+  if (n <= 3584) return run_bwd<X, SHIFT, 16, 224, S>(a, o, max_blocks, blocks, s);
+  if (n <= 4096) return run_bwd<X, SHIFT, 16, 256, S>(a, o, max_blocks, blocks, s);
+  if (n <= 5632) return run_bwd<X, SHIFT, 16, 352, 3>(a, o, max_blocks, blocks, s);
+  if (n <= 8192) return run_bwd<X, SHIFT, 16, 512, 3>(a, o, max_blocks, blocks, s);
+  if constexpr (B && !SHIFT)
+    if (n <= 16384) return run_bwd<X, SHIFT, 32, 512, 2>(a, o, max_blocks, blocks, s);
+  return backward_rows<X>(a, max_blocks, blocks, s);
+}
+
+template <typename X>
+cudaError_t forward_any(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
+  if (o.vectors) return forward<X, false>(a, o, s);
+  if (o.same) return forward<X, true>(a, o, s);
+  norm_fwd_rows_kernel<X><<<(unsigned)a.T, 1024, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename X>
+cudaError_t backward_any(const BwdArgs& a, const Offsets& o, int64_t max_blocks, int* blocks, cudaStream_t s) {
+  if (o.vectors) return backward<X, false>(a, o, max_blocks, blocks, s);
+  if (o.same) return backward<X, true>(a, o, max_blocks, blocks, s);
+  return backward_rows<X>(a, max_blocks, blocks, s);
 }
 
 }  // namespace
 
 cudaError_t launch_layer_norm(const NormDesc& d, const void* x, const void* gamma, const void* beta,
                               void* y, float* mean, float* rstd, cudaStream_t s) {
-  FwdArgs a{x, gamma, beta, y, mean, rstd, d.ld_x, d.ld_y, d.T, d.H, d.wtype, d.eps};
+  const FwdArgs a{x, gamma, beta, y, mean, rstd, d.ld_x, d.ld_y, d.T, d.H, d.wtype, d.eps};
   const int es = d.xtype == MOE_TYPE_BF16 ? 2 : 4;
-  const bool vec = ((int64_t)d.H * es) % 16 == 0 && rows16(x, d.ld_x, d.T, es) && rows16(y, d.ld_y, d.T, es);
-  if (es == 2) return vec ? forward<__nv_bfloat16, 8>(a, s) : forward<__nv_bfloat16, 1>(a, s);
-  return vec ? forward<float, 4>(a, s) : forward<float, 1>(a, s);
+  const void* p[2] = {x, y};
+  const int64_t ld[2] = {d.ld_x, d.ld_y};
+  const Offsets o = offsets_of(p, ld, 2, es, d.T, d.H);
+  return es == 2 ? forward_any<__nv_bfloat16>(a, o, s) : forward_any<float>(a, o, s);
 }
 
 int64_t norm_partial_blocks(int T) { return T < 1024 ? T : 1024; }
@@ -734,19 +806,17 @@ cudaError_t launch_layer_norm_backward(const NormDesc& d, const void* dy, const 
                                        void* dx, void* dgamma, void* dbeta, float* partial,
                                        cudaStream_t s) {
   const bool params = dgamma || dbeta;
-  BwdArgs a{dy, x, gamma, mean, rstd, dx, params ? partial : nullptr, d.ld_y, d.ld_x, d.ld_dx,
-            d.T, d.H, d.wtype};
+  const BwdArgs a{dy, x, gamma, mean, rstd, dx, params ? partial : nullptr, d.ld_y, d.ld_x, d.ld_dx,
+                  d.T, d.H, d.wtype};
   const int es = d.xtype == MOE_TYPE_BF16 ? 2 : 4;
   int blocks = 0;
   if (d.T > 0) {
-    const bool vec = ((int64_t)d.H * es) % 16 == 0 && rows16(x, d.ld_x, d.T, es) &&
-                     rows16(dy, d.ld_y, d.T, es) && rows16(dx, d.ld_dx, d.T, es);
+    const void* p[3] = {x, dy, dx};
+    const int64_t ld[3] = {d.ld_x, d.ld_y, d.ld_dx};
+    const Offsets o = offsets_of(p, ld, 3, es, d.T, d.H);
     const int64_t most = norm_partial_blocks(d.T);
-    cudaError_t e;
-    if (es == 2)
-      e = vec ? backward<__nv_bfloat16, 8>(a, most, &blocks, s) : backward<__nv_bfloat16, 1>(a, most, &blocks, s);
-    else
-      e = vec ? backward<float, 4>(a, most, &blocks, s) : backward<float, 1>(a, most, &blocks, s);
+    const cudaError_t e = es == 2 ? backward_any<__nv_bfloat16>(a, o, most, &blocks, s)
+                                  : backward_any<float>(a, o, most, &blocks, s);
     if (e != cudaSuccess) return e;
   }
   if (params) {
