@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, kNormPerSm)
     grad_squares_kernel(const __grid_constant__ ClipList<N> l, double* partial) {
   __shared__ double sm[32];
   let_next_start();
+  wait_for_previous();
   double acc = 0.0;
   const int64_t chunks = l.first[l.count];
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -176,6 +177,7 @@ __device__ __forceinline__ void publish_norm(float norm, float* out, int32_t* st
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* partial, int np, float* norm,
                                                              int32_t* status) {
   __shared__ double sm[32];
+  let_next_start();
   wait_for_previous();
   const float v = norm_of(partial, np, sm);
   if (threadIdx.x == 0) publish_norm(v, norm, status);
@@ -223,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, kScalePerSm)
     grad_scale_kernel(const __grid_constant__ ClipList<N> l, const double* partial, int np,
                       float max_norm, float* norm, int32_t* status) {
   __shared__ double sm[32];
+  let_next_start();
   wait_for_previous();
   const float total = norm_of(partial, np, sm);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) publish_norm(total, norm, status);
@@ -287,8 +290,7 @@ cudaError_t run(const moe_grad_tensor* t, int count, bool clip, float max_norm, 
     if (l.count == 0) continue;
     int grid = grid_of(l.first[l.count], kNormPerSm);
     if (grid > kMaxBlocks) grid = kMaxBlocks;
-    grad_squares_kernel<N><<<grid, kThreads, 0, s>>>(l, partial + np);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapped(grad_squares_kernel<N>, grid, kThreads, 0, s, l, partial + np);
     if (e != cudaSuccess) return e;
     np += grid;
   }
@@ -298,13 +300,13 @@ cudaError_t run(const moe_grad_tensor* t, int count, bool clip, float max_norm, 
       if (count > N) fill(l, t + i, count - i < N ? count - i : N, chunk);
       if (l.count == 0) continue;
       const cudaError_t e =
-          launch_after(grad_scale_kernel<N>, grid_of(l.first[l.count], kScalePerSm), kThreads, 0, s, l,
+          launch_overlapped(grad_scale_kernel<N>, grid_of(l.first[l.count], kScalePerSm), kThreads, 0, s, l,
                        (const double*)partial, np, max_norm, told ? nullptr : norm, status);
       if (e != cudaSuccess) return e;
       told = true;
     }
   return told ? cudaSuccess
-              : launch_after(grad_norm_kernel, 1, kThreads, 0, s, (const double*)partial, np, norm, status);
+              : launch_overlapped(grad_norm_kernel, 1, kThreads, 0, s, (const double*)partial, np, norm, status);
 }
 
 constexpr int kShort = 48, kLong = 512;   // tensors per launch

@@ -31,7 +31,7 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31; }
 
 // ------------------------------------------------------------- launch order
-// For kernels launched with launch_after(): returns once the kernel before
+// For kernels launched with launch_overlapped(): returns once the kernel before
 // this one has completed and its writes are visible.
 __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -155,12 +155,13 @@ bool make_tmap_out_f32(CUtensorMap* m, void* base, int64_t n, int64_t rows, int6
 // SMs of the current device.
 int sm_count();
 
-// Launch of a kernel that follows another one of the same call on the same
-// stream: its blocks may start while the last blocks of the first kernel run,
-// so every thread has to call wait_for_previous() (common.cuh) before it reads
-// what that kernel wrote, or writes what it may still read.
+// Launch whose blocks may start while the last blocks of the kernel before it
+// on the stream (of this library or not) still run, if that kernel allows it
+// (let_next_start in common.cuh).  Every thread calls wait_for_previous()
+// before its first access to global memory, which returns once that kernel
+// has completed, so only the start-up of the blocks overlaps.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

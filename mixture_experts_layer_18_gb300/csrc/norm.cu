@@ -370,12 +370,14 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 800 / kBlock<L> : 1)
   using Str = Stream<X, CPT, L, SHIFT, S, TH>;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ float sm[2][TH / 32];
+  let_next_start();
   const int group = threadIdx.x / L;
   const int64_t stride = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + group;
   const Lane<X, CPT, L, SHIFT> lane(
       a.H, SHIFT ? shift_of(static_cast<const X*>(a.x) + (row < a.T ? row : 0) * a.ld_x) : 0);
   Str xs(lane, a.x, a.ld_x, dyn);
+  wait_for_previous();
 #pragma unroll
   for (int st = 0; st < S - 1; ++st) {
     xs.fetch(lane, row + st * stride, a.T, st);
@@ -447,6 +449,8 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 800 / kBlock<L> : 1)
 template <typename X>
 __global__ void __launch_bounds__(1024) norm_fwd_rows_kernel(const FwdArgs a) {
   __shared__ float sm[2][32];
+  let_next_start();
+  wait_for_previous();
   const int64_t row = blockIdx.x;
   const X* x = static_cast<const X*>(a.x) + row * a.ld_x;
   float s[1] = {0.f}, q[1] = {0.f};
@@ -499,6 +503,7 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
   const Lane<X, CPT, L, SHIFT> lane(
       a.H, SHIFT ? shift_of(static_cast<const X*>(a.x) + (row < a.T ? row : 0) * a.ld_x) : 0);
   Str xs(lane, a.x, a.ld_x, dyn), ds(lane, a.dy, a.ld_dy, dyn + Str::RING);
+  wait_for_previous();
 #pragma unroll
   for (int st = 0; st < S - 1; ++st) {
     xs.fetch(lane, row + st * stride, a.T, st);
@@ -588,6 +593,7 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
 __global__ void __launch_bounds__(1024) norm_param_grad_kernel(const float* partial, int blocks, int H,
                                                                int wtype, void* dgamma, void* dbeta) {
   __shared__ float sm[32][33];
+  let_next_start();
   wait_for_previous();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
@@ -611,6 +617,8 @@ __global__ void __launch_bounds__(1024) norm_param_grad_kernel(const float* part
 template <typename X>
 __global__ void __launch_bounds__(1024) norm_bwd_rows_kernel(const BwdArgs a) {
   __shared__ float sm[64];
+  let_next_start();
+  wait_for_previous();
   const int64_t row = blockIdx.x;
   const X* x = static_cast<const X*>(a.x) + row * a.ld_x;
   const X* dy = static_cast<const X*>(a.dy) + row * a.ld_dy;
@@ -633,6 +641,8 @@ __global__ void __launch_bounds__(1024) norm_bwd_rows_kernel(const BwdArgs a) {
 // Before the rows kernel: dx may overwrite x or dy.
 template <typename X>
 __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const BwdArgs a) {
+  let_next_start();
+  wait_for_previous();
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= a.H) return;
   float dg = 0.f, db = 0.f;
@@ -654,13 +664,12 @@ cudaError_t backward_rows(const BwdArgs& a, int64_t max_blocks, int* blocks, cud
     int64_t slabs = 64;
     if (slabs > a.T) slabs = a.T;
     if (slabs > max_blocks) slabs = max_blocks;
-    norm_bwd_cols_kernel<X><<<dim3((a.H + 255) / 256, (unsigned)slabs), 256, 0, s>>>(a);
     *blocks = (int)slabs;
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapped(norm_bwd_cols_kernel<X>, dim3((a.H + 255) / 256, (unsigned)slabs),
+                                            256, 0, s, a);
     if (e != cudaSuccess) return e;
   }
-  norm_bwd_rows_kernel<X><<<(unsigned)a.T, 1024, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(norm_bwd_rows_kernel<X>, (unsigned)a.T, 1024, 0, s, a);
 }
 
 // Where the rows of a call's tensors start relative to 16-byte boundaries.
@@ -704,9 +713,8 @@ cudaError_t run(K kern, CtxCache<int>& cache, const Args& a, int rows, int threa
     while (unit * rows % period) ++unit;
     blocks = blocks > unit ? blocks / unit * unit : unit;
   }
-  kern<<<(unsigned)blocks, threads, smem, s>>>(a);
   *blocks_out = (int)blocks;
-  return cudaGetLastError();
+  return launch_overlapped(kern, (unsigned)blocks, threads, smem, s, a);
 }
 
 template <typename X, bool SHIFT, int CPT, int L, int S>
@@ -747,8 +755,7 @@ cudaError_t forward(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
   if (n <= 8192) return run_fwd<X, SHIFT, 16, 512, 3>(a, o, s);
   if constexpr (!SHIFT)
     if (n <= 16384) return run_fwd<X, SHIFT, 32, 512, sizeof(X) == 2 ? 2 : 1>(a, o, s);
-  norm_fwd_rows_kernel<X><<<(unsigned)a.T, 1024, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(norm_fwd_rows_kernel<X>, (unsigned)a.T, 1024, 0, s, a);
 }
 
 // As the forward; fp32 rows over 8192 would not fit the ring with two tensors.
@@ -776,8 +783,7 @@ template <typename X>
 cudaError_t forward_any(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
   if (o.vectors) return forward<X, false>(a, o, s);
   if (o.same) return forward<X, true>(a, o, s);
-  norm_fwd_rows_kernel<X><<<(unsigned)a.T, 1024, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(norm_fwd_rows_kernel<X>, (unsigned)a.T, 1024, 0, s, a);
 }
 
 template <typename X>
@@ -820,7 +826,7 @@ cudaError_t launch_layer_norm_backward(const NormDesc& d, const void* dy, const 
     if (e != cudaSuccess) return e;
   }
   if (params) {
-    return launch_after(norm_param_grad_kernel, dim3((d.H + 31) / 32, 2), 1024, 0, s,
+    return launch_overlapped(norm_param_grad_kernel, dim3((d.H + 31) / 32, 2), 1024, 0, s,
                         (const float*)partial, blocks, d.H, d.wtype, dgamma, dbeta);
   }
   return cudaSuccess;

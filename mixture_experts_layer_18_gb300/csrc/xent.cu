@@ -521,13 +521,25 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int
   __shared__ int sc[32];
   __shared__ bool last;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
+  const int row = blockIdx.x * 32 + lane, r = blockIdx.x * 32 + w;
   float m = -INFINITY, s = 0.f;
+  let_next_start();
   wait_for_previous();
+  // what the row's last step needs, asked for early (z is read for a valid target only)
+  const int t = r < T ? target_of(targets, index64, ignore, V, r) : -1;
+  const float z = t >= 0 ? zt[r] : 0.f;
   if (row < T)
-    for (int i = w; i < np; i += 32) {
-      const float2 p = part[(size_t)i * T + row];
-      join(m, s, p.x, p.y);
+    for (int i = w; i < np; i += 128) {          // four pieces at a time
+      float2 p[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        p[k] = i + 32 * k < np ? part[(size_t)(i + 32 * k) * T + row] : make_float2(-INFINITY, 0.f);
+      const float mn = fmaxf(m, fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x)));
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      s *= ex2(m - ref);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s += p[k].y * ex2(p[k].x - ref);
+      m = mn;
     }
   sm[lane][w] = make_float2(m, s);
   __syncthreads();
@@ -540,16 +552,14 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
     join(m, s, m2, s2);
   }
-  const int r = blockIdx.x * 32 + w;
   if (lane == 0) {
     double mine_loss = 0.0;
     int counts = 0;
     if (r < T) {
       const float l = (m + log2f(s)) * 0.6931471805599453f;
-      const int t = target_of(targets, index64, ignore, V, r);
       if (t == -2) report(status, MOE_ERR_BAD_INDEX);
       counts = t >= 0;
-      const float v = counts ? l - zt[r] : 0.f;
+      const float v = counts ? l - z : 0.f;
       lse[r] = l;
       loss[r] = v;
       mine_loss = v;
@@ -558,34 +568,36 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int
     sc[w] = counts;
   }
   __syncthreads();
-  if (w == 0) {
-    double a = ss[lane];
-    int n = sc[lane];
+  if (gridDim.x > 1) {
+    if (w == 0) {
+      double a = ss[lane];
+      int n = sc[lane];
+      warp_sum(a, n);
+      if (lane == 0) {
+        sums[blockIdx.x] = BlockSum{a, n, 0};
+        __threadfence();
+        last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+      }
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double a = 0.0;
+    int n = 0;
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += 1024) {
+      a += __ldcg(&sums[i].sum);
+      n += __ldcg(&sums[i].count);
+    }
     warp_sum(a, n);
     if (lane == 0) {
-      sums[blockIdx.x] = BlockSum{a, n, 0};
-      __threadfence();
-      last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+      ss[w] = a;
+      sc[w] = n;
     }
+    __syncthreads();
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  double a = 0.0;
-  int n = 0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += 1024) {
-    a += __ldcg(&sums[i].sum);
-    n += __ldcg(&sums[i].count);
-  }
-  warp_sum(a, n);
-  if (lane == 0) {
-    ss[w] = a;
-    sc[w] = n;
-  }
-  __syncthreads();
   if (w) return;
-  a = ss[lane];
-  n = sc[lane];
+  double a = ss[lane];
+  int n = sc[lane];
   warp_sum(a, n);
   if (lane == 0) {
     total[0] = (float)a;
@@ -641,6 +653,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewPerSm) xent_few_kernel(con
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   let_next_start();
+  wait_for_previous();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   const int words = a.pitch / 16;
   for (int i = threadIdx.x; i < 8 * NB * words; i += 32 * kFewWarps) {
@@ -725,6 +738,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewPerSm) xent_few_kernel(con
 __global__ void __launch_bounds__(256) xent_dx_kernel(const float* acc, int ks, int T, int H, int Hp,
                                                       const float* dloss, const float* total,
                                                       int reduction, __nv_bfloat16* dX) {
+  let_next_start();
   wait_for_previous();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int per = H / 8;
@@ -756,9 +770,8 @@ int group_for(int64_t row_bytes) {
   return g < 1 ? 1 : (int)(g < 4096 ? g : 4096);
 }
 
-// `after`: another kernel of the same call comes before this one.
 template <bool BWD>
-cudaError_t launch(const XParams& P, bool after, cudaStream_t s) {
+cudaError_t launch(const XParams& P, cudaStream_t s) {
   auto kern = xent_gemm_kernel<BWD>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -772,13 +785,14 @@ cudaError_t launch(const XParams& P, bool after, cudaStream_t s) {
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   static CtxCache<int> resident;   // pairs that run at once, per context
   int pairs = 0;
   cudaError_t e = resident.get(&pairs, [&](int* v) {
     cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (r != cudaSuccess) return r;
     cudaLaunchConfig_t c = cfg;
+    c.numAttrs = 1;
     c.gridDim = dim3(2 * (sm_count() / 2), 1, 1);
     int n = 0;
     r = cudaOccupancyMaxActiveClusters(&n, kern, &c);
@@ -791,7 +805,6 @@ cudaError_t launch(const XParams& P, bool after, cudaStream_t s) {
   for (int p = 0; p < P.njob; ++p) tiles += (int64_t)P.job[p].mt * P.job[p].nt * P.job[p].ks;
   if (tiles < pairs) pairs = (int)tiles;
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  cfg.numAttrs = after ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
@@ -835,8 +848,7 @@ cudaError_t run_few(const FewArgs& a, int* blocks, cudaStream_t s) {
   if (n > kFewMaxBlocks) n = kFewMaxBlocks;
   if (n > tasks) n = tasks;
   *blocks = n;
-  xent_few_kernel<NB><<<n, 32 * kFewWarps, 8 * NB * a.pitch, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(xent_few_kernel<NB>, n, 32 * kFewWarps, 8 * NB * a.pitch, s, a);
 }
 
 cudaError_t launch_few(const XentDesc& d, const void* X, const void* W, const void* targets, float2* part,
@@ -945,9 +957,9 @@ cudaError_t launch_xent_forward(const XentDesc& d, const void* X, const void* W,
       return cudaSuccess;
     }
     np = 2 * P.job[0].nt;
-    XENT_TRY(launch<false>(P, false, s));
+    XENT_TRY(launch<false>(P, s));
   }
-  return launch_after(xent_join_kernel, up(d.T, 32), 1024, 0, s, (const float2*)part, np, (const float*)zt,
+  return launch_overlapped(xent_join_kernel, up(d.T, 32), 1024, 0, s, (const float2*)part, np, (const float*)zt,
                       targets, i64, d.ignore_index, d.T, d.V, loss, lse,
                       reinterpret_cast<BlockSum*>(ws + w.sums), ticket, total, status);
 }
@@ -976,7 +988,7 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
     P.job[0].kind = XK_DZ;
     bool ok = logits_job(P.job[0], d, X, W, v0, cols) &&
               make_tmap_out(&P.job[0].tmO, dz, d.T, w.piece, w.piece);
-    if (ok) XENT_TRY(launch<true>(P, v0 > 0, s));
+    if (ok) XENT_TRY(launch<true>(P, s));
     // dX (+)= dz W[piece], dW[piece] = dz^T X
     XParams Q = params_of(d, targets, status);
     Q.dloss = dloss;
@@ -1020,11 +1032,11 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
       *st = MOE_ERR_CUDA;
       return cudaSuccess;
     }
-    XENT_TRY(launch<true>(Q, true, s));
+    XENT_TRY(launch<true>(Q, s));
   }
   if (dX && w.slices > 1) {
     const int64_t n = (int64_t)d.T * (d.H / 8);
-    return launch_after(xent_dx_kernel, (unsigned)((n + 255) / 256), 256, 0, s,
+    return launch_overlapped(xent_dx_kernel, (unsigned)((n + 255) / 256), 256, 0, s,
                         reinterpret_cast<const float*>(ws + w.acc), w.slices, d.T, d.H, w.Hp, dloss, total,
                         reduction, static_cast<__nv_bfloat16*>(dX));
   }
