@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(kThreads, kScalePerSm)
 }
 
 // ------------------------------------------------------------------ host
-// Elements per chunk: enough chunks for every block to have several, between
-// 2048 (a thread's one vector) and 32768 elements.
+// Elements per chunk: enough for every block to have several, between
+// 2048 (a vector per thread) and 32768 elements.  (A dozen per block, for an
+// evener share, measured 20% slower: a chunk starts with empty loads.)
 int chunk_for(const moe_grad_tensor* t, int count, int blocks) {
   int64_t total = 0;
   for (int i = 0; i < count; ++i) total += t[i].n;

@@ -284,20 +284,25 @@ struct Stream {
   static constexpr int V = kVec<X>, NL = CPT / V;
   static constexpr int RING = S * NL * THREADS * 16;    // bytes per block
   using Lane_ = Lane<X, CPT, L, SHIFT>;
-  const X* p;
-  int64_t ld;
+  const X* q;            // this lane's part of the next row to fetch
+  int64_t ld, step;      // elements from row to row, and between this group's rows
   uint8_t* at;
-  __device__ __forceinline__ Stream(const Lane_& l, const void* base, int64_t ld_, uint8_t* ring)
-      : p(static_cast<const X*>(base) + l.first()), ld(ld_), at(ring + threadIdx.x * 16) {
+  __device__ __forceinline__ Stream(const Lane_& l, const void* base, int64_t ld_, uint32_t row, uint32_t stride,
+                                    uint8_t* ring)
+      : q(static_cast<const X*>(base) + row * ld_ + l.first()), ld(ld_), step(stride * ld_),
+        at(ring + threadIdx.x * 16) {
 #pragma unroll
     for (int j = 0; j < NL; ++j)
       if (!l.valid(j))
         for (int st = 0; st < S; ++st)
           *reinterpret_cast<uint4*>(at + (st * NL + j) * THREADS * 16) = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void fetch(const Lane_& l, int64_t row, int T, int st) {
-    if (row >= T) return;
-    const X* q = p + row * ld;
+  // Starts the copies of `row` (the group's next one) into ring stage st.
+  __device__ __forceinline__ void fetch(const Lane_& l, uint32_t row, uint32_t T, int st) {
+    if (row < T) copy(l, row, T, st);
+    q += step;
+  }
+  __device__ __forceinline__ void copy(const Lane_& l, uint32_t row, uint32_t T, int st) {
     uint8_t* d = at + st * (NL * THREADS * 16);
     if (!SHIFT || !l.ends) {
 #pragma unroll
@@ -306,7 +311,7 @@ struct Stream {
       return;
     }
     // elements from the tensor's first to this lane's, and to the tensor's end
-    const int64_t before = row * ld + l.first();
+    const int64_t before = (int64_t)row * ld + l.first();
     const int64_t after = (int64_t)(T - 1 - row) * ld + l.left;
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
@@ -372,15 +377,17 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 800 / kBlock<L> : 1)
   __shared__ float sm[2][TH / 32];
   let_next_start();
   const int group = threadIdx.x / L;
-  const int64_t stride = (int64_t)gridDim.x * ROWS;
-  int64_t row = (int64_t)blockIdx.x * ROWS + group;
+  const uint32_t T = a.T, stride = gridDim.x * ROWS;   // (T below 2^31: rows past it do not wrap)
+  uint32_t row = blockIdx.x * ROWS + group;
   const Lane<X, CPT, L, SHIFT> lane(
-      a.H, SHIFT ? shift_of(static_cast<const X*>(a.x) + (row < a.T ? row : 0) * a.ld_x) : 0);
-  Str xs(lane, a.x, a.ld_x, dyn);
+      a.H, SHIFT ? shift_of(static_cast<const X*>(a.x) + (row < T ? row : 0) * a.ld_x) : 0);
+  Str xs(lane, a.x, a.ld_x, row, stride, dyn);
+  X* out = static_cast<X*>(a.y) + row * a.ld_y;
+  const int64_t out_step = stride * a.ld_y;
   wait_for_previous();
 #pragma unroll
   for (int st = 0; st < S - 1; ++st) {
-    xs.fetch(lane, row + st * stride, a.T, st);
+    xs.fetch(lane, row + st * stride, T, st);
     copy_commit();
   }
   Weights<X, CPT, L, SHIFT, TH> gam, bet;
@@ -389,9 +396,9 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 800 / kBlock<L> : 1)
   bet.load(lane, a.beta, a.wtype, 0.f, wsm + CPT / 4 * TH);
   const float inv = 1.f / (float)a.H;
   int st = 0;
-  for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.T; base += stride, row += stride) {
+  for (uint32_t base = blockIdx.x * ROWS; base < T; base += stride, row += stride) {
     F2 x[CPT / 2];
-    xs.fetch(lane, row + (S - 1) * stride, a.T, st == 0 ? S - 1 : st - 1);
+    xs.fetch(lane, row + (S - 1) * stride, T, st == 0 ? S - 1 : st - 1);
     copy_commit();
     copy_wait<S - 1>();
     xs.take(lane, x, st);
@@ -432,13 +439,14 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 800 / kBlock<L> : 1)
     const F2 rr = f2(r, r);
 #pragma unroll
     for (int i = 0; i < CPT / 2; ++i) x[i] = fma2(mul2(x[i], rr), g[i], b[i]);
-    if (row < a.T) {
-      store_row(lane, static_cast<X*>(a.y) + row * a.ld_y, x);
+    if (row < T) {
+      store_row(lane, out, x);
       if (lane.t == 0) {
         if (a.mean) a.mean[row] = mu;
         if (a.rstd) a.rstd[row] = r;
       }
     }
+    out += out_step;
   }
   copy_wait<0>();
 }
@@ -498,19 +506,21 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
   __shared__ float sm[2][TH / 16];
   let_next_start();
   const int group = threadIdx.x / L;
-  const int64_t stride = (int64_t)gridDim.x * ROWS;
-  int64_t row = (int64_t)blockIdx.x * ROWS + group;
+  const uint32_t T = a.T, stride = gridDim.x * ROWS;   // (T below 2^31: rows past it do not wrap)
+  uint32_t row = blockIdx.x * ROWS + group;
   const Lane<X, CPT, L, SHIFT> lane(
-      a.H, SHIFT ? shift_of(static_cast<const X*>(a.x) + (row < a.T ? row : 0) * a.ld_x) : 0);
-  Str xs(lane, a.x, a.ld_x, dyn), ds(lane, a.dy, a.ld_dy, dyn + Str::RING);
+      a.H, SHIFT ? shift_of(static_cast<const X*>(a.x) + (row < T ? row : 0) * a.ld_x) : 0);
+  Str xs(lane, a.x, a.ld_x, row, stride, dyn), ds(lane, a.dy, a.ld_dy, row, stride, dyn + Str::RING);
+  X* dx = static_cast<X*>(a.dx) + row * a.ld_dx;
+  const int64_t dx_step = stride * a.ld_dx;
   wait_for_previous();
 #pragma unroll
   for (int st = 0; st < S - 1; ++st) {
-    xs.fetch(lane, row + st * stride, a.T, st);
-    ds.fetch(lane, row + st * stride, a.T, st);
+    xs.fetch(lane, row + st * stride, T, st);
+    ds.fetch(lane, row + st * stride, T, st);
     copy_commit();
   }
-  auto at = [&](int64_t q) { return q < a.T ? q : a.T - 1; };
+  auto at = [&](uint32_t q) { return q < T ? q : T - 1; };
   float mu = a.mean[at(row)], r = a.rstd[at(row)];
   Weights<X, CPT, L, SHIFT, TH> gam;
   gam.load(lane, a.gamma, a.wtype, 1.f, reinterpret_cast<float4*>(dyn + 2 * Str::RING));
@@ -519,14 +529,14 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
   for (int i = 0; i < CPT / 2; ++i) dg[i] = db[i] = f2(0.f, 0.f);
   const float inv = 1.f / (float)a.H;
   int st = 0, par = 0;
-  for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.T; base += stride, row += stride) {
+  for (uint32_t base = blockIdx.x * ROWS; base < T; base += stride, row += stride) {
     const float rc = r, bc = -mu * r;
-    const bool live = row < a.T;
+    const bool live = row < T;
     mu = a.mean[at(row + stride)];
     r = a.rstd[at(row + stride)];
     const int to = st == 0 ? S - 1 : st - 1;
-    xs.fetch(lane, row + (S - 1) * stride, a.T, to);
-    ds.fetch(lane, row + (S - 1) * stride, a.T, to);
+    xs.fetch(lane, row + (S - 1) * stride, T, to);
+    ds.fetch(lane, row + (S - 1) * stride, T, to);
     copy_commit();
     copy_wait<S - 1>();
     const F2 rr = f2(rc, rc), bb = f2(bc, bc);
@@ -556,7 +566,8 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
     const F2 AA = f2(A, A), BB = f2(B, B);
 #pragma unroll
     for (int i = 0; i < CPT / 2; ++i) x[i] = fma2(d[i], rr, fma2(x[i], AA, BB));
-    if (live) store_row(lane, static_cast<X*>(a.dx) + row * a.ld_dx, x);
+    if (live) store_row(lane, dx, x);
+    dx += dx_step;
   }
   copy_wait<0>();
   if (!a.partial) return;
