@@ -345,7 +345,8 @@ typedef enum { MOE_REDUCE_NONE = 0, MOE_REDUCE_SUM = 1, MOE_REDUCE_MEAN = 2 } mo
  *   ignore_index  targets with this value do not count (loss 0, gradient 0).
  *   index_type    of targets.
  * Limits: T >= 0, V >= 1, H a positive multiple of 8; other H return
- * MOE_ERR_UNSUPPORTED (TMA rows start on 16-byte boundaries). */
+ * MOE_ERR_UNSUPPORTED (TMA rows start on 16-byte boundaries), and so do sizes
+ * of 2^28 and more 256 x 256 tiles. */
 typedef struct {
   int T, H, V;
   int64_t ld_x, ld_w;
@@ -377,6 +378,8 @@ moe_status moe_cross_entropy(const moe_xent_dims* dims, const void* X, const voi
  *   reduction  s_t: MOE_REDUCE_NONE dloss[t] (dloss float [T]),
  *              MOE_REDUCE_SUM dloss[0], MOE_REDUCE_MEAN dloss[0] / total[2].
  *   lse, total from the forward (total may be NULL unless MEAN).
+ * A row that does not count adds exact zeros to dz; as dW = dz^T X runs over
+ * all rows, a NaN or an infinity in such a row of X still reaches dW.
  *   dX [T, H], dW [V, H] bf16, contiguous; NULL leaves one out. */
 moe_status moe_cross_entropy_backward(const moe_xent_dims* dims, const void* X, const void* W,
                                       const void* targets, const float* lse, const float* total,

@@ -136,8 +136,8 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int group, float* sm) {
 // 1 / sqrt(v): the approximation and one Newton step (below one ulp of fp32).
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float r = rsqrtf(v);
-  // v = 0 gives infinity, which the step would turn into NaN
-  return v > 0.f ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
+  // (0 and infinity have their values already; the step would make them NaN)
+  return v > 0.f && v <= 3.402823466e38f ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
 }
 
 // ------------------------------------------------------------------ rows

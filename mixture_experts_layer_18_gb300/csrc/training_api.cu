@@ -33,8 +33,10 @@ moe_status xent_check(const moe_xent_dims* d) {
   if (d->index_type != MOE_INDEX_I32 && d->index_type != MOE_INDEX_I64) return MOE_ERR_INVALID_ARG;
   if (d->H % 8 || d->ld_x % 8 || d->ld_w % 8) return MOE_ERR_UNSUPPORTED;
   if (d->T > (1 << 30) || d->V > (1 << 30) || d->H > (1 << 20)) return MOE_ERR_UNSUPPORTED;
-  const int64_t tiles = (((int64_t)d->T + 255) / 256) * (((int64_t)d->V + 255) / 256);
-  return tiles < (1 << 30) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  auto tiles = [](int64_t n) { return (n + 255) / 256; };
+  const int64_t t = tiles(d->T), h = tiles(d->H), v = tiles(d->V);
+  // (192-column tiles and slices of K at most double a count)
+  return t * v < (1 << 28) && t * h < (1 << 28) && v * h < (1 << 28) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 XentDesc xent_desc(const moe_xent_dims* d) {
   return XentDesc{d->T, d->H, d->V, d->ld_x, d->ld_w, d->ignore_index, d->index_type, wait_limit_ns()};

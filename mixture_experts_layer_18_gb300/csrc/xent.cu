@@ -908,13 +908,14 @@ XParams params_of(const XentDesc& d, const void* targets, int32_t* status) {
 }
 
 // Width of the logit tiles: 256 columns, or 192 where that saves enough of the
-// last, partly filled round of tiles over the SM pairs to make up for moving
-// 8% more operand bytes per product (T = 1001, V = 10007: 3 rounds of either,
-// TNMEASURE).
+// last, partly filled round of tiles over the SM pairs to make up for the
+// operand bytes, a sixth more per product.  Measured, forward: T = 1001, H =
+// 1032, V = 10007 (three rounds of either) 28.8 against 30.6 us; T = 1500, H =
+// 2048, V = 30000 (no round saved) 141 against 117 us.
 int tile_width(int T, int cols, int pairs) {
   const int64_t mt = up(T, kTile);
   const int64_t r256 = up(mt * up(cols, 256), pairs) * 256LL, r192 = up(mt * up(cols, 192), pairs) * 192LL;
-  return r192 * 108 < r256 * 100 ? 192 : 256;
+  return r192 * 115 < r256 * 100 ? 192 : 256;
 }
 
 bool logits_job(XJob& g, const XentDesc& d, const void* X, const void* W, int v0, int cols) {

@@ -3,7 +3,8 @@ step: layer norm, cross entropy over a vocabulary, and gradient clipping.
 
 As in ``layer``, PyTorch supplies device memory and the stream; every
 computation is a call into libmoe_gb300.so.  Each class owns the statistics
-and the workspace of one problem shape on one device, checks the tensors it
+and the workspace of one problem shape on one device (calls on different
+streams have to be ordered by the caller), checks the tensors it
 is given against that shape, and raises ``MoEError`` on any non-OK return code
 and for tensors that do not fit.
 """

@@ -112,6 +112,25 @@ def test_strided_rows(pad, off, dtype):
     _check(x, w, b, dy, _run(x, w, b, dy))
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_tensors_at_different_offsets(dtype):
+    """x, y, dy and dx that start at different places in their 16-byte vectors."""
+    import torch
+    from mixture_experts_layer_18_gb300.training import LayerNorm
+    dt = getattr(torch, dtype)
+    x, w, b, dy = _make(77, 300, dt, torch.float32, pad=3)
+    flat = torch.zeros(77 * 300 + 5, dtype=dt, device="cuda")
+    n = LayerNorm(77, 300, dtype=dt, weight_dtype=torch.float32)
+    y, dx = flat[1:1 + 77 * 300].view(77, 300), torch.zeros((77, 301), dtype=dt, device="cuda")[:, 1:]
+    dg, db = torch.zeros_like(w), torch.zeros_like(w)
+    n.forward(x, w, b, y)
+    n.backward(dy, x, w, dx, dg, db)
+    torch.cuda.synchronize()
+    out = dict(y=_f64(y), dx=_f64(dx), dgamma=_f64(dg), dbeta=_f64(db), mean=_f64(n.mean), rstd=_f64(n.rstd))
+    _check(x, w, b, dy, out)
+    assert flat[0] == 0 and not flat[1 + 77 * 300:].any()
+
+
 def test_many_rows():
     import torch
     x, w, b, dy = _make(20011, 192, torch.float32, torch.bfloat16)
@@ -145,6 +164,15 @@ def test_constant_rows_and_zeros():
     out = _run(x, w, b, dy)
     _check(x, w, b, dy, out)
     assert np.array_equal(out["y"][0], _f64(b)) and np.array_equal(out["y"][1], _f64(b))
+
+
+def test_variance_past_fp32():
+    """A row whose variance overflows fp32 has rstd 0, as the formula says: y is beta."""
+    import torch
+    x, w, b, dy = _make(5, 256, torch.float32, torch.float32)
+    x[1] *= 1e25
+    out = _run(x, w, b, dy)
+    assert out["rstd"][1] == 0 and np.array_equal(out["y"][1], _f64(b)) and np.isfinite(out["y"]).all()
 
 
 def test_bad_rows_stay_alone():

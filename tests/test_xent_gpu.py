@@ -178,6 +178,29 @@ def test_bad_rows_stay_alone():
     assert np.isnan(out["dX"][5]).all() and np.array_equal(out["lse"][rows], clean["lse"][rows])
 
 
+def test_bad_rows_stay_alone_among_few_tokens():
+    X, W, t = _make(6, 72, 900)
+    clean = _run(X, W, t, backward=False)
+    X[2, 70], X[4, 0] = float("nan"), float("inf")
+    out = _run(X, W, t, backward=False)
+    assert np.isnan(out["loss"][[2, 4]]).all() and np.isnan(out["lse"][[2, 4]]).all()
+    keep = [0, 1, 3, 5]
+    assert np.array_equal(out["loss"][keep], clean["loss"][keep])
+    assert np.array_equal(out["lse"][keep], clean["lse"][keep])
+
+
+def test_ignored_value_inside_the_vocabulary():
+    from mixture_experts_layer_18_gb300.training import CrossEntropy
+    for T in (12, 130):
+        X, W, t = _make(T, 64, 300)
+        t[::3] = 7
+        c = CrossEntropy(T, 64, 300, ignore_index=7)
+        out = _run(X, W, t, op=c)
+        ref, _, mean = O.cross_entropy(_f64(X), _f64(W), t.cpu().numpy(), 7)
+        assert (out["loss"][::3] == 0).all() and abs(out["total"][1] - mean) <= 1e-4 * mean
+        assert out["total"][2] == (ref != 0).sum()
+
+
 def test_no_tokens():
     X, W, t = _make(0, 64, 300)
     out = _run(X, W, t)
