@@ -388,7 +388,8 @@ moe_status moe_cross_entropy_backward(const moe_xent_dims* dims, const void* X, 
                                       void* stream);
 
 /* One gradient tensor of n contiguous elements; dst (same type) is used by
- * moe_clip_grads and may be src, else it must not overlap any src.  Pointers
+ * moe_clip_grads and may be src, else it must not overlap any src; a list
+ * names no memory twice (a shared weight has one gradient).  Pointers
  * need only the alignment of their element type; src and dst with the same
  * offset from a 16-byte boundary run fastest. */
 typedef struct {
@@ -403,8 +404,8 @@ size_t moe_grad_workspace_size(int count);
 
 /* Global L2 norm: *norm = sqrt(sum over all tensors of g^2).  `tensors` is
  * HOST memory, read before the call returns.  Sums are fp32 over a few dozen
- * elements, double above that; gradients whose squares leave the range of
- * fp32 are summed in double.  A norm that is not finite is written as it is
+ * elements, pairs of fp32 numbers above that; gradients whose squares leave
+ * the range of fp32 are summed in double.  A norm that is not finite is written as it is
  * and reported (MOE_ERR_BAD_INPUT).  No tensor (or only empty ones): 0.
  *   norm  float [1] (device).   ws  16-byte aligned. */
 moe_status moe_grad_norm(const moe_grad_tensor* tensors, int count, float* norm, void* ws,

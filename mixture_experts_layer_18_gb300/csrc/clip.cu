@@ -10,8 +10,13 @@
 // launch per pass.  The list travels in the kernel's parameters: no table is
 // copied to the device.
 //
-// The sums of a thread are fp32 over one chunk, then double; every sum has a
-// fixed order, so the norm is the same in every run on one GPU.
+// A thread's squares are summed in fp32 over one chunk (at most 32 terms to an
+// accumulator), everything above that in pairs of fp32 numbers (the sum and
+// what its rounding lost, by Knuth's two-sum), which is about as exact as
+// double: the GPU's double rate is so low that a block's sum and root in double
+// took 5 us.  Chunks whose sum leaves the range in which fp32 keeps squares go
+// through a double instead.  Every sum has a fixed order, so the norm is the
+// same in every run on one GPU.
 //
 // Measured on 1.21 GB of bf16 gradients: the norm reads 6.4 TB/s.  The scaling
 // pass wants every warp the SM can hold, each with two vectors on the way
@@ -50,16 +55,43 @@ __device__ __forceinline__ int tensor_of(const ClipList<N>& l, int64_t c) {
   return lo;
 }
 
-__device__ __forceinline__ double block_sum(double v, double* sm) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// A sum as hi + lo.
+struct Sum2 {
+  float hi, lo;
+  __device__ __forceinline__ void add(float h, float l) {
+    const float s = hi + h, t = s - hi;
+    lo += ((hi - (s - t)) + (h - t)) + l;
+    hi = s;
+  }
+};
+
+// What a block hands on: its sum, and the part of it that was taken in double.
+struct Partial {
+  Sum2 sum;
+  double wild;
+};
+
+// Sums over the block, the same in every thread.  The double one costs
+// nothing where every thread's is zero.
+__device__ __forceinline__ Partial block_sum(Partial v) {
+  __shared__ Partial sm[kThreads / 32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const bool wild = __syncthreads_or(v.wild != 0.0);     // (a NaN too)
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float h = __shfl_xor_sync(0xffffffffu, v.sum.hi, o), l = __shfl_xor_sync(0xffffffffu, v.sum.lo, o);
+    v.sum.add(h, l);
+    if (wild) v.wild += __shfl_xor_sync(0xffffffffu, v.wild, o);
+  }
   if (lane == 0) sm[w] = v;
   __syncthreads();
-  v = lane < kThreads / 32 ? sm[lane] : 0.0;
+  v = sm[0];
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return __shfl_sync(0xffffffffu, v, 0);
+  for (int i = 1; i < kThreads / 32; ++i) {
+    v.sum.add(sm[i].sum.hi, sm[i].sum.lo);
+    if (wild) v.wild += sm[i].wild;
+  }
+  return v;
 }
 
 // ------------------------------------------------------------- elements
@@ -92,9 +124,9 @@ __device__ __forceinline__ int head_of(const G* p, int n) {
 }
 
 // ----------------------------------------------------------------- norm
-// This thread's share of the squares of p[0, n).
+// Adds this thread's share of the squares of p[0, n).
 template <typename G>
-__device__ __forceinline__ double squares(const G* p, int n) {
+__device__ __forceinline__ void squares(const G* p, int n, Partial& acc) {
   constexpr int V = Vec<G>::N;
   const int head = head_of(p, n);
   const int nv = (n - head) / V;
@@ -122,11 +154,15 @@ __device__ __forceinline__ double squares(const G* p, int n) {
     s[1] += v * v;
   }
   const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-  // squares that left the range where fp32 keeps them (a sum beyond 2^120, or
-  // one below 2^-116, where a square may have been rounded as a subnormal
-  // number) are taken again in double
+  // squares that left the range where fp32 keeps them (a sum beyond 2^80,
+  // which leaves room for the sums of all chunks, or one below 2^-116, where a
+  // square may have been rounded as a subnormal number) are taken again in
+  // double; a NaN stays one
   const bool low = sum < 1.2e-35f && (bits & (sizeof(G) == 2 ? 0x7fff7fffu : 0x7fffffffu));
-  if (!low && !(sum > 1.3e36f)) return (double)sum;   // NaN stays NaN
+  if (!low && !(sum > 1.2e24f)) {
+    acc.sum.add(sum, 0.f);
+    return;
+  }
   double d = 0.0;
   for (int i = threadIdx.x; i < nv; i += kThreads) {
     float v[V];
@@ -138,35 +174,39 @@ __device__ __forceinline__ double squares(const G* p, int n) {
     const double v = get(p + tail0 + threadIdx.x);
     d += v * v;
   }
-  return d;
+  acc.wild += d;
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, kNormPerSm)
-    grad_squares_kernel(const __grid_constant__ ClipList<N> l, double* partial) {
-  __shared__ double sm[32];
+    grad_squares_kernel(const __grid_constant__ ClipList<N> l, Partial* partial) {
   let_next_start();
   wait_for_previous();
-  double acc = 0.0;
+  Partial acc = {{0.f, 0.f}, 0.0};
   const int64_t chunks = l.first[l.count];
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int i = tensor_of(l, c);
     const int64_t e0 = (c - l.first[i]) * l.chunk;
     const int64_t left = l.n[i] - e0;
     const int n = left < l.chunk ? (int)left : l.chunk;
-    acc += l.type[i] == MOE_TYPE_BF16
-               ? squares(static_cast<const __nv_bfloat16*>(l.src[i]) + e0, n)
-               : squares(static_cast<const float*>(l.src[i]) + e0, n);
+    if (l.type[i] == MOE_TYPE_BF16) squares(static_cast<const __nv_bfloat16*>(l.src[i]) + e0, n, acc);
+    else squares(static_cast<const float*>(l.src[i]) + e0, n, acc);
   }
-  acc = block_sum(acc, sm);
+  acc = block_sum(acc);
   if (threadIdx.x == 0) partial[blockIdx.x] = acc;
 }
 
 // The norm from all blocks' partial sums (every thread gets it).
-__device__ __forceinline__ float norm_of(const double* partial, int np, double* sm) {
-  double v = 0.0;
-  for (int i = threadIdx.x; i < np; i += kThreads) v += partial[i];
-  return (float)sqrt(block_sum(v, sm));
+__device__ __forceinline__ float norm_of(const Partial* partial, int np) {
+  Partial v = {{0.f, 0.f}, 0.0};
+  for (int i = threadIdx.x; i < np; i += kThreads) {
+    const Partial p = partial[i];
+    v.sum.add(p.sum.hi, p.sum.lo);
+    if (p.wild != 0.0) v.wild += p.wild;
+  }
+  v = block_sum(v);
+  if (v.wild != 0.0) return (float)sqrt(v.wild + (double)v.sum.hi + (double)v.sum.lo);
+  return sqrtf(v.sum.hi + v.sum.lo);
 }
 
 __device__ __forceinline__ void publish_norm(float norm, float* out, int32_t* status) {
@@ -174,12 +214,11 @@ __device__ __forceinline__ void publish_norm(float norm, float* out, int32_t* st
   if (!(norm <= 3.402823466e38f)) report(status, MOE_ERR_BAD_INPUT);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* partial, int np, float* norm,
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Partial* partial, int np, float* norm,
                                                              int32_t* status) {
-  __shared__ double sm[32];
   let_next_start();
   wait_for_previous();
-  const float v = norm_of(partial, np, sm);
+  const float v = norm_of(partial, np);
   if (threadIdx.x == 0) publish_norm(v, norm, status);
 }
 
@@ -222,12 +261,11 @@ __device__ __forceinline__ void scale_chunk(const G* p, G* q, int n, float c) {
 // the end of the list: what the norm's pass read last is still in L2.
 template <int N>
 __global__ void __launch_bounds__(kThreads, kScalePerSm)
-    grad_scale_kernel(const __grid_constant__ ClipList<N> l, const double* partial, int np,
+    grad_scale_kernel(const __grid_constant__ ClipList<N> l, const Partial* partial, int np,
                       float max_norm, float* norm, int32_t* status) {
-  __shared__ double sm[32];
   let_next_start();
   wait_for_previous();
-  const float total = norm_of(partial, np, sm);
+  const float total = norm_of(partial, np);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) publish_norm(total, norm, status);
   // a norm that is not finite scales nothing (the status says so)
   const float c = total > max_norm && total <= 3.402823466e38f ? max_norm / total : 1.f;
@@ -281,7 +319,7 @@ int grid_of(int64_t chunks, int per_sm) {
 }
 
 template <int N>
-cudaError_t run(const moe_grad_tensor* t, int count, bool clip, float max_norm, double* partial,
+cudaError_t run(const moe_grad_tensor* t, int count, bool clip, float max_norm, Partial* partial,
                 float* norm, int32_t* status, cudaStream_t s) {
   const int chunk = chunk_for(t, count, sm_count() * kNormPerSm);
   ClipList<N> l;
@@ -302,12 +340,12 @@ cudaError_t run(const moe_grad_tensor* t, int count, bool clip, float max_norm, 
       if (l.count == 0) continue;
       const cudaError_t e =
           launch_overlapped(grad_scale_kernel<N>, grid_of(l.first[l.count], kScalePerSm), kThreads, 0, s, l,
-                       (const double*)partial, np, max_norm, told ? nullptr : norm, status);
+                       (const Partial*)partial, np, max_norm, told ? nullptr : norm, status);
       if (e != cudaSuccess) return e;
       told = true;
     }
   return told ? cudaSuccess
-              : launch_overlapped(grad_norm_kernel, 1, kThreads, 0, s, (const double*)partial, np, norm, status);
+              : launch_overlapped(grad_norm_kernel, 1, kThreads, 0, s, (const Partial*)partial, np, norm, status);
 }
 
 constexpr int kShort = 48, kLong = 512;   // tensors per launch
@@ -317,12 +355,13 @@ constexpr int kShort = 48, kLong = 512;   // tensors per launch
 size_t grad_workspace_bytes(int count) {
   const int n = count <= kShort ? kShort : kLong;
   const size_t launches = count <= 0 ? 1 : ((size_t)count + n - 1) / n;
-  return launches * kMaxBlocks * sizeof(double);
+  return launches * kMaxBlocks * sizeof(Partial);
 }
 
 // Short lists use a small parameter block (a launch copies it).
 cudaError_t launch_grad_clip(const moe_grad_tensor* t, int count, bool clip, float max_norm,
-                             double* partial, float* norm, int32_t* status, cudaStream_t s) {
+                             void* ws, float* norm, int32_t* status, cudaStream_t s) {
+  Partial* partial = static_cast<Partial*>(ws);
   if (count <= kShort) return run<kShort>(t, count, clip, max_norm, partial, norm, status, s);
   return run<kLong>(t, count, clip, max_norm, partial, norm, status, s);
 }

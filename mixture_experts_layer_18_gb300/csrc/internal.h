@@ -194,7 +194,7 @@ cudaError_t launch_layer_norm_backward(const NormDesc& d, const void* dy, const 
 // clip.cu
 size_t grad_workspace_bytes(int count);
 cudaError_t launch_grad_clip(const moe_grad_tensor* t, int count, bool clip, float max_norm,
-                             double* partial, float* norm, int32_t* status, cudaStream_t s);
+                             void* ws, float* norm, int32_t* status, cudaStream_t s);
 
 // xent.cu
 struct XentDesc {

@@ -61,7 +61,7 @@ moe_status grads(const moe_grad_tensor* t, int count, bool clip, float max_norm,
       ws_bytes < grad_workspace_bytes(count))
     return MOE_ERR_INVALID_ARG;
   if (clip && !(std::isfinite(max_norm) && max_norm >= 0.f)) return MOE_ERR_INVALID_ARG;
-  return cuda_status(launch_grad_clip(t, count, clip, max_norm, static_cast<double*>(ws), norm,
+  return cuda_status(launch_grad_clip(t, count, clip, max_norm, ws, norm,
                                       dev_status, static_cast<cudaStream_t>(stream)));
 }
 

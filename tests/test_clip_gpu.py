@@ -2,7 +2,7 @@
 definition.
 
 Tolerances: a thread's squares are summed in fp32, at most 32 terms to an
-accumulator and each rounded once when squared, then in double: the sum of
+accumulator and each rounded once when squared, then almost exactly: the sum of
 squares is within 40 * 2^-24 of its value, the norm within half of that plus
 its own rounding.  A clipped value adds the division's, the product's and the
 stored type's rounding."""
