@@ -24,13 +24,20 @@
 // one m only (its stride over the rows is a multiple of the period), so its
 // columns stay the same.  The vectors at a row's ends hold elements of its
 // neighbours too: those are masked after the copy, and the stores there go by
-// elements (4097 x 2049 bf16, forward and backward: all moves by elements 14.3
-// and 22.7 us, SHIFTMEASURE).  L and the columns per lane are compile-time numbers:
+// elements.  L and the columns per lane are compile-time numbers:
 // a row's offsets are then part of the instructions, which with the arithmetic
 // in pairs (fp32x2) keeps a row's instructions below the time that HBM takes
 // for it (they were the bound of a first version with both at run time).
 // Columns past the row's end read as zero; a group past the last row works on
 // what its slots hold and stores nothing.
+//
+// Measured (GB300, bf16, gamma and beta bf16):
+//   16384 x 4096, from HBM: forward 42.5 us (6.3 TB/s), backward 67 us (6.0
+//   TB/s) and 4 - 6 us for the column sums' last step;
+//   4097 x 2049, from L2: forward 11.8, backward 18.4 us; 2056 columns, on
+//   vectors, 7.8 and 15.8 us;  one row of 4096: 2.3 and 4.9 us.
+// From L2 the bound is the issue rate (13 instructions per element forward),
+// from HBM its bandwidth.
 #include "common.cuh"
 #include "internal.h"
 
@@ -452,9 +459,33 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 800 / kBlock<L> : 1)
 }
 
 // Rows that the kernel above does not take (too long, or x and y at different
-// offsets from 16-byte boundaries): a block per row, three passes over it
-// (the second and third find most of it in L1 or L2).
-template <typename X>
+// offsets from 16-byte boundaries): a block per row, three passes over it (the
+// second and third find most of it in L1 or L2), by vectors where all rows
+// start on 16-byte boundaries (V = kVec), else by elements (V = 1).
+template <typename X, int V>
+__device__ __forceinline__ void load_part(const X* p, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = to_f(*p);
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      v[i] = sizeof(X) == 4 ? __uint_as_float(w[i & 3]) : i & 1 ? bf16_hi(w[(i / 2) & 3]) : bf16_lo(w[(i / 2) & 3]);
+  }
+}
+template <typename X, int V>
+__device__ __forceinline__ void store_part(X* p, const float (&v)[V]) {
+  if constexpr (V == 1)
+    put(p, v[0]);
+  else if constexpr (sizeof(X) == 2)
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  else
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+template <typename X, int V>
 __global__ void __launch_bounds__(1024) norm_fwd_rows_kernel(const FwdArgs a) {
   __shared__ float sm[2][32];
   let_next_start();
@@ -462,22 +493,38 @@ __global__ void __launch_bounds__(1024) norm_fwd_rows_kernel(const FwdArgs a) {
   const int64_t row = blockIdx.x;
   const X* x = static_cast<const X*>(a.x) + row * a.ld_x;
   float s[1] = {0.f}, q[1] = {0.f};
-  for (int c = threadIdx.x; c < a.H; c += blockDim.x) s[0] += to_f(x[c]);
+#pragma unroll 8
+  for (int c = threadIdx.x * V; c < a.H; c += 1024 * V) {
+    float v[V];
+    load_part(x + c, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[0] += v[i];
+  }
   row_sums<1, 1024>(s, 0, sm[0]);
   const float mu = s[0] / (float)a.H;
-  for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
-    const float d = to_f(x[c]) - mu;
-    q[0] += d * d;
+#pragma unroll 8
+  for (int c = threadIdx.x * V; c < a.H; c += 1024 * V) {
+    float v[V];
+    load_part(x + c, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[0] += (v[i] - mu) * (v[i] - mu);
   }
   row_sums<1, 1024>(q, 0, sm[1]);
-  const float r = 1.f / sqrtf(q[0] / (float)a.H + a.eps);
+  const float r = inv_sqrt(q[0] / (float)a.H + a.eps);
   if (threadIdx.x == 0) {
     if (a.mean) a.mean[row] = mu;
     if (a.rstd) a.rstd[row] = r;
   }
   X* y = static_cast<X*>(a.y) + row * a.ld_y;
-  for (int c = threadIdx.x; c < a.H; c += blockDim.x)
-    put(y + c, (to_f(x[c]) - mu) * r * load_w1(a.gamma, a.wtype, c, 1.f) + load_w1(a.beta, a.wtype, c, 0.f));
+#pragma unroll 2
+  for (int c = threadIdx.x * V; c < a.H; c += 1024 * V) {
+    float v[V];
+    load_part(x + c, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      v[i] = (v[i] - mu) * r * load_w1(a.gamma, a.wtype, c + i, 1.f) + load_w1(a.beta, a.wtype, c + i, 0.f);
+    store_part(y + c, v);
+  }
 }
 
 // -------------------------------------------------------------- backward
@@ -497,7 +544,8 @@ struct BwdArgs {
 //   dx = r g + x A + B,  A = -r r mean(g h),  B = -r mean(g) - b r mean(g h).
 // (Three blocks per SM instead of two, with gamma in shared memory and the row
 // read from the ring a second time, measured no faster: 79 against 76 us.)
-template <typename X, bool SHIFT, int CPT, int L, int S>
+// GRADS: with the column sums of dgamma and dbeta.
+template <typename X, bool SHIFT, int CPT, int L, int S, bool GRADS>
 __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
     norm_bwd_kernel(const __grid_constant__ BwdArgs a) {
   constexpr int TH = kBlock<L>, ROWS = kRows<L>, V = kVec<X>;
@@ -552,7 +600,7 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
       const F2 gy = mul2(d[i], g[i]);
       s1 = add2(s1, gy);
       s2 = fma2(gy, h, s2);
-      if (live) {
+      if (GRADS && live) {
         dg[i] = fma2(d[i], h, dg[i]);
         db[i] = add2(db[i], d[i]);
       }
@@ -570,7 +618,7 @@ __global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
     dx += dx_step;
   }
   copy_wait<0>();
-  if (!a.partial) return;
+  if (!GRADS || !a.partial) return;
   // the block's column sums, through shared memory: groups of one block are
   // added in order, and the stores are coalesced
   float* out = a.partial + (size_t)blockIdx.x * 2 * a.H;
@@ -624,8 +672,8 @@ __global__ void __launch_bounds__(1024) norm_param_grad_kernel(const float* part
 }
 
 // Rows that the kernel above does not take: dx with a block per row (two
-// passes), the column sums from a second read with a thread per column.
-template <typename X>
+// passes); the column sums from a read of their own, a thread per column.
+template <typename X, int V>
 __global__ void __launch_bounds__(1024) norm_bwd_rows_kernel(const BwdArgs a) {
   __shared__ float sm[64];
   let_next_start();
@@ -635,21 +683,34 @@ __global__ void __launch_bounds__(1024) norm_bwd_rows_kernel(const BwdArgs a) {
   const X* dy = static_cast<const X*>(a.dy) + row * a.ld_dy;
   const float mu = a.mean[row], r = a.rstd[row];
   float s[2] = {0.f, 0.f};
-  for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
-    const float gy = to_f(dy[c]) * load_w1(a.gamma, a.wtype, c, 1.f);
-    s[0] += gy;
-    s[1] += gy * ((to_f(x[c]) - mu) * r);
+#pragma unroll 4
+  for (int c = threadIdx.x * V; c < a.H; c += 1024 * V) {
+    float d[V], v[V];
+    load_part(dy + c, d);
+    load_part(x + c, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float gy = d[i] * load_w1(a.gamma, a.wtype, c + i, 1.f);
+      s[0] += gy;
+      s[1] += gy * ((v[i] - mu) * r);
+    }
   }
   row_sums<2, 1024>(s, 0, sm);
   const float c1 = s[0] / (float)a.H, c2 = s[1] / (float)a.H;
   X* dx = static_cast<X*>(a.dx) + row * a.ld_dx;
-  for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
-    const float gy = to_f(dy[c]) * load_w1(a.gamma, a.wtype, c, 1.f);
-    put(dx + c, r * (gy - c1 - (to_f(x[c]) - mu) * r * c2));
+#pragma unroll 2
+  for (int c = threadIdx.x * V; c < a.H; c += 1024 * V) {
+    float d[V], v[V];
+    load_part(dy + c, d);
+    load_part(x + c, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      v[i] = r * (d[i] * load_w1(a.gamma, a.wtype, c + i, 1.f) - c1 - (v[i] - mu) * r * c2);
+    store_part(dx + c, v);
   }
 }
 
-// Before the rows kernel: dx may overwrite x or dy.
+// (Runs before the kernel of dx, which may overwrite x or dy.)
 template <typename X>
 __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const BwdArgs a) {
   let_next_start();
@@ -657,6 +718,7 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const BwdArgs a) {
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= a.H) return;
   float dg = 0.f, db = 0.f;
+#pragma unroll 8
   for (int64_t row = blockIdx.y; row < a.T; row += gridDim.y) {
     const float d = to_f(static_cast<const X*>(a.dy)[row * a.ld_dy + c]);
     const float x = to_f(static_cast<const X*>(a.x)[row * a.ld_x + c]);
@@ -670,17 +732,20 @@ __global__ void __launch_bounds__(256) norm_bwd_cols_kernel(const BwdArgs a) {
 
 // ------------------------------------------------------------------ host
 template <typename X>
+cudaError_t backward_cols(const BwdArgs& a, int64_t max_blocks, int* blocks, cudaStream_t s) {
+  if (!a.partial) return cudaSuccess;
+  int64_t slabs = 64;
+  if (slabs > a.T) slabs = a.T;
+  if (slabs > max_blocks) slabs = max_blocks;
+  *blocks = (int)slabs;
+  return launch_overlapped(norm_bwd_cols_kernel<X>, dim3((a.H + 255) / 256, (unsigned)slabs), 256, 0, s, a);
+}
+
+template <typename X, int V>
 cudaError_t backward_rows(const BwdArgs& a, int64_t max_blocks, int* blocks, cudaStream_t s) {
-  if (a.partial) {
-    int64_t slabs = 64;
-    if (slabs > a.T) slabs = a.T;
-    if (slabs > max_blocks) slabs = max_blocks;
-    *blocks = (int)slabs;
-    const cudaError_t e = launch_overlapped(norm_bwd_cols_kernel<X>, dim3((a.H + 255) / 256, (unsigned)slabs),
-                                            256, 0, s, a);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_overlapped(norm_bwd_rows_kernel<X>, (unsigned)a.T, 1024, 0, s, a);
+  const cudaError_t e = backward_cols<X>(a, max_blocks, blocks, s);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(norm_bwd_rows_kernel<X, V>, (unsigned)a.T, 1024, 0, s, a);
 }
 
 // Where the rows of a call's tensors start relative to 16-byte boundaries.
@@ -738,19 +803,19 @@ cudaError_t run_fwd(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
              INT64_MAX, &blocks, s);
 }
 
-template <typename X, bool SHIFT, int CPT, int L, int S>
+template <typename X, bool SHIFT, int CPT, int L, int S, bool GRADS = true>
 cudaError_t run_bwd(const BwdArgs& a, const Offsets& o, int64_t max_blocks, int* blocks, cudaStream_t s) {
   static CtxCache<int> cache;
   constexpr int TH = kBlock<L>;
   constexpr int kRing = 2 * Stream<X, CPT, L, SHIFT, S, TH>::RING + (CPT > 16 ? CPT * 4 * TH : 0);
   constexpr int kSums = kRows<L> * 2 * L * CPT * 4;    // H <= L CPT
-  return run(norm_bwd_kernel<X, SHIFT, CPT, L, S>, cache, a, kRows<L>, TH, kRing > kSums ? kRing : kSums,
+  return run(norm_bwd_kernel<X, SHIFT, CPT, L, S, GRADS>, cache, a, kRows<L>, TH, kRing > kSums ? kRing : kSums,
              SHIFT ? o.period : 1, max_blocks, blocks, s);
 }
 
 // The fewest lanes that hold a row (with SHIFT, one from any place in its
 // first vector) at 16 columns each, 8 in short rows; 512 lanes of 32 columns
-// for aligned rows over 8192.
+// for rows over 8192.
 template <typename X, bool SHIFT>
 cudaError_t forward(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
   const int n = SHIFT ? a.H + kVec<X> - 1 : a.H;
@@ -764,12 +829,11 @@ cudaError_t forward(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
   if (n <= 4096) return run_fwd<X, SHIFT, 16, 256, 4>(a, o, s);
   if (n <= 5632) return run_fwd<X, SHIFT, 16, 352, 3>(a, o, s);
   if (n <= 8192) return run_fwd<X, SHIFT, 16, 512, 3>(a, o, s);
-  if constexpr (!SHIFT)
-    if (n <= 16384) return run_fwd<X, SHIFT, 32, 512, sizeof(X) == 2 ? 2 : 1>(a, o, s);
-  return launch_overlapped(norm_fwd_rows_kernel<X>, (unsigned)a.T, 1024, 0, s, a);
+  if (n <= 16384) return run_fwd<X, SHIFT, 32, 512, sizeof(X) == 2 ? 2 : 1>(a, o, s);
+  return launch_overlapped(norm_fwd_rows_kernel<X, SHIFT ? 1 : kVec<X>>, (unsigned)a.T, 1024, 0, s, a);
 }
 
-// As the forward; fp32 rows over 8192 would not fit the ring with two tensors.
+// As the forward.
 template <typename X, bool SHIFT>
 cudaError_t backward(const BwdArgs& a, const Offsets& o, int64_t max_blocks, int* blocks, cudaStream_t s) {
   constexpr bool B = sizeof(X) == 2;
@@ -785,23 +849,31 @@ cudaError_t backward(const BwdArgs& a, const Offsets& o, int64_t max_blocks, int
   if (n <= 4096) return run_bwd<X, SHIFT, 16, 256, S>(a, o, max_blocks, blocks, s);
   if (n <= 5632) return run_bwd<X, SHIFT, 16, 352, 3>(a, o, max_blocks, blocks, s);
   if (n <= 8192) return run_bwd<X, SHIFT, 16, 512, 3>(a, o, max_blocks, blocks, s);
-  if constexpr (B && !SHIFT)
-    if (n <= 16384) return run_bwd<X, SHIFT, 32, 512, 2>(a, o, max_blocks, blocks, s);
-  return backward_rows<X>(a, max_blocks, blocks, s);
+  if (n <= 16384) {
+    if constexpr (B) {
+      return run_bwd<X, SHIFT, 32, 512, 2>(a, o, max_blocks, blocks, s);
+    } else {   // the ring holds one row of both tensors, and the registers no sums
+      const cudaError_t e = backward_cols<X>(a, max_blocks, blocks, s);
+      if (e != cudaSuccess) return e;
+      int unused;
+      return run_bwd<X, SHIFT, 32, 512, 1, false>(a, o, INT64_MAX, &unused, s);
+    }
+  }
+  return backward_rows<X, SHIFT ? 1 : kVec<X>>(a, max_blocks, blocks, s);
 }
 
 template <typename X>
 cudaError_t forward_any(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
   if (o.vectors) return forward<X, false>(a, o, s);
   if (o.same) return forward<X, true>(a, o, s);
-  return launch_overlapped(norm_fwd_rows_kernel<X>, (unsigned)a.T, 1024, 0, s, a);
+  return launch_overlapped(norm_fwd_rows_kernel<X, 1>, (unsigned)a.T, 1024, 0, s, a);
 }
 
 template <typename X>
 cudaError_t backward_any(const BwdArgs& a, const Offsets& o, int64_t max_blocks, int* blocks, cudaStream_t s) {
   if (o.vectors) return backward<X, false>(a, o, max_blocks, blocks, s);
   if (o.same) return backward<X, true>(a, o, max_blocks, blocks, s);
-  return backward_rows<X>(a, max_blocks, blocks, s);
+  return backward_rows<X, 1>(a, max_blocks, blocks, s);
 }
 
 }  // namespace

@@ -90,7 +90,7 @@ def _make(T, H, dtype, wdtype, pad=0, off=0, seed=0):
 # fused kernels and the long rows past them; odd widths take the element-wise form
 SHAPES = [(1, 1), (1, 4096), (3, 7), (5, 8), (33, 64), (129, 96), (1000, 256), (257, 264), (700, 513), (311, 1000),
           (400, 2049), (640, 4096), (97, 4104), (70, 5001), (65, 8192), (40, 8200), (33, 16384), (9, 16392), (5, 20001),
-          (3, 40000)]
+          (3, 40000), (200, 9001), (31, 12004), (17, 16377)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
