@@ -62,8 +62,9 @@ struct XJob {
 };
 
 struct XParams {
-  XJob job[3];
+  XJob job[2];
   int njob;
+  int catch_up;          // tiles of job 1 that weigh as much as one of job 0
   int T, H, V;
   // targets and statistics
   const void* targets;
@@ -99,15 +100,47 @@ __device__ __forceinline__ int target_of(const void* targets, int index64, int i
   return t >= 0 && t < V ? (int)t : -2;
 }
 
+// The tiles of one SM pair, in the order that all of its roles follow.  The
+// first job's tiles go round the pairs; where its last round leaves some pairs
+// without a tile, those first take as many of the second job's tiles as weigh
+// as much (`catch_up`), and the rest goes round all pairs, theirs first.
+// (Against going round regardless: 1% of the whole step at T = 8192, H = 4096,
+// V = 131072, 2% at T = 4096, H = 2048, V = 50001.)
+struct Schedule {
+  int pair, pairs, n0, n1, own0, short_from, shared, catch_up;
+  __device__ __forceinline__ Schedule(const XParams& P) {
+    pair = blockIdx.x / 2;
+    pairs = gridDim.x / 2;
+    n0 = P.job[0].mt * P.job[0].nt * P.job[0].ks;
+    n1 = P.njob > 1 ? P.job[1].mt * P.job[1].nt * P.job[1].ks : 0;
+    own0 = pair < n0 ? (n0 - 1 - pair) / pairs + 1 : 0;
+    short_from = n0 % pairs;               // pairs from here on have a tile less (0: none has)
+    shared = short_from ? P.catch_up * (pairs - short_from) : 0;
+    catch_up = pair >= short_from && short_from ? P.catch_up : 0;
+  }
+  // The k-th tile: its number over both jobs, or -1 past the last.
+  __device__ __forceinline__ int tile(int k) const {
+    if (k < own0) return pair + k * pairs;
+    k -= own0;
+    int i;
+    if (k < catch_up) {
+      i = k * (pairs - short_from) + pair - short_from;
+    } else {
+      i = pair - short_from;
+      i = shared + (i < 0 ? i + pairs : i) + (k - catch_up) * pairs;
+    }
+    return i < n1 ? n0 + i : -1;
+  }
+};
+
 struct XTile {
   int p, kind, m0, n0, ntile, slice, kb0, kb1;
 };
 
-__device__ __forceinline__ XTile decode(const XParams& P, const int (&cum)[4], int t, int rank) {
-  int p = 0;
-  while (p + 1 < P.njob && t >= cum[p + 1]) ++p;
+__device__ __forceinline__ XTile decode(const XParams& P, const Schedule& sc, int t, int rank) {
+  const int p = t >= sc.n0;
   const XJob& g = P.job[p];
-  int lt = t - cum[p];
+  int lt = t - (p ? sc.n0 : 0);
   XTile ti;
   ti.p = p;
   ti.kind = g.kind;
@@ -126,13 +159,12 @@ __device__ __forceinline__ XTile decode(const XParams& P, const int (&cum)[4], i
 
 // Loads A (part 0, which also arms the leader's full barrier) or B (part 1)
 // of every stage: this CTA's 128 rows of A and its half of the tile's B columns.
-__device__ void load_role(const XParams& P, const int (&cum)[4], int rank, uint8_t* stages,
+__device__ void load_role(const XParams& P, const Schedule& sc, int rank, uint8_t* stages,
                           uint64_t* full, uint64_t* empty, const WaitCtl& wc, int part) {
   int it = 0;
-  const int cl = blockIdx.x / 2, ncl = gridDim.x / 2;
   bool ok = true;
-  for (int t = cl; ok && t < cum[P.njob]; t += ncl) {
-    const XTile ti = decode(P, cum, t, rank);
+  for (int k = 0, t; ok && (t = sc.tile(k)) >= 0; ++k) {
+    const XTile ti = decode(P, sc, t, rank);
     const XJob& g = P.job[ti.p];
     const int n0 = ti.n0 + rank * (g.tn / 2) + g.b_n0;
     const uint32_t bytes = 2 * (kABytes + g.tn * 64);   // both CTAs' A rows and halves of B
@@ -172,16 +204,15 @@ __device__ void load_role(const XParams& P, const int (&cum)[4], int rank, uint8
 }
 
 // One thread of the leader CTA issues every MMA of the pair.
-__device__ void mma_role(const XParams& P, const int (&cum)[4], uint8_t* stages, uint64_t* full,
+__device__ void mma_role(const XParams& P, const Schedule& sc, uint8_t* stages, uint64_t* full,
                          uint64_t* empty, uint64_t* tfull, uint64_t* tempty, uint64_t* drain,
                          uint32_t tmem_base, const WaitCtl& wc) {
   int acc = 0, s = 0;
   uint32_t ph = 0, soff = 0;
   const uint32_t sbase = smem_u32(stages);
-  const int cl = blockIdx.x / 2, ncl = gridDim.x / 2;
   bool ok = true;
-  for (int t = cl; ok && t < cum[P.njob]; t += ncl, ++acc) {
-    const XTile ti = decode(P, cum, t, 0);
+  for (int t; ok && (t = sc.tile(acc)) >= 0; ++acc) {
+    const XTile ti = decode(P, sc, t, 0);
     const XJob& g = P.job[ti.p];
     const int buf = acc & 1;
     if (!wait_bar_cluster(&tempty[buf], ((acc >> 1) & 1) ^ 1, wc)) break;
@@ -227,13 +258,12 @@ __device__ __forceinline__ float common_scale(const float* dloss, const float* t
 }
 
 template <bool BWD>
-__device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, uint64_t* tfull,
+__device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, uint64_t* tfull,
                               uint64_t* tempty, uint32_t tmem_base, uint8_t* stg, const WaitCtl& wc) {
   const int ew = (threadIdx.x >> 5) - 2;
   const int q = (threadIdx.x >> 5) & 3;          // TMEM lane quarter of this warp
   const int half = ew >> 2;                      // which half of the tile's columns
   const int lane = threadIdx.x & 31;
-  const int cl = blockIdx.x / 2, ncl = gridDim.x / 2;
   uint8_t* sb0 = stg + ew * 4096;
   uint8_t* sb1 = sb0 + 2048;
   const uint32_t te0 = mapa_shared(smem_u32(&tempty[0]), 0);
@@ -261,8 +291,8 @@ __device__ void epilogue_role(const XParams& P, const int (&cum)[4], int rank, u
   };
   const float gs = BWD ? common_scale(P.dloss, P.total, P.reduction) : 1.f;
   int acc = 0;
-  for (int t = cl; t < cum[P.njob]; t += ncl, ++acc) {
-    const XTile ti = decode(P, cum, t, rank);
+  for (int t; (t = sc.tile(acc)) >= 0; ++acc) {
+    const XTile ti = decode(P, sc, t, rank);
     const XJob& g = P.job[ti.p];
     const int buf = acc & 1;
     const int y0 = ti.m0 + q * 32;               // first row of this warp
@@ -461,22 +491,19 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
   wait_for_previous();
   if (!BWD && blockIdx.x == 0 && threadIdx.x == 0) *P.ticket = 0;   // of the join kernel
   const uint32_t tmem_base = *tmem_holder;
-  int cum[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int p = 0; p < 3; ++p)
-    cum[p + 1] = cum[p] + (p < P.njob ? P.job[p].mt * P.job[p].nt * P.job[p].ks : 0);
+  const Schedule sc(P);
   const WaitCtl wc{abort_flag, P.status, P.wait_ns};
   if (warp == 0) {
-    if ((threadIdx.x & 31) == 0) load_role(P, cum, rank, stages, full, empty, wc, 0);
+    if ((threadIdx.x & 31) == 0) load_role(P, sc, rank, stages, full, empty, wc, 0);
     __syncwarp();
   } else if (warp == 1) {
     if ((threadIdx.x & 31) == 0 && rank == 0)
-      mma_role(P, cum, stages, full, empty, tfull, tempty, drain, tmem_base, wc);
+      mma_role(P, sc, stages, full, empty, tfull, tempty, drain, tmem_base, wc);
     __syncwarp();
   } else if (warp < 2 + kEpiWarps) {
-    epilogue_role<BWD>(P, cum, rank, tfull, tempty, tmem_base, stg, wc);
+    epilogue_role<BWD>(P, sc, rank, tfull, tempty, tmem_base, stg, wc);
   } else {
-    if ((threadIdx.x & 31) == 0) load_role(P, cum, rank, stages, full, empty, wc, 1);
+    if ((threadIdx.x & 31) == 0) load_role(P, sc, rank, stages, full, empty, wc, 1);
     __syncwarp();
   }
   tc_fence_before();
@@ -1040,6 +1067,10 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
     if (!ok) {
       *st = MOE_ERR_CUDA;
       return cudaSuccess;
+    }
+    if (Q.njob == 2) {
+      const int w0 = up(Q.job[0].kblocks, Q.job[0].ks), w1 = Q.job[1].kblocks;
+      Q.catch_up = (w0 + w1 / 2) / w1;
     }
     XENT_TRY(launch<true>(Q, s));
   }
