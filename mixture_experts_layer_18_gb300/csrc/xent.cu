@@ -22,6 +22,13 @@
 // issues the MMAs, warps 2..9 are the epilogue (two per TMEM lane quarter,
 // 128 columns each: an exponential per logit is too much for four warps),
 // warp 10 loads B.  Every wait is bounded, as there.
+//
+// Measured (GB300): forward at T = 16384, H = 2048, V = 65536 2.3 ms cold and
+// 2.5 ms under the power cap (1.9 and 1.73 PFLOP/s); forward and backward at T
+// = 8192, H = 4096, V = 131072 21.0 ms (1.68 PFLOP/s of the 8 T V H products,
+// the cap's rate for plain bf16 products); tensor pipe 86 - 90% busy.  Pieces
+// of 256 MB of dz: 64 MB are 8% slower (more adds to dX), 512 MB 1% faster.
+// Sweeps of 8 m-tiles over n: 4, 16 and 32 are 1 - 2% slower.
 #include <cstring>
 
 #include "common.cuh"
