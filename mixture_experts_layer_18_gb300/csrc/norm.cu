@@ -357,10 +357,18 @@ struct Stream {
   }
 };
 
-template <int L>
-constexpr int kRows = L > 128 ? 1 : 256 / L;      // rows of a block
-template <int L>
-constexpr int kBlock = kRows<L>* L;
+// Rows that a block of about N threads works on side by side, and its threads.
+template <int L, int N>
+constexpr int kRows = L > N / 2 ? 1 : N / L;
+template <int L, int N>
+constexpr int kBlock = kRows<L, N>* L;
+// The backward of bf16 rows has larger blocks: their column sums are joined in
+// shared memory before they go to memory (16384 x 4096: 2 us less; fp32 rows
+// fill the ring with fewer in flight: 5003 x 1536 takes 17.0 us so, 15.3 with
+// 256 threads).
+constexpr int kFwdThreads = 256;
+template <typename X>
+constexpr int kBwdThreads = sizeof(X) == 2 ? 512 : 256;
 
 // --------------------------------------------------------------- forward
 struct FwdArgs {
@@ -376,9 +384,9 @@ struct FwdArgs {
 };
 
 template <typename X, bool SHIFT, int CPT, int L, int S>
-__global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 800 / kBlock<L> : 1)
+__global__ void __launch_bounds__(kBlock<L, kFwdThreads>, CPT <= 16 ? 800 / kBlock<L, kFwdThreads> : 1)
     norm_fwd_kernel(const __grid_constant__ FwdArgs a) {
-  constexpr int TH = kBlock<L>, ROWS = kRows<L>, V = kVec<X>;
+  constexpr int TH = kBlock<L, kFwdThreads>, ROWS = kRows<L, kFwdThreads>, V = kVec<X>;
   using Str = Stream<X, CPT, L, SHIFT, S, TH>;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ float sm[2][TH / 32];
@@ -546,9 +554,9 @@ struct BwdArgs {
 // read from the ring a second time, measured no faster: 79 against 76 us.)
 // GRADS: with the column sums of dgamma and dbeta.
 template <typename X, bool SHIFT, int CPT, int L, int S, bool GRADS>
-__global__ void __launch_bounds__(kBlock<L>, CPT <= 16 ? 512 / kBlock<L> : 1)
+__global__ void __launch_bounds__(kBlock<L, kBwdThreads<X>>, CPT <= 16 ? 512 / kBlock<L, kBwdThreads<X>> : 1)
     norm_bwd_kernel(const __grid_constant__ BwdArgs a) {
-  constexpr int TH = kBlock<L>, ROWS = kRows<L>, V = kVec<X>;
+  constexpr int TH = kBlock<L, kBwdThreads<X>>, ROWS = kRows<L, kBwdThreads<X>>, V = kVec<X>;
   using Str = Stream<X, CPT, L, SHIFT, S, TH>;
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ float sm[2][TH / 16];
@@ -796,20 +804,20 @@ cudaError_t run(K kern, CtxCache<int>& cache, const Args& a, int rows, int threa
 template <typename X, bool SHIFT, int CPT, int L, int S>
 cudaError_t run_fwd(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
   static CtxCache<int> cache;
-  constexpr int TH = kBlock<L>;
+  constexpr int TH = kBlock<L, kFwdThreads>;
   constexpr int kBytes = Stream<X, CPT, L, SHIFT, S, TH>::RING + (CPT > 16 ? 2 * CPT * 4 * TH : 0);
   int blocks;
-  return run(norm_fwd_kernel<X, SHIFT, CPT, L, S>, cache, a, kRows<L>, TH, kBytes, SHIFT ? o.period : 1,
+  return run(norm_fwd_kernel<X, SHIFT, CPT, L, S>, cache, a, kRows<L, kFwdThreads>, TH, kBytes, SHIFT ? o.period : 1,
              INT64_MAX, &blocks, s);
 }
 
 template <typename X, bool SHIFT, int CPT, int L, int S, bool GRADS = true>
 cudaError_t run_bwd(const BwdArgs& a, const Offsets& o, int64_t max_blocks, int* blocks, cudaStream_t s) {
   static CtxCache<int> cache;
-  constexpr int TH = kBlock<L>;
+  constexpr int TH = kBlock<L, kBwdThreads<X>>;
   constexpr int kRing = 2 * Stream<X, CPT, L, SHIFT, S, TH>::RING + (CPT > 16 ? CPT * 4 * TH : 0);
-  constexpr int kSums = kRows<L> * 2 * L * CPT * 4;    // H <= L CPT
-  return run(norm_bwd_kernel<X, SHIFT, CPT, L, S, GRADS>, cache, a, kRows<L>, TH, kRing > kSums ? kRing : kSums,
+  constexpr int kSums = kRows<L, kBwdThreads<X>> * 2 * L * CPT * 4;    // H <= L CPT
+  return run(norm_bwd_kernel<X, SHIFT, CPT, L, S, GRADS>, cache, a, kRows<L, kBwdThreads<X>>, TH, kRing > kSums ? kRing : kSums,
              SHIFT ? o.period : 1, max_blocks, blocks, s);
 }
 
