@@ -18,16 +18,26 @@
 // GEMM structure (as the expert engine in gemm.cu): persistent SM pairs
 // (clusters of two CTAs, cta_group::2 tcgen05 MMAs of 256 x 256 x 16), TMA
 // loads into a ring of 64-element K stages, two TMEM accumulators so that one
-// tile's epilogue runs under the next tile's MMAs.  Warp 0 loads A, warp 1
-// issues the MMAs, warps 2..9 are the epilogue (two per TMEM lane quarter,
-// 128 columns each: an exponential per logit is too much for four warps),
-// warp 10 loads B.  Every wait is bounded, as there.
+// tile's epilogue runs under the next tile's MMAs.  An accumulator truncates
+// what it adds, towards 0: over 4096 columns of K the log sum came out 2e-5 too
+// small on average, over 512 2.4e-6, which is what rounded fp32 sums lose.  The
+// forward therefore adds its logits up in fp32 registers from segments of up to
+// 512 columns, one accumulator each.  (T = 2000, H = 4096, V = 32768: the losses
+// are 2e-7 off their 64-bit values, 4e-7 with segments of 1024 columns, 2e-6 with
+// whole tiles.  It costs 6% of the forward at T = 16384, H = 2048, V = 65536 and
+// 1% of a training step; segments of 1024 half that; of 256 20%, since an
+// epilogue then takes longer than a segment.)  The backward's exponentials are
+// rounded to bf16 and keep whole tiles.
 //
-// Measured (GB300): forward at T = 16384, H = 2048, V = 65536 2.3 ms cold and
-// 2.5 ms under the power cap (1.9 and 1.73 PFLOP/s); forward and backward at T
-// = 8192, H = 4096, V = 131072 21.0 ms (1.68 PFLOP/s of the 8 T V H products,
-// the cap's rate for plain bf16 products); tensor pipe 86 - 90% busy.  Pieces
-// of 256 MB of dz: 64 MB are 8% slower (more adds to dX), 512 MB 1% faster.
+// Warp 0 loads A, warp 1 issues the MMAs, warps 2..9 are the epilogue (two per
+// TMEM lane quarter, 128 columns each: an exponential per logit is too much for
+// four warps), warp 10 loads B.  Every wait is bounded, as there.
+//
+// Measured (GB300): forward at T = 16384, H = 2048, V = 65536 2.8 ms (1.57
+// PFLOP/s); forward and backward at T = 8192, H = 4096, V = 131072 21.8 ms (1.61
+// PFLOP/s of the 8 T V H products; a library's plain bf16 products sustain 1.70
+// under the power cap); tensor pipe 86 - 90% busy in the backward.  Pieces of
+// 256 MB of dz: 64 MB are 8% slower (more adds to dX), 512 MB 1% faster.
 // Sweeps of 8 m-tiles over n: 4, 16 and 32 are 1 - 2% slower.
 #include <cstring>
 
@@ -48,6 +58,7 @@ constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
 constexpr int kStgBytes = kEpiWarps * 4096;     // two 32 x 32 bf16 boxes per epilogue warp
 constexpr int kSmemBytes = kStages * kStageBytes + kStgBytes + 1024 + 256;
 constexpr int kTile = 256;
+constexpr int kSegment = 8;                     // most K blocks that the forward adds up in one accumulator
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFewTokens = 16;                  // most tokens of the kernel for few tokens
 constexpr int kFewMaxBlocks = 512;
@@ -80,9 +91,10 @@ struct XParams {
   const float* dloss;
   const float* total;    // {sum, mean, count}
   int reduction;
+  int segment;           // STATS: K blocks per accumulator
   // outputs
   float2* part;          // STATS: [2 nt][T] {max, sum} in the log2 domain
-  float* zt;             // STATS: [T] target logits
+  float* zt;             // STATS: [T] target logits times log2(e)
   unsigned* ticket;      // STATS: zeroed for the join kernel
   float* acc;            // DX: fp32 sums [ks][T][Hp]
   int zcols;             // DZ: columns of the dz buffer
@@ -210,7 +222,9 @@ __device__ void load_role(const XParams& P, const Schedule& sc, int rank, uint8_
   }
 }
 
-// One thread of the leader CTA issues every MMA of the pair.
+// One thread of the leader CTA issues every MMA of the pair.  A tile goes
+// through one accumulator, or (forward) one after another per segment of K.
+template <bool BWD>
 __device__ void mma_role(const XParams& P, const Schedule& sc, uint8_t* stages, uint64_t* full,
                          uint64_t* empty, uint64_t* tfull, uint64_t* tempty, uint64_t* drain,
                          uint32_t tmem_base, const WaitCtl& wc) {
@@ -218,13 +232,9 @@ __device__ void mma_role(const XParams& P, const Schedule& sc, uint8_t* stages, 
   uint32_t ph = 0, soff = 0;
   const uint32_t sbase = smem_u32(stages);
   bool ok = true;
-  for (int t; ok && (t = sc.tile(acc)) >= 0; ++acc) {
+  for (int k = 0, t; ok && (t = sc.tile(k)) >= 0; ++k) {
     const XTile ti = decode(P, sc, t, 0);
     const XJob& g = P.job[ti.p];
-    const int buf = acc & 1;
-    if (!wait_bar_cluster(&tempty[buf], ((acc >> 1) & 1) ^ 1, wc)) break;
-    tc_fence_after();
-    const uint32_t d = tmem_base + buf * kTile;
     const uint32_t a_mn = g.a_mn ? 1u : 0u, b_mn = g.b_mn ? 1u : 0u;
     // D fp32, A and B bf16, their majors, N, M = 256
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) |
@@ -233,21 +243,30 @@ __device__ void mma_role(const XParams& P, const Schedule& sc, uint8_t* stages, 
     const uint64_t b0 = smem_desc_sw128(sbase + kABytes, b_mn ? kAtomBytes : 16, 1024);
     // an MMA's K step: 16 rows of an MN-major block, or 32 bytes of a row
     const uint32_t ak = a_mn ? (16 * 128) >> 4 : 2, bk = b_mn ? (16 * 128) >> 4 : 2;
-    for (int kb = ti.kb0; kb < ti.kb1; ++kb) {
-      if (!wait_bar_cluster(&full[s], ph, wc)) { ok = false; break; }
+    for (int kb = ti.kb0; kb < ti.kb1;) {
+      const int buf = acc & 1;
+      if (!wait_bar_cluster(&tempty[buf], ((acc >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t d = tmem_base + buf * kTile;
+      const int first = kb, end = BWD ? ti.kb1 : min(kb + P.segment, ti.kb1);
+      for (; kb < end; ++kb) {
+        if (!wait_bar_cluster(&full[s], ph, wc)) { ok = false; break; }
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_f16_pair(d, a0 + soff + kk * ak, b0 + soff + kk * bk, idesc, kb != ti.kb0 || kk != 0);
-      tc_commit_pair(&empty[s], 3);
-      if (++s == kStages) {
-        s = 0;
-        ph ^= 1;
-        soff = 0;
-      } else {
-        soff += kStageBytes >> 4;
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16_pair(d, a0 + soff + kk * ak, b0 + soff + kk * bk, idesc, kb != first || kk != 0);
+        tc_commit_pair(&empty[s], 3);
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1;
+          soff = 0;
+        } else {
+          soff += kStageBytes >> 4;
+        }
       }
+      if (!ok) break;
+      tc_commit_pair(&tfull[buf], 3);
+      ++acc;
     }
-    if (ok) tc_commit_pair(&tfull[buf], 3);
   }
   tc_commit_pair(drain, 1);
   wait_bar_drain(drain, 0, wc.limit_ns);
@@ -262,6 +281,23 @@ __device__ __forceinline__ float common_scale(const float* dloss, const float* t
   if (reduction == MOE_REDUCE_NONE) return 1.f;
   if (reduction == MOE_REDUCE_SUM) return dloss[0];
   return dloss[0] / fmaxf(total[2], 1.f);   // total[2]: rows that count
+}
+
+// Load 16 consecutive fp32 columns of the warp's 32 TMEM lanes (half of
+// tmem_ld32, where a row's 128 sums leave few registers).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 template <bool BWD>
@@ -297,11 +333,23 @@ __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, ui
     else if (lane == 0) bulk_commit();
   };
   const float gs = BWD ? common_scale(P.dloss, P.total, P.reduction) : 1.f;
-  int acc = 0;
-  for (int t; (t = sc.tile(acc)) >= 0; ++acc) {
+  int acc = 0;                                   // accumulators taken so far
+  // waits for the next accumulator, and gives it back
+  auto take = [&]() {
+    const bool got = wait_bar_cluster(&tfull[acc & 1], (acc >> 1) & 1, wc);
+    if (!__all_sync(0xffffffffu, got)) return false;
+    tc_fence_after();
+    return true;
+  };
+  auto give = [&]() {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(acc & 1 ? te1 : te0);
+    ++acc;
+  };
+  for (int k = 0, t; (t = sc.tile(k)) >= 0; ++k) {
     const XTile ti = decode(P, sc, t, rank);
     const XJob& g = P.job[ti.p];
-    const int buf = acc & 1;
     const int y0 = ti.m0 + q * 32;               // first row of this warp
     const int row = y0 + lane;
     const int cw = g.tn / 2, c0 = half * cw;     // this warp's columns
@@ -317,45 +365,61 @@ __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, ui
         scale = P.reduction == MOE_REDUCE_NONE ? P.dloss[row] : 1.f;
       }
     }
-    const bool got = wait_bar_cluster(&tfull[buf], (acc >> 1) & 1, wc);
-    if (!__all_sync(0xffffffffu, got)) break;
-    tc_fence_after();
-    const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + buf * kTile + c0;
-    if (!BWD) {
+    const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16) + c0;
+    if constexpr (!BWD) {
       const int v0 = ti.n0 + c0;                 // first vocabulary entry of this warp
-      float m = -INFINITY, s = 0.f;
-#pragma unroll 1
-      for (int c = 0; c < cw; c += 32) {
-        float v[32];
-        tmem_ld32(taddr + c, v);
-        if (v0 + c + 32 > P.V) {
+      float z[4][32] = {};                       // the row's logits (cw of them)
+      bool got = true;
+      for (int kb = ti.kb0; kb < ti.kb1; kb += P.segment) {
+        got = take();
+        if (!got) break;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (16 * c >= cw) continue;
+          float v[16];
+          tmem_ld16(lanes + (acc & 1) * kTile + 16 * c, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[c >> 1][16 * (c & 1) + i] += v[i];
+        }
+        give();
+      }
+      if (!got) break;
+      float m = -INFINITY, s = 0.f;              // of the logits times log2(e)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (32 * c >= cw) continue;
+        if (v0 + 32 * c + 32 > P.V) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (v0 + c + i >= P.V) v[i] = -INFINITY;
+            if (v0 + 32 * c + i >= P.V) z[c][i] = -INFINITY;
         }
-        const int rel = tgt - (v0 + c);
+        const int rel = tgt - (v0 + 32 * c);
         if (__any_sync(0xffffffffu, tgt >= 0 && rel >= 0 && rel < 32)) {
-          float z = 0.f;
+          float zt = 0.f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z = rel == i ? v[i] : z;
-          if (tgt >= 0 && rel >= 0 && rel < 32) P.zt[row] = z;
+          for (int i = 0; i < 32; ++i) zt = rel == i ? z[c][i] : zt;
+          if (tgt >= 0 && rel >= 0 && rel < 32) P.zt[row] = zt * kLog2e;
         }
-        float cm = v[0];
+        float cm = z[c][0];
 #pragma unroll
-        for (int i = 1; i < 32; ++i) cm = fmaxf(cm, v[i]);
+        for (int i = 1; i < 32; ++i) cm = fmaxf(cm, z[c][i]);
         const float mn = fmaxf(m, cm * kLog2e);
         const float ref = mn == -INFINITY ? 0.f : mn;   // nothing finite so far: every term is 0
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          a += ex2(fmaf(v[i], kLog2e, -ref));
-          b += ex2(fmaf(v[i + 1], kLog2e, -ref));
+          a += ex2(fmaf(z[c][i], kLog2e, -ref));
+          b += ex2(fmaf(z[c][i + 1], kLog2e, -ref));
         }
         s = s * ex2(m - ref) + (a + b);
         m = mn;
       }
       if (live) P.part[(size_t)(2 * ti.ntile + half) * P.T + row] = make_float2(m, s);
-    } else if (ti.kind == XK_DZ) {
+      continue;
+    }
+    if (!take()) break;
+    const uint32_t taddr = lanes + (acc & 1) * kTile;
+    if (ti.kind == XK_DZ) {
       const int v0 = g.b_n0 + ti.n0 + c0;
 #pragma unroll 1
       for (int c = 0; c < cw; c += 64) {         // (96 columns: the second box of the last turn is left out)
@@ -448,9 +512,7 @@ __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, ui
         if (g.out_m0 + y0 < P.V) store_boxes(&g.tmO, a, b, ti.n0 + c0 + c, g.out_m0 + y0, P.H);
       }
     }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(buf ? te1 : te0);
+    give();
   }
   if (lane == 0) bulk_wait_all();
   __syncwarp();
@@ -505,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
     __syncwarp();
   } else if (warp == 1) {
     if ((threadIdx.x & 31) == 0 && rank == 0)
-      mma_role(P, sc, stages, full, empty, tfull, tempty, drain, tmem_base, wc);
+      mma_role<BWD>(P, sc, stages, full, empty, tfull, tempty, drain, tmem_base, wc);
     __syncwarp();
   } else if (warp < 2 + kEpiWarps) {
     epilogue_role<BWD>(P, sc, rank, tfull, tempty, tmem_base, stg, wc);
@@ -596,10 +658,12 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int
     double mine_loss = 0.0;
     int counts = 0;
     if (r < T) {
-      const float l = (m + log2f(s)) * 0.6931471805599453f;
+      // (the loss from differences of logits, not of lse: a small one keeps its digits)
+      constexpr float kLn2 = 0.6931471805599453f;
+      const float lg = log2f(s), l = (m + lg) * kLn2;
       if (t == -2) report(status, MOE_ERR_BAD_INDEX);
       counts = t >= 0;
-      const float v = counts ? l - z : 0.f;
+      const float v = counts ? ((m - z) + lg) * kLn2 : 0.f;
       lse[r] = l;
       loss[r] = v;
       mine_loss = v;
@@ -722,7 +786,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewPerSm) xent_few_kernel(con
     const int r0 = task * 16 + g, r1 = r0 + 8;
     const __nv_bfloat16* p0 = a.W + (int64_t)r0 * a.ld_w + t * 8;
     const __nv_bfloat16* p1 = a.W + (int64_t)r1 * a.ld_w + t * 8;
-    float c[NB][4] = {};
+    float c[NB][4] = {}, z[NB][4] = {};
     uint4 u0[kFewAhead], u1[kFewAhead];
     auto load = [&](int q, uint4& x, uint4& y) {
       const bool in = q * 32 + t * 8 < a.H;
@@ -745,16 +809,24 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewPerSm) xent_few_kernel(con
           }
         }
       }
+      // segments of 256 columns, for the reason given at the top (here they cost nothing)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[b][i] += c[b][i];
+          c[b][i] = 0.f;
+        }
     }
-    // c[b][0], c[b][1]: row r0, tokens 8 b + 2 t, + 1;  c[b][2], c[b][3]: row r1
+    // z[b][0], z[b][1]: row r0, tokens 8 b + 2 t, + 1;  z[b][2], z[b][3]: row r1
 #pragma unroll
     for (int j = 0; j < 2 * NB; ++j) {
-      const float z0 = c[j >> 1][j & 1], z1 = c[j >> 1][2 + (j & 1)];
+      const float z0 = z[j >> 1][j & 1] * kLog2e, z1 = z[j >> 1][2 + (j & 1)] * kLog2e;
       const int n = (j >> 1) * 8 + 2 * t + (j & 1);
       if (tgt[j] >= 0 && tgt[j] == r0) a.zt[n] = z0;
       if (tgt[j] >= 0 && tgt[j] == r1) a.zt[n] = z1;
-      if (r0 < a.V) join(m[j], s[j], z0 * kLog2e, 1.f);
-      if (r1 < a.V) join(m[j], s[j], z1 * kLog2e, 1.f);
+      if (r0 < a.V) join(m[j], s[j], z0, 1.f);
+      if (r1 < a.V) join(m[j], s[j], z1, 1.f);
     }
   }
 #pragma unroll
@@ -992,6 +1064,9 @@ cudaError_t launch_xent_forward(const XentDesc& d, const void* X, const void* W,
     XParams P = params_of(d, targets, status);
     P.part = part;
     P.zt = zt;
+    // segments of like length: none at a tile's end that is too short for the epilogue
+    const int kblocks = up(d.H, kBK);
+    P.segment = up(kblocks, up(kblocks, kSegment));
     P.ticket = ticket;
     P.njob = 1;
     P.job[0].kind = XK_STATS;

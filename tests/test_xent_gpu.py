@@ -152,6 +152,25 @@ def test_target_outside_the_vocabulary_is_reported():
         assert out["total"][2] == (67 if index == "int64" else 68)
 
 
+@pytest.mark.parametrize("T,H", [(16, 4096), (16, 4104), (200, 512), (200, 4096), (333, 4136), (200, 8192)])
+def test_log_sums_are_not_biased(T, H):
+    """A tensor-core accumulator truncates: added up in one of them, 4096
+    products move lse by 2e-5, every row the same way.  Segments of at most 512
+    columns bound that: 32 additions, each of at most half a unit of 2^-21 on
+    average (the logits that make up lse are below 8 here), and no more than two
+    units (2^-20) from the few roundings of lse itself."""
+    X, W, t = _make(T, H, 5003)
+    out = _run(X, W, t, backward=False)
+    Xd, Wd, td = _f64(X), _f64(W), t.cpu().numpy()
+    loss, lse, _ = O.cross_entropy(Xd, Wd, td, IGNORE)
+    z = Xd @ Wd.T
+    p = np.exp(z - lse[:, None])
+    assert (p * np.abs(z)).sum(1).mean() < 8
+    tol = 32 * 2.0 ** -22 + 2 * 2.0 ** -20
+    assert abs((out["lse"] - lse).mean()) <= tol
+    assert abs((out["loss"] - loss).mean()) <= tol
+
+
 def test_large_logits():
     """Logits in the hundreds: exp of the raw logit would overflow."""
     X, W, t = _make(130, 256, 600, sharp=60.0)
