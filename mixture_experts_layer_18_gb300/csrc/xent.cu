@@ -62,6 +62,8 @@ constexpr int kSegment = 8;                     // most K blocks that the forwar
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFewTokens = 16;                  // most tokens of the kernel for few tokens
 constexpr int kFewMaxBlocks = 512;
+constexpr int kSplitRows = 32;                  // most tokens whose dz is kept as two bf16 numbers
+static_assert(2 * kSplitRows == kBK, "both parts are one K block of dW");
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 enum : int { XK_STATS = 0, XK_DZ = 1, XK_DX = 2, XK_DW = 3 };
@@ -98,6 +100,8 @@ struct XParams {
   unsigned* ticket;      // STATS: zeroed for the join kernel
   float* acc;            // DX: fp32 sums [ks][T][Hp]
   int zcols;             // DZ: columns of the dz buffer
+  int split;             // dz as a sum of two bf16 numbers: rows 0..31 and 32..63
+  int rows;              // rows of dz and of dX's sums: T, or 64 if split
   int Hp;
   int add, last;         // DX: add to acc; write bf16 results
   int32_t* status;
@@ -203,7 +207,13 @@ __device__ void load_role(const XParams& P, const Schedule& sc, int rank, uint8_
         }
       } else {
         uint8_t* sB = sA + kABytes;
-        if (g.b_mn) {
+        if (P.split && ti.kind == XK_DW) {       // X's rows for either part of dz
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            tma_load_2d_pair(sB + i * (kAtomBytes / 2), &g.tmB, n0, 0, fbar);
+            tma_load_2d_pair(sB + kAtomBytes + i * (kAtomBytes / 2), &g.tmB, n0 + 64, 0, fbar);
+          }
+        } else if (g.b_mn) {
           tma_load_2d_pair(sB, &g.tmB, n0, k0 + g.b_k0, fbar);
           tma_load_2d_pair(sB + kAtomBytes, &g.tmB, n0 + 64, k0 + g.b_k0, fbar);
         } else {
@@ -454,8 +464,16 @@ __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, ui
             if (v0 + c + 32 + i >= P.V) b[i] = 0.f;
           }
         }
-        const int x = ti.n0 + c0 + c;
-        if (y0 < P.T) store_boxes(&g.tmO, a, b, x, y0, two ? P.zcols : min(P.zcols, x + 32));
+        const int x = ti.n0 + c0 + c, end = two ? P.zcols : min(P.zcols, x + 32);
+        if (y0 < P.T) store_boxes(&g.tmO, a, b, x, y0, end);
+        if (y0 < P.T && P.split) {               // (y0 is 0) what that rounding left, 32 rows on
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            a[i] -= __bfloat162float(__float2bfloat16_rn(a[i]));
+            b[i] -= __bfloat162float(__float2bfloat16_rn(b[i]));
+          }
+          store_boxes(&g.tmO, a, b, x, kSplitRows, end);
+        }
       }
     } else if (ti.kind == XK_DX && P.last) {     // the sums of the pieces before + this one, to bf16
       const float* sums = P.acc + ((size_t)ti.slice * P.T + (live ? row : 0)) * P.Hp + ti.n0 + c0;
@@ -487,7 +505,7 @@ __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, ui
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
-        if (y0 >= P.T) continue;
+        if (y0 >= P.rows) continue;
         if (lane == 0) bulk_wait_read_all();
         __syncwarp();
         stage_f32_row(sb0, lane, v);
@@ -849,7 +867,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, kFewPerSm) xent_few_kernel(con
 }
 
 // dX from the slices' fp32 sums (H a multiple of 8).
-__global__ void __launch_bounds__(256) xent_dx_kernel(const float* acc, int ks, int T, int H, int Hp,
+__global__ void __launch_bounds__(256) xent_dx_kernel(const float* acc, int ks, int rows, int parts, int T, int H, int Hp,
                                                       const float* dloss, const float* total,
                                                       int reduction, __nv_bfloat16* dX) {
   let_next_start();
@@ -860,11 +878,18 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float* acc, int ks, 
   const int64_t row = i / per;
   const int c = (int)(i - row * per) * 8;
   float v[8] = {};
-  for (int k = 0; k < ks; ++k) {
-    const float4* p = reinterpret_cast<const float4*>(acc + ((size_t)k * T + row) * Hp + c);
-    const float4 a = p[0], b = p[1];
+  const float* p = acc + (size_t)row * Hp + c;
+  const size_t step = (size_t)rows * Hp, half = (size_t)kSplitRows * Hp;
+#pragma unroll 8
+  for (int k = 0; k < ks; ++k, p += step) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
     v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
     v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    if (parts > 1) {                             // the second part of a split dz
+      const float4 e = *reinterpret_cast<const float4*>(p + half), f = *reinterpret_cast<const float4*>(p + half + 4);
+      v[0] += e.x; v[1] += e.y; v[2] += e.z; v[3] += e.w;
+      v[4] += f.x; v[5] += f.y; v[6] += f.z; v[7] += f.w;
+    }
   }
   const float gs = common_scale(dloss, total, reduction);
 #pragma unroll
@@ -974,15 +999,21 @@ cudaError_t launch_few(const XentDesc& d, const void* X, const void* W, const vo
 }
 
 // The backward's pieces of the vocabulary: [T, piece] of dz in bf16 is held
-// to about 256 MB, and a piece to whole tiles.
+// to about 256 MB, and a piece to whole tiles.  Up to 32 tokens (whose 64 rows
+// fill one K block and a part of one row tile all the same) it is kept as a sum
+// of two bf16 numbers: where one target's rounding is most of an output's error,
+// it could be twice that of the output's own rounding (one token, V = 1000:
+// 0.0030 against 0.0019 relative; from 64 tokens on it averages out, 0.0020).
+// The second half costs 3 us of 18 at 7 x 512, V = 5000.
 struct BwdWs {
   size_t dz, acc, total;
-  int piece, slices, Hp;
+  int piece, slices, Hp, rows;
 };
 BwdWs bwd_ws(const XentDesc& d) {
   BwdWs w;
   const int vp = up(d.V, kTile) * kTile;
-  int64_t piece = (256LL << 20) / (2 * (d.T < 1 ? 1 : (int64_t)d.T)) / kTile * kTile;
+  w.rows = d.T <= kSplitRows ? 2 * kSplitRows : d.T;
+  int64_t piece = (256LL << 20) / (2 * (int64_t)w.rows) / kTile * kTile;
   if (piece < 4096) piece = 4096;
   w.piece = piece < vp ? (int)piece : vp;
   w.Hp = up(d.H, kTile) * kTile;
@@ -993,8 +1024,8 @@ BwdWs bwd_ws(const XentDesc& d) {
   if (ks > w.piece / 512) ks = w.piece / 512;
   w.slices = ks < 1 ? 1 : ks;
   size_t o = 0;
-  w.dz = o; o += align256((size_t)d.T * w.piece * 2);
-  w.acc = o; o += align256((size_t)w.slices * d.T * w.Hp * sizeof(float));
+  w.dz = o; o += align256((size_t)w.rows * w.piece * 2);
+  w.acc = o; o += align256((size_t)w.slices * w.rows * w.Hp * sizeof(float));
   w.total = o ? o : 256;
   return w;
 }
@@ -1092,6 +1123,7 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
   if (!dX && !dW) return cudaSuccess;
   const BwdWs w = bwd_ws(d);
   void* dz = ws + w.dz;
+  const bool split = d.T <= kSplitRows, join = w.slices > 1 || split;   // a last kernel adds dX's sums up
   for (int v0 = 0; v0 < d.V; v0 += w.piece) {
     const int cols = d.V - v0 < w.piece ? d.V - v0 : w.piece;
     const bool last = v0 + cols == d.V;
@@ -1102,10 +1134,12 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
     P.reduction = reduction;
     P.lse = lse;
     P.zcols = w.piece;
+    P.split = split;
+    P.rows = w.rows;
     P.njob = 1;
     P.job[0].kind = XK_DZ;
     bool ok = logits_job(P.job[0], d, X, W, v0, cols) &&
-              make_tmap_out(&P.job[0].tmO, dz, d.T, w.piece, w.piece);
+              make_tmap_out(&P.job[0].tmO, dz, w.rows, w.piece, w.piece);
     if (ok) XENT_TRY(launch<true>(P, s));
     // dX (+)= dz W[piece], dW[piece] = dz^T X
     XParams Q = params_of(d, targets, status);
@@ -1115,7 +1149,9 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
     Q.acc = reinterpret_cast<float*>(ws + w.acc);
     Q.Hp = w.Hp;
     Q.add = v0 > 0;
-    Q.last = last && w.slices == 1;
+    Q.last = last && !join;
+    Q.split = split;
+    Q.rows = w.rows;
     if (ok && dX) {
       XJob& g = Q.job[Q.njob++];
       g.kind = XK_DX;
@@ -1127,10 +1163,10 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
       g.ks = w.slices;
       g.group = 8;
       g.b_k0 = v0;
-      ok = make_tmap(&g.tmA, dz, 2, d.T, w.piece, kBK, 128, w.piece) &&
+      ok = make_tmap(&g.tmA, dz, 2, w.rows, w.piece, kBK, 128, w.piece) &&
            make_tmap(&g.tmB, W, 2, d.V, d.H, 64, kBK, d.ld_w) &&
            (Q.last ? make_tmap_out(&g.tmO, dX, d.T, d.H)
-                   : make_tmap_out_f32(&g.tmO, Q.acc, w.slices, d.T, w.Hp));
+                   : make_tmap_out_f32(&g.tmO, Q.acc, w.slices, w.rows, w.Hp));
     }
     if (ok && dW) {
       XJob& g = Q.job[Q.njob++];
@@ -1139,12 +1175,12 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
       g.tn = kTile;
       g.mt = up(cols, kTile);
       g.nt = up(d.H, kTile);
-      g.kblocks = up(d.T, kBK);
+      g.kblocks = up(w.rows, kBK);
       g.ks = 1;
       g.group = 8;
       g.out_m0 = v0;
-      ok = make_tmap(&g.tmA, dz, 2, d.T, w.piece, 64, kBK, w.piece) &&
-           make_tmap(&g.tmB, X, 2, d.T, d.H, 64, kBK, d.ld_x) && make_tmap_out(&g.tmO, dW, d.V, d.H);
+      ok = make_tmap(&g.tmA, dz, 2, w.rows, w.piece, 64, kBK, w.piece) &&
+           make_tmap(&g.tmB, X, 2, d.T, d.H, 64, split ? kSplitRows : kBK, d.ld_x) && make_tmap_out(&g.tmO, dW, d.V, d.H);
     }
     if (!ok) {
       *st = MOE_ERR_CUDA;
@@ -1156,10 +1192,10 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
     }
     XENT_TRY(launch<true>(Q, s));
   }
-  if (dX && w.slices > 1) {
+  if (dX && join) {
     const int64_t n = (int64_t)d.T * (d.H / 8);
     return launch_overlapped(xent_dx_kernel, (unsigned)((n + 255) / 256), 256, 0, s,
-                        reinterpret_cast<const float*>(ws + w.acc), w.slices, d.T, d.H, w.Hp, dloss, total,
+                        reinterpret_cast<const float*>(ws + w.acc), w.slices, w.rows, split ? 2 : 1, d.T, d.H, w.Hp, dloss, total,
                         reduction, static_cast<__nv_bfloat16*>(dX));
   }
   return cudaSuccess;

@@ -171,6 +171,26 @@ def test_log_sums_are_not_biased(T, H):
     assert abs((out["loss"] - loss).mean()) <= tol
 
 
+@pytest.mark.parametrize("T,H,V", [(1, 128, 1000), (1, 1032, 3001), (5, 512, 2000), (31, 264, 1500), (32, 512, 9000)])
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+def test_few_tokens_round_their_gradients_once(T, H, V, reduction):
+    """dz of up to 32 tokens is held to 16 bits, so dX and dW carry their own
+    rounding to bf16 and nothing else of that size: the root mean square of it
+    is at most 2^-7 / sqrt(12) of the values' (5% for the chance in a few
+    hundred of them)."""
+    import torch
+    X, W, t = _make(T, H, V)
+    d = torch.linspace(0.3, 1.7, T, device="cuda") if reduction == "none" else None
+    out = _run(X, W, t, dloss=d, reduction=reduction)
+    Xd, Wd, td = _f64(X), _f64(W), t.cpu().numpy()
+    _, lse, _ = O.cross_entropy(Xd, Wd, td, IGNORE)
+    dz = np.exp(Xd @ Wd.T - lse[:, None])
+    dz[np.arange(T), td] -= 1
+    dz *= np.full((T, 1), 1.0 / T) if d is None else _f64(d)[:, None]
+    for got, want in ((out["dX"], dz @ Wd), (out["dW"], dz.T @ Xd)):
+        assert np.linalg.norm(got - want) <= 1.05 * 2.0 ** -7 / 12 ** 0.5 * np.linalg.norm(want)
+
+
 def test_large_logits():
     """Logits in the hundreds: exp of the raw logit would overflow."""
     X, W, t = _make(130, 256, 600, sharp=60.0)
