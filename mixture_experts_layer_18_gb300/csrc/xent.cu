@@ -43,6 +43,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "staging.h"
 
 namespace moe {
 
@@ -310,6 +311,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+struct BulkCopies {
+  template <int N>
+  __device__ __forceinline__ void wait_read() { bulk_wait_read<N>(); }
+  __device__ __forceinline__ void commit() { bulk_commit(); }
+};
+
 template <bool BWD>
 __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, uint64_t* tfull,
                               uint64_t* tempty, uint32_t tmem_base, uint8_t* stg, const WaitCtl& wc) {
@@ -321,26 +328,27 @@ __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, ui
   uint8_t* sb1 = sb0 + 2048;
   const uint32_t te0 = mapa_shared(smem_u32(&tempty[0]), 0);
   const uint32_t te1 = mapa_shared(smem_u32(&tempty[1]), 0);
+  StagingTurns<BulkCopies> turns;                // (lane 0's)
   // 64 columns of bf16 results as two boxes, a staging buffer each; columns at
   // or past `cols` are left out.  A buffer is written again once its own last
   // store has been read, while the other's may still be on its way.
   auto store_box = [&](const CUtensorMap* m, uint8_t* buf, const float (&v)[32], int x, int y) {
-    if (lane == 0) bulk_wait_read<1>();
+    if (lane == 0) turns.before_box();
     __syncwarp();
     stage_bf16_row(buf, lane, v);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       tma_store_2d(m, buf, x, y);
-      bulk_commit();
+      turns.after_box();
     }
   };
   auto store_boxes = [&](const CUtensorMap* m, const float (&a)[32], const float (&b)[32], int x, int y,
                          int cols) {
     if (x < cols) store_box(m, sb0, a, x, y);
-    else if (lane == 0) bulk_commit();           // (an empty group keeps the buffers' turns)
+    else if (lane == 0) turns.after_box();
     if (x + 32 < cols) store_box(m, sb1, b, x + 32, y);
-    else if (lane == 0) bulk_commit();
+    else if (lane == 0) turns.after_box();
   };
   const float gs = BWD ? common_scale(P.dloss, P.total, P.reduction) : 1.f;
   int acc = 0;                                   // accumulators taken so far
@@ -506,7 +514,7 @@ __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, ui
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
         if (y0 >= P.rows) continue;
-        if (lane == 0) bulk_wait_read_all();
+        if (lane == 0) turns.before_both();
         __syncwarp();
         stage_f32_row(sb0, lane, v);
         fence_proxy_async_smem();
@@ -514,7 +522,7 @@ __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, ui
         if (lane == 0) {
           if (P.add) tma_add_3d(&g.tmO, sb0, ti.n0 + c0 + c, y0, ti.slice);
           else tma_store_3d(&g.tmO, sb0, ti.n0 + c0 + c, y0, ti.slice);
-          bulk_commit();
+          turns.after_both();
         }
       }
     } else {
