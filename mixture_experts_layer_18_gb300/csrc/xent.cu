@@ -44,13 +44,14 @@
 #include "common.cuh"
 #include "internal.h"
 #include "staging.h"
+#include "xent_plan.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int kStages = 6;
-constexpr int kBK = 64;                         // K elements per stage
+constexpr int kBK = kXentBK;                    // K elements per stage
 constexpr int kABytes = 128 * 128;              // 128 rows x 64 bf16
 constexpr int kStageBytes = 2 * kABytes;        // a CTA's A rows and its half of B
 constexpr int kAtomBytes = kBK * 128;           // 64 K rows x 64 MN elements (MN-major box)
@@ -58,12 +59,12 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
 constexpr int kStgBytes = kEpiWarps * 4096;     // two 32 x 32 bf16 boxes per epilogue warp
 constexpr int kSmemBytes = kStages * kStageBytes + kStgBytes + 1024 + 256;
-constexpr int kTile = 256;
+constexpr int kTile = kXentTile;
 constexpr int kSegment = 8;                     // most K blocks that the forward adds up in one accumulator
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kFewTokens = 16;                  // most tokens of the kernel for few tokens
 constexpr int kFewMaxBlocks = 512;
-constexpr int kSplitRows = 32;                  // most tokens whose dz is kept as two bf16 numbers
+constexpr int kSplitRows = kXentSplitRows;
 static_assert(2 * kSplitRows == kBK, "both parts are one K block of dW");
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -176,8 +177,8 @@ __device__ __forceinline__ XTile decode(const XParams& P, const Schedule& sc, in
   ti.ntile = r / gm;
   ti.m0 = (gi * g.group + (r - ti.ntile * gm)) * kTile + rank * 128;
   ti.n0 = ti.ntile * g.tn;
-  ti.kb0 = (int)((int64_t)g.kblocks * ti.slice / g.ks);
-  ti.kb1 = (int)((int64_t)g.kblocks * (ti.slice + 1) / g.ks);
+  ti.kb0 = xent_slice_start(g.kblocks, g.ks, ti.slice);
+  ti.kb1 = xent_slice_start(g.kblocks, g.ks, ti.slice + 1);
   return ti;
 }
 
@@ -234,7 +235,8 @@ __device__ void load_role(const XParams& P, const Schedule& sc, int rank, uint8_
 }
 
 // One thread of the leader CTA issues every MMA of the pair.  A tile goes
-// through one accumulator, or (forward) one after another per segment of K.
+// through one accumulator, or (forward) one after another per segment of K;
+// every tile has K blocks.
 template <bool BWD>
 __device__ void mma_role(const XParams& P, const Schedule& sc, uint8_t* stages, uint64_t* full,
                          uint64_t* empty, uint64_t* tfull, uint64_t* tempty, uint64_t* drain,
@@ -509,10 +511,6 @@ __device__ void epilogue_role(const XParams& P, const Schedule& sc, int rank, ui
       for (int c = 0; c < 128; c += 32) {
         float v[32];
         tmem_ld32(taddr + c, v);
-        if (ti.kb0 == ti.kb1) {                  // a slice with no K: nothing was multiplied
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
         if (y0 >= P.rows) continue;
         if (lane == 0) turns.before_both();
         __syncwarp();
@@ -908,8 +906,8 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float* acc, int ks, 
 }
 
 // ------------------------------------------------------------------ host
-int up(int64_t a, int b) { return (int)((a + b - 1) / b); }
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+int up(int64_t a, int b) { return xent_up(a, b); }
+size_t align256(size_t x) { return xent_align(x); }
 
 // m-tiles that keep their rows of A in L2 (48 MB) through one sweep over N.
 int group_for(int64_t row_bytes) {
@@ -1006,38 +1004,6 @@ cudaError_t launch_few(const XentDesc& d, const void* X, const void* W, const vo
   return d.T <= 8 ? run_few<1>(a, np, s) : run_few<2>(a, np, s);
 }
 
-// The backward's pieces of the vocabulary: [T, piece] of dz in bf16 is held
-// to about 256 MB, and a piece to whole tiles.  Up to 32 tokens (whose 64 rows
-// fill one K block and a part of one row tile all the same) it is kept as a sum
-// of two bf16 numbers: where one target's rounding is most of an output's error,
-// it could be twice that of the output's own rounding (one token, V = 1000:
-// 0.0030 against 0.0019 relative; from 64 tokens on it averages out, 0.0020).
-// The second half costs 3 us of 18 at 7 x 512, V = 5000.
-struct BwdWs {
-  size_t dz, acc, total;
-  int piece, slices, Hp, rows;
-};
-BwdWs bwd_ws(const XentDesc& d) {
-  BwdWs w;
-  const int vp = up(d.V, kTile) * kTile;
-  w.rows = d.T <= kSplitRows ? 2 * kSplitRows : d.T;
-  int64_t piece = (256LL << 20) / (2 * (int64_t)w.rows) / kTile * kTile;
-  if (piece < 4096) piece = 4096;
-  w.piece = piece < vp ? (int)piece : vp;
-  w.Hp = up(d.H, kTile) * kTile;
-  // few dX tiles: their K (the piece) is cut into slices until every SM pair
-  // has two tiles; a slice keeps at least 512 columns
-  const int tiles = up(d.T < 1 ? 1 : d.T, kTile) * up(d.H, kTile);
-  int ks = up(152, tiles);
-  if (ks > w.piece / 512) ks = w.piece / 512;
-  w.slices = ks < 1 ? 1 : ks;
-  size_t o = 0;
-  w.dz = o; o += align256((size_t)w.rows * w.piece * 2);
-  w.acc = o; o += align256((size_t)w.slices * w.rows * w.Hp * sizeof(float));
-  w.total = o ? o : 256;
-  return w;
-}
-
 XParams params_of(const XentDesc& d, const void* targets, int32_t* status) {
   XParams P;
   memset(&P, 0, sizeof(P));
@@ -1078,7 +1044,7 @@ bool logits_job(XJob& g, const XentDesc& d, const void* X, const void* W, int v0
 }  // namespace
 
 size_t xent_forward_bytes(const XentDesc& d) { return fwd_ws(d).total; }
-size_t xent_backward_bytes(const XentDesc& d) { return bwd_ws(d).total; }
+size_t xent_backward_bytes(const XentDesc& d) { return xent_backward_plan(d.T, d.H, d.V).total; }
 
 #define XENT_TRY(expr)                       \
   do {                                       \
@@ -1129,7 +1095,7 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
   if (d.T == 0)   // no token: dW is zero
     return dW ? cudaMemsetAsync(dW, 0, (size_t)d.V * d.H * 2, s) : cudaSuccess;
   if (!dX && !dW) return cudaSuccess;
-  const BwdWs w = bwd_ws(d);
+  const XentBackwardPlan w = xent_backward_plan(d.T, d.H, d.V);
   void* dz = ws + w.dz;
   const bool split = d.T <= kSplitRows, join = w.slices > 1 || split;   // a last kernel adds dX's sums up
   for (int v0 = 0; v0 < d.V; v0 += w.piece) {
@@ -1168,7 +1134,7 @@ cudaError_t launch_xent_backward(const XentDesc& d, const void* X, const void* W
       g.mt = up(d.T, kTile);
       g.nt = up(d.H, kTile);
       g.kblocks = up(cols, kBK);
-      g.ks = w.slices;
+      g.ks = xent_piece_slices(w, cols);
       g.group = 8;
       g.b_k0 = v0;
       ok = make_tmap(&g.tmA, dz, 2, w.rows, w.piece, kBK, 128, w.piece) &&
