@@ -68,6 +68,10 @@ class _Op:
             self._refuse(name, t, shape, dtype, "adjacent elements in rows that do not overlap")
         return t.data_ptr(), ld
 
+    def _keep(self, *tensors):
+        """Keeps the memory of tensors whose addresses are recorded."""
+        self._kept = tensors
+
     def _refuse(self, name, t, shape, dtype, layout):
         got = f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}" \
             if isinstance(t, torch.Tensor) else repr(t)
@@ -107,6 +111,7 @@ class LayerNorm(_Op):
         f32 = dict(dtype=torch.float32, device=self.device)
         self.mean = torch.empty(T, **f32) if backward else None
         self.rstd = torch.empty(T, **f32) if backward else None
+        self._keep(self.mean, self.rstd)
         self._stats = (_ptr(self.mean), _ptr(self.rstd))
         self.ws = torch.empty(need if backward else 0, dtype=torch.uint8, device=self.device)
 
@@ -170,6 +175,7 @@ class CrossEntropy(_Op):
         self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
         self.with_backward = backward
+        self._keep(self.loss, self.lse, self.total)
         self._out = (self.loss.data_ptr(), self.lse.data_ptr(), self.total.data_ptr())
 
     def _inputs(self, X, W, targets):
@@ -209,38 +215,59 @@ class CrossEntropy(_Op):
         return dict(dX=torch.empty((self.T, self.H), **b), dW=torch.empty((self.V, self.H), **b))
 
 
+_address = torch.Tensor.data_ptr
+
+
 class GradClip(_Op):
-    """Global L2 norm of a fixed list of gradient tensors (contiguous, float32
-    or bfloat16), and clipping by it: in place, or into the tensors `out`.
-    After either call ``norm`` [] holds the norm (float32 on the device)."""
+    """Global L2 norm of a list of gradient tensors (contiguous, float32 or
+    bfloat16), and clipping by it: in place, or into the tensors `out`.  Where
+    the tensors lie is looked up at every call (their ``data`` may have been
+    replaced since); a size that changes in the same place is not noticed, and
+    the memory given before stays in use.  After either call ``norm`` [] holds
+    the norm (float32 on the device)."""
 
     def __init__(self, grads, out=None, device="cuda"):
         self.grads = list(grads)
         self.out = self.grads if out is None else list(out)
         _require(len(self.out) == len(self.grads), "GradClip: as many outputs as gradients")
         self._device(self.grads[0].device if self.grads else device)
-        for i, (g, o) in enumerate(zip(self.grads, self.out)):
-            _require(isinstance(g, torch.Tensor) and g.dtype in TYPES, f"grads[{i}]: float32 or bfloat16")
-            self._fits(f"grads[{i}]", g, g.shape, g.dtype)
-            self._fits(f"out[{i}]", o, g.shape, g.dtype)
-        self.list = (moe_grad_tensor * max(1, len(self.grads)))(
-            *[moe_grad_tensor(_ptr(g), _ptr(o), g.numel(), TYPES[g.dtype])
-              for g, o in zip(self.grads, self.out)])
+        self._tensors = self.grads if out is None else self.grads + self.out
+        self._describe()
         self.norm = torch.empty((), dtype=torch.float32, device=self.device)
         self.ws = torch.empty(moe_grad_workspace_size(len(self.grads)), dtype=torch.uint8,
                               device=self.device)
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self._keep(self.norm, self.ws, self.status)
         self._buffers = (self.norm.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
                          self.status.data_ptr())
 
+    def _describe(self):
+        """Checks the tensors and lists them for the library."""
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            _require(isinstance(g, torch.Tensor) and g.dtype in TYPES, f"grads[{i}]: float32 or bfloat16")
+            self._fits(f"grads[{i}]", g, g.shape, g.dtype)
+            self._fits(f"out[{i}]", o, g.shape, g.dtype)
+        entries = (moe_grad_tensor * max(1, len(self.grads)))(
+            *[moe_grad_tensor(_ptr(g), _ptr(o), g.numel(), TYPES[g.dtype])
+              for g, o in zip(self.grads, self.out)])
+        # (aliases of their own, which keep the listed memory whatever becomes of the tensors)
+        self._listed = (entries, list(map(_address, self._tensors)), [t.detach() for t in self._tensors])
+        return entries
+
+    def _list(self):
+        """The list, made again if a tensor lies elsewhere.  (0.08 us per tensor;
+        without it a freed address would be written to.  Sizes too: twice that.)"""
+        entries, addresses, _ = self._listed
+        return entries if list(map(_address, self._tensors)) == addresses else self._describe()
+
     def measure(self, stream=None):
         """The norm alone."""
-        rc = moe_grad_norm(self.list, len(self.grads), *self._buffers, self._current(stream))
+        rc = moe_grad_norm(self._list(), len(self.grads), *self._buffers, self._current(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_grad_norm")
 
     def clip(self, max_norm, stream=None):
         """out = grads * min(1, max_norm / norm)."""
-        rc = moe_clip_grads(self.list, len(self.grads), max_norm, *self._buffers, self._current(stream))
+        rc = moe_clip_grads(self._list(), len(self.grads), max_norm, *self._buffers, self._current(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_clip_grads")

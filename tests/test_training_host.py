@@ -1,0 +1,81 @@
+"""The Python side of the training-step operators, run on the CPU: host tensors
+stand in for device memory and a recorder for the library's calls, so what is
+checked is what would be launched."""
+import weakref
+
+import pytest
+import torch
+
+import mixture_experts_layer_18_gb300 as M
+from mixture_experts_layer_18_gb300 import training
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """Ops on host memory; returns the module."""
+    def device(self, _):
+        self.index, self.device = -1, torch.device("cpu")
+    monkeypatch.setattr(training._Op, "_device", device)
+    monkeypatch.setattr(training._Op, "_current", lambda self, stream: 0)
+    return training
+
+
+def _entries(array, count):
+    return [(array[i].src, array[i].dst, array[i].n, array[i].type) for i in range(count)]
+
+
+def test_gradients_that_move_are_found(host, monkeypatch):
+    """A gradient whose memory was replaced or resized is read and written where
+    it is at the time of the call, never where it was."""
+    seen = []
+    monkeypatch.setattr(host, "moe_clip_grads", lambda t, n, *a: seen.append(_entries(t, n)) or 0)
+    monkeypatch.setattr(host, "moe_grad_norm", lambda t, n, *a: seen.append(_entries(t, n)) or 0)
+    a, b, o = torch.zeros(10), torch.zeros(6, dtype=torch.bfloat16), torch.zeros(10)
+
+    def want(first, out):
+        return [(first.data_ptr(), out.data_ptr(), first.numel(), M.MOE_TYPE_F32),
+                (b.data_ptr(), b.data_ptr(), 6, M.MOE_TYPE_BF16)]
+    c = host.GradClip([a, b], out=[o, b])
+    for call in (lambda: c.clip(1.0), c.measure):
+        call()
+        assert seen[-1] == want(a, o)
+        keep = a.data                                  # (so that its address is not given out again)
+        a.data = torch.ones(10)
+        call()
+        assert seen[-1] == want(a, o) and seen[-1][0][0] != keep.data_ptr()
+        keep = o.data
+        o.data = torch.ones(10)
+        call()
+        assert seen[-1] == want(a, o) and seen[-1][0][1] != keep.data_ptr()
+    n = len(seen)
+    keep = a.data
+    a.resize_(100)                                     # more than its memory holds: moved
+    with pytest.raises(M.MoEError):
+        c.clip(1.0)                                    # its output no longer fits
+    o.resize_(100)
+    c.clip(1.0)
+    assert len(seen) == n + 1 and seen[-1] == want(a, o) and seen[-1][0][2] == 100
+    a.data = torch.ones(100, dtype=torch.float64)
+    with pytest.raises(M.MoEError):
+        c.clip(1.0)
+
+
+def test_memory_of_the_list_stays(host, monkeypatch):
+    """Between a change and the next call the listed memory is not given away."""
+    a = torch.zeros(1000)
+    c = host.GradClip([a])
+    held = [weakref.ref(t) for t in c._listed[-1]]
+    a.data = torch.empty(0)
+    assert held[0]().numel() == 1000 and held[0]().data_ptr() != a.data_ptr()
+
+
+def test_memory_whose_address_is_recorded_stays(host):
+    """The results' names may be given to other tensors; the memory that the
+    library was given stays."""
+    for op, names in ((host.GradClip([torch.zeros(8)]), ("norm", "ws", "status")),
+                      (host.CrossEntropy(4, 64, 100), ("loss", "lse", "total")),
+                      (host.LayerNorm(4, 64), ("mean", "rstd"))):
+        held = {k: weakref.ref(getattr(op, k)) for k in names}
+        for k in names:
+            setattr(op, k, None)
+        assert all(r() is not None for r in held.values()), op
