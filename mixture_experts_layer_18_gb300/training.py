@@ -25,8 +25,10 @@ INDEX_TYPES = {torch.int32: MOE_INDEX_I32, torch.int64: MOE_INDEX_I64}
 REDUCTIONS = {"none": MOE_REDUCE_NONE, "sum": MOE_REDUCE_SUM, "mean": MOE_REDUCE_MEAN}
 
 
-# torch.cuda.current_stream(index).cuda_stream without the Stream object (3 us)
+# torch.cuda.current_stream(index).cuda_stream without the Stream object (3 us),
+# torch.cuda.current_device() without its first-call initialisation
 _current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _require(ok, what):
@@ -79,8 +81,13 @@ class _Op:
                                             f"{layout}; got {got}")
 
     def _current(self, stream):
-        """Handle of `stream`, or of the device's current stream."""
-        return stream.cuda_stream if stream is not None else _current_stream(self.index)
+        """Handle of `stream`, or of the device's current stream.  The library
+        launches on the thread's current device, so that has to be this one."""
+        if _current_device() != self.index or (
+                stream is not None and getattr(stream, "device_index", self.index) != self.index):
+            raise MoEError(MOE_ERR_INVALID_ARG, f"called for {self.device}, but cuda:{_current_device()} "
+                                                f"is current (stream: {stream})")
+        return _current_stream(self.index) if stream is None else stream.cuda_stream
 
     def _device(self, device):
         d = torch.device(device)

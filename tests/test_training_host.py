@@ -79,3 +79,24 @@ def test_memory_whose_address_is_recorded_stays(host):
         for k in names:
             setattr(op, k, None)
         assert all(r() is not None for r in held.values()), op
+
+
+class _Stream:
+    def __init__(self, index):
+        self.device_index, self.cuda_stream = index, 77
+
+
+def test_calls_on_another_device_are_refused(monkeypatch):
+    """An op of one device is not launched while another is current, nor on
+    another's stream: the library launches on the current device."""
+    monkeypatch.setattr(training, "_current_stream", lambda index: 5)
+    op = training._Op()
+    op.index, op.device = 1, torch.device("cuda", 1)
+    monkeypatch.setattr(training, "_current_device", lambda: 1, raising=False)
+    assert op._current(None) == 5 and op._current(_Stream(1)) == 77
+    with pytest.raises(M.MoEError):
+        op._current(_Stream(0))
+    monkeypatch.setattr(training, "_current_device", lambda: 0)
+    for stream in (None, _Stream(0), _Stream(1)):
+        with pytest.raises(M.MoEError):
+            op._current(stream)
