@@ -3,10 +3,11 @@ step: layer norm, cross entropy over a vocabulary, and gradient clipping.
 
 As in ``layer``, PyTorch supplies device memory and the stream; every
 computation is a call into libmoe_gb300.so.  Each class owns the statistics
-and the workspace of one problem shape on one device (calls on different
-streams have to be ordered by the caller), checks the tensors it
-is given against that shape, and raises ``MoEError`` on any non-OK return code
-and for tensors that do not fit.
+and the workspace of one problem shape on one device (an object's calls on
+different streams, or from different threads, have to be ordered by the caller:
+they share those; a LayerNorm with ``backward=False`` has none to share), checks
+the tensors it is given against that shape, and raises ``MoEError`` on any
+non-OK return code and for tensors that do not fit.
 """
 from __future__ import annotations
 
@@ -70,6 +71,11 @@ class _Op:
             self._refuse(name, t, shape, dtype, "adjacent elements in rows that do not overlap")
         return t.data_ptr(), ld
 
+    @property
+    def dims(self):
+        """The library's description of the problem, as of the last call."""
+        return self._described[1]
+
     def _keep(self, *tensors):
         """Keeps the memory of tensors whose addresses are recorded."""
         self._kept = tensors
@@ -112,8 +118,8 @@ class LayerNorm(_Op):
         self.T, self.H, self.dtype, self.weight_dtype, self.eps = T, H, dtype, weight_dtype, eps
         self._device(device)
         self.shape = torch.Size((T, H))
-        self.dims = moe_norm_dims(T, H, H, H, H, TYPES[dtype], TYPES[weight_dtype], eps)
-        need = moe_layer_norm_workspace_size(self.dims)
+        self._described = (None, None)
+        need = moe_layer_norm_workspace_size(self._dims(H, H, H))
         _require(need > 0, "LayerNorm: invalid sizes")
         f32 = dict(dtype=torch.float32, device=self.device)
         self.mean = torch.empty(T, **f32) if backward else None
@@ -122,29 +128,39 @@ class LayerNorm(_Op):
         self._stats = (_ptr(self.mean), _ptr(self.rstd))
         self.ws = torch.empty(need if backward else 0, dtype=torch.uint8, device=self.device)
 
+    def _dims(self, *lds):
+        """The library's description with these distances of rows.  A published
+        one is never written again: a call in another thread may be reading it."""
+        known = self._described
+        if known[0] != lds:
+            known = self._described = (lds, moe_norm_dims(self.T, self.H, *lds, TYPES[self.dtype],
+                                                          TYPES[self.weight_dtype], self.eps))
+        return known[1]
+
     def forward(self, x, gamma, beta, y, stream=None):
         """y = layer norm of x; gamma and beta may be None (1 and 0)."""
-        d, shape, dt, wt, w = self.dims, self.shape, self.dtype, self.weight_dtype, self.shape[1:]
-        x, d.ld_x = self._rows("x", x, shape, dt)
-        y, d.ld_y = self._rows("y", y, shape, dt)
+        shape, dt, wt, w = self.shape, self.dtype, self.weight_dtype, self.shape[1:]
+        x, ld_x = self._rows("x", x, shape, dt)
+        y, ld_y = self._rows("y", y, shape, dt)
         gamma = self._fits_or_none("gamma", gamma, w, wt)
         beta = self._fits_or_none("beta", beta, w, wt)
-        rc = moe_layer_norm(d, x, gamma, beta, y, *self._stats, self._current(stream))
+        rc = moe_layer_norm(self._dims(ld_x, ld_y, self.H), x, gamma, beta, y, *self._stats,
+                            self._current(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_layer_norm")
 
     def backward(self, dy, x, gamma, dx, dgamma=None, dbeta=None, stream=None):
         """dx, dgamma and dbeta (None leaves one out) of the last forward's x."""
-        d, shape, dt, wt, w = self.dims, self.shape, self.dtype, self.weight_dtype, self.shape[1:]
+        shape, dt, wt, w = self.shape, self.dtype, self.weight_dtype, self.shape[1:]
         _require(self.mean is not None, "LayerNorm: built with backward=False")
-        dy, d.ld_y = self._rows("dy", dy, shape, dt)
-        x, d.ld_x = self._rows("x", x, shape, dt)
-        dx, d.ld_dx = self._rows("dx", dx, shape, dt)
+        dy, ld_dy = self._rows("dy", dy, shape, dt)
+        x, ld_x = self._rows("x", x, shape, dt)
+        dx, ld_dx = self._rows("dx", dx, shape, dt)
         gamma = self._fits_or_none("gamma", gamma, w, wt)
         dgamma = self._fits_or_none("dgamma", dgamma, w, wt)
         dbeta = self._fits_or_none("dbeta", dbeta, w, wt)
-        rc = moe_layer_norm_backward(d, dy, x, gamma, *self._stats, dx, dgamma, dbeta,
-                                     self.ws.data_ptr(), self.ws.numel(), self._current(stream))
+        rc = moe_layer_norm_backward(self._dims(ld_x, ld_dy, ld_dx), dy, x, gamma, *self._stats, dx, dgamma,
+                                     dbeta, self.ws.data_ptr(), self.ws.numel(), self._current(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_layer_norm_backward")
 
@@ -168,12 +184,13 @@ class CrossEntropy(_Op):
         self.T, self.H, self.V, self.ignore_index = T, H, V, ignore_index
         self.index_dtype = index_dtype
         self._device(device)
-        self.dims = moe_xent_dims(T, H, V, H, H, ignore_index, INDEX_TYPES[index_dtype])
-        need = moe_cross_entropy_workspace_size(self.dims, MOE_WS_FORWARD)
+        self._described = (None, None)
+        dims = self._dims(H, H)
+        need = moe_cross_entropy_workspace_size(dims, MOE_WS_FORWARD)
         _require(need > 0, "CrossEntropy: invalid sizes (H has to be a multiple of 8)")
         if backward:
             # the two calls of a step run one after the other: one workspace
-            need = max(need, moe_cross_entropy_workspace_size(self.dims, MOE_WS_BACKWARD))
+            need = max(need, moe_cross_entropy_workspace_size(dims, MOE_WS_BACKWARD))
         f32 = dict(dtype=torch.float32, device=self.device)
         self.loss = torch.empty(T, **f32)
         self.lse = torch.empty(T, **f32)
@@ -185,11 +202,18 @@ class CrossEntropy(_Op):
         self._keep(self.loss, self.lse, self.total)
         self._out = (self.loss.data_ptr(), self.lse.data_ptr(), self.total.data_ptr())
 
+    def _dims(self, *lds):
+        """As LayerNorm's."""
+        known = self._described
+        if known[0] != lds:
+            known = self._described = (lds, moe_xent_dims(self.T, self.H, self.V, *lds, self.ignore_index,
+                                                          INDEX_TYPES[self.index_dtype]))
+        return known[1]
+
     def _inputs(self, X, W, targets):
-        d = self.dims
-        X, d.ld_x = self._rows("X", X, (self.T, self.H), torch.bfloat16)
-        W, d.ld_w = self._rows("W", W, (self.V, self.H), torch.bfloat16)
-        return d, X, W, self._fits("targets", targets, (self.T,), self.index_dtype)
+        X, ld_x = self._rows("X", X, (self.T, self.H), torch.bfloat16)
+        W, ld_w = self._rows("W", W, (self.V, self.H), torch.bfloat16)
+        return self._dims(ld_x, ld_w), X, W, self._fits("targets", targets, (self.T,), self.index_dtype)
 
     def forward(self, X, W, targets, stream=None):
         d, X, W, targets = self._inputs(X, W, targets)

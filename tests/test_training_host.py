@@ -1,6 +1,7 @@
 """The Python side of the training-step operators, run on the CPU: host tensors
 stand in for device memory and a recorder for the library's calls, so what is
 checked is what would be launched."""
+import threading
 import weakref
 
 import pytest
@@ -100,3 +101,45 @@ def test_calls_on_another_device_are_refused(monkeypatch):
     for stream in (None, _Stream(0), _Stream(1)):
         with pytest.raises(M.MoEError):
             op._current(stream)
+
+
+def _two_calls(first, second):
+    """Runs both at once, each from a thread of its own."""
+    errors = []
+
+    def run(f):
+        try:
+            f()
+        except BaseException as e:      # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=(f,)) for f in (first, second)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(20)
+    assert not errors, errors
+
+
+@pytest.mark.parametrize("op", ["norm", "xent"])
+def test_calls_of_two_threads_keep_their_strides(host, monkeypatch, op):
+    """Both calls are inside the library at the same time; each has the
+    distances of its own rows."""
+    meet, seen = threading.Barrier(2, timeout=10), {}
+
+    def library(d, x, *a):
+        meet.wait()                     # (both callers have described their rows)
+        seen[x] = (d.ld_x, d.ld_y if op == "norm" else d.ld_w)
+        return 0
+    monkeypatch.setattr(host, "moe_layer_norm", library)
+    monkeypatch.setattr(host, "moe_cross_entropy", library)
+    make = lambda pad: torch.zeros((6, 64 + pad), dtype=torch.bfloat16)[:, :64]   # noqa: E731
+    x, other = [make(8), make(24)], [make(16), make(40)]
+    if op == "norm":
+        n = host.LayerNorm(6, 64)
+        calls = [lambda i=i: n.forward(x[i], None, None, other[i]) for i in (0, 1)]
+    else:
+        c, t = host.CrossEntropy(6, 64, 6), torch.zeros(6, dtype=torch.int64)
+        calls = [lambda i=i: c.forward(x[i], other[i], t) for i in (0, 1)]
+    _two_calls(*calls)
+    assert seen == {x[0].data_ptr(): (72, 80), x[1].data_ptr(): (88, 104)}
+    assert (n if op == "norm" else c).dims.T == 6
