@@ -37,6 +37,11 @@ def _require(ok, what):
         raise MoEError(MOE_ERR_INVALID_ARG, what)
 
 
+def _require_int32(what, *numbers):
+    # (ctypes would keep the low 32 bits of others)
+    _require(all(-(1 << 31) <= n < 1 << 31 for n in numbers), what + ": sizes and ignored values have 32 bits")
+
+
 class _Op:
     """The checks cost about as much as a small kernel, so they are a few
     comparisons each and build no text unless something is wrong."""
@@ -115,6 +120,7 @@ class LayerNorm(_Op):
                  backward=True):
         weight_dtype = dtype if weight_dtype is None else weight_dtype
         _require(dtype in TYPES and weight_dtype in TYPES, "LayerNorm: float32 or bfloat16")
+        _require_int32("LayerNorm", T, H)
         self.T, self.H, self.dtype, self.weight_dtype, self.eps = T, H, dtype, weight_dtype, eps
         self._device(device)
         self.shape = torch.Size((T, H))
@@ -181,6 +187,7 @@ class CrossEntropy(_Op):
     def __init__(self, T, H, V, ignore_index=-100, index_dtype=torch.int64, device="cuda",
                  backward=True):
         _require(index_dtype in INDEX_TYPES, "CrossEntropy: int32 or int64 targets")
+        _require_int32("CrossEntropy", T, H, V, ignore_index)
         self.T, self.H, self.V, self.ignore_index = T, H, V, ignore_index
         self.index_dtype = index_dtype
         self._device(device)

@@ -143,3 +143,20 @@ def test_calls_of_two_threads_keep_their_strides(host, monkeypatch, op):
     _two_calls(*calls)
     assert seen == {x[0].data_ptr(): (72, 80), x[1].data_ptr(): (88, 104)}
     assert (n if op == "norm" else c).dims.T == 6
+
+
+@pytest.mark.parametrize("make", [
+    lambda m: m.LayerNorm((1 << 32) + 4, 64), lambda m: m.LayerNorm(4, (1 << 32) + 64), lambda m: m.LayerNorm(1 << 31, 8),
+    lambda m: m.CrossEntropy((1 << 32) + 4, 64, 100), lambda m: m.CrossEntropy(4, (1 << 32) + 64, 100),
+    lambda m: m.CrossEntropy(4, 64, (1 << 32) + 100), lambda m: m.CrossEntropy(4, 64, 100, ignore_index=1 << 32),
+    lambda m: m.CrossEntropy(4, 64, 100, ignore_index=-(1 << 31) - 1)])
+def test_numbers_past_32_bits_are_refused(host, make):
+    """The library's sizes have 32 bits; what does not fit would be cut to its
+    low ones (4 rows instead of 2^32 + 4, another value ignored)."""
+    with pytest.raises(M.MoEError):
+        make(host)
+
+
+def test_the_ends_of_32_bits_are_taken(host):
+    for ignore in (-(1 << 31), (1 << 31) - 1):
+        assert host.CrossEntropy(4, 64, 100, ignore_index=ignore).dims.ignore_index == ignore
