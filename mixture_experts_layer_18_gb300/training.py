@@ -232,12 +232,12 @@ class CrossEntropy(_Op):
     def backward(self, X, W, targets, dloss, dX, dW, reduction="mean", stream=None):
         """dX and dW (None leaves one out) after ``forward`` on the same inputs.
         dloss: the gradient of each row's loss [T] (reduction "none"), or of
-        their sum or mean [1]."""
+        their sum or mean, [] or [1]."""
         _require(self.with_backward, "CrossEntropy: built with backward=False")
         _require(reduction in REDUCTIONS, "CrossEntropy: reduction is none, sum or mean")
         d, X, W, targets = self._inputs(X, W, targets)
-        n = self.T if reduction == "none" else 1
-        dloss = self._fits("dloss", dloss, (n,), torch.float32)
+        shape = (self.T,) if reduction == "none" else () if getattr(dloss, "ndim", 1) == 0 else (1,)
+        dloss = self._fits("dloss", dloss, shape, torch.float32)
         dX = self._fits_or_none("dX", dX, (self.T, self.H), torch.bfloat16)
         dW = self._fits_or_none("dW", dW, (self.V, self.H), torch.bfloat16)
         _, lse, total = self._out

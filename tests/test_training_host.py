@@ -160,3 +160,25 @@ def test_numbers_past_32_bits_are_refused(host, make):
 def test_the_ends_of_32_bits_are_taken(host):
     for ignore in (-(1 << 31), (1 << 31) - 1):
         assert host.CrossEntropy(4, 64, 100, ignore_index=ignore).dims.ignore_index == ignore
+
+
+def test_gradient_of_a_scalar_loss(host, monkeypatch):
+    """The gradient of the sum or mean has its shape, () or [1]; one per row is [T]."""
+    seen = []
+    monkeypatch.setattr(host, "moe_cross_entropy_backward", lambda *a: seen.append(a[6]) or 0)
+    c = host.CrossEntropy(4, 64, 100)
+    X, W = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((100, 64), dtype=torch.bfloat16)
+    t, io = torch.zeros(4, dtype=torch.int64), c.empty_io()
+
+    def call(d, reduction):
+        c.backward(X, W, t, d, io["dX"], io["dW"], reduction=reduction)
+    for d in (torch.ones(()), torch.ones(1)):
+        for reduction in ("sum", "mean"):
+            call(d, reduction)
+            assert seen[-1] == d.data_ptr()
+    call(torch.ones(4), "none")
+    for d, reduction in ((torch.ones(4), "mean"), (torch.ones(()), "none"), (torch.ones((1, 1)), "sum"),
+                         (torch.ones(()).double(), "mean")):
+        with pytest.raises(M.MoEError):
+            call(d, reduction)
+    assert c.mean.shape == ()
