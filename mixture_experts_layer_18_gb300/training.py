@@ -227,7 +227,7 @@ class CrossEntropy(_Op):
         rc = moe_cross_entropy(d, X, W, targets, *self._out, self.ws.data_ptr(), self.ws.numel(),
                                self.status.data_ptr(), self._current(stream))
         if rc != MOE_OK:
-            raise MoEError(rc, "moe_cross_entropy")
+            self._failed(rc, "moe_cross_entropy", d, X=X, W=W)
 
     def backward(self, X, W, targets, dloss, dX, dW, reduction="mean", stream=None):
         """dX and dW (None leaves one out) after ``forward`` on the same inputs.
@@ -245,7 +245,13 @@ class CrossEntropy(_Op):
                                         dW, self.ws.data_ptr(), self.ws.numel(),
                                         self.status.data_ptr(), self._current(stream))
         if rc != MOE_OK:
-            raise MoEError(rc, "moe_cross_entropy_backward")
+            self._failed(rc, "moe_cross_entropy_backward", d, X=X, W=W, dX=dX, dW=dW)
+
+    def _failed(self, rc, call, d, **addresses):
+        """Names the tensors whose rows do not all start on 16-byte boundaries."""
+        ld = dict(X=d.ld_x, W=d.ld_w)
+        off = [k for k, p in addresses.items() if p and p % 16 or ld.get(k, 0) % 8]
+        raise MoEError(rc, f"{call}: {', '.join(off)}: rows have to start on 16-byte boundaries" if off else call)
 
     def empty_io(self):
         """Output tensors of the backward: dX, dW."""

@@ -182,3 +182,23 @@ def test_gradient_of_a_scalar_loss(host, monkeypatch):
         with pytest.raises(M.MoEError):
             call(d, reduction)
     assert c.mean.shape == ()
+
+
+def test_refusals_name_the_tensor(host):
+    """What the library refuses by its address or its rows' distance is named."""
+    c = host.CrossEntropy(4, 64, 100)
+    b = dict(dtype=torch.bfloat16)
+    X, W, t = torch.zeros((4, 64), **b), torch.zeros((100, 64), **b), torch.zeros(4, dtype=torch.int64)
+    one = torch.ones(1)
+    off = torch.zeros(100 * 64 + 64, **b)
+    off = off[1:]
+    odd = torch.zeros((100, 68), **b)[:, :64]
+    shifted = off[:4 * 64].view(4, 64)
+    assert shifted.data_ptr() % 16
+    for name, call in (("X", lambda: c.forward(shifted, W, t)),
+                       ("W", lambda: c.forward(X, off[:6400].view(100, 64), t)),
+                       ("X", lambda: c.forward(odd[:4], W, t)), ("W", lambda: c.forward(X, odd, t)),
+                       ("dX", lambda: c.backward(X, W, t, one, shifted, None)),
+                       ("dW", lambda: c.backward(X, W, t, one, None, off[:6400].view(100, 64)))):
+        with pytest.raises(M.MoEError, match=rf"\b{name}\b"):
+            call()
