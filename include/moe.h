@@ -344,9 +344,10 @@ typedef enum { MOE_REDUCE_NONE = 0, MOE_REDUCE_SUM = 1, MOE_REDUCE_MEAN = 2 } mo
  *                 (>= H, multiples of 8).
  *   ignore_index  targets with this value do not count (loss 0, gradient 0).
  *   index_type    of targets.
- * Limits: T >= 0, V >= 1, H a positive multiple of 8; other H return
- * MOE_ERR_UNSUPPORTED (TMA rows start on 16-byte boundaries), and so do sizes
- * of 2^28 and more 256 x 256 tiles. */
+ * Limits: 0 <= T <= 2^30, 1 <= V <= 2^30, 1 <= H <= 2^20; H, ld_x and ld_w
+ * multiples of 8 (TMA rows start on 16-byte boundaries); fewer than 2^28
+ * tiles of 256 x 256 in each of [T, V], [T, H] and [V, H].  What passes an
+ * upper limit or is no multiple of 8 returns MOE_ERR_UNSUPPORTED. */
 typedef struct {
   int T, H, V;
   int64_t ld_x, ld_w;
@@ -374,7 +375,8 @@ moe_status moe_cross_entropy(const moe_xent_dims* dims, const void* X, const voi
  * - [v = targets[t]]) for rows that count, 0 for the others,
  *   dX = dz W,  dW = dz^T X.
  * The vocabulary is gone through in pieces: a piece's logits are formed
- * again, its dz is held in bf16, the products accumulate in fp32.
+ * again, its dz is held in bf16 (as a sum of two bf16 numbers where T <= 32),
+ * the products accumulate in fp32.
  *   reduction  s_t: MOE_REDUCE_NONE dloss[t] (dloss float [T]),
  *              MOE_REDUCE_SUM dloss[0], MOE_REDUCE_MEAN dloss[0] / total[2].
  *   lse, total from the forward (total may be NULL unless MEAN).

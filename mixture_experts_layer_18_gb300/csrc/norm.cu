@@ -469,7 +469,10 @@ __global__ void __launch_bounds__(kBlock<L, kFwdThreads>, CPT <= 16 ? 800 / kBlo
 // Rows that the kernel above does not take (too long, or x and y at different
 // offsets from 16-byte boundaries): a block per row, three passes over it (the
 // second and third find most of it in L1 or L2), by vectors where all rows
-// start on 16-byte boundaries (V = kVec), else by elements (V = 1).
+// start on 16-byte boundaries (V = kVec), else by elements (V = 1).  Measured,
+// bf16: 4097 x 2048 with tensors at different offsets 45 us forward and 69
+// backward (4097 x 2049 at one offset 13 and 20); 4000 x 20000 184 and 366 (47 and
+// 71 from HBM).
 template <typename X, int V>
 __device__ __forceinline__ void load_part(const X* p, float (&v)[V]) {
   if constexpr (V == 1) {
@@ -821,9 +824,15 @@ cudaError_t run_bwd(const BwdArgs& a, const Offsets& o, int64_t max_blocks, int*
              SHIFT ? o.period : 1, max_blocks, blocks, s);
 }
 
-// The fewest lanes that hold a row (with SHIFT, one from any place in its
-// first vector) at 16 columns each, 8 in short rows; 512 lanes of 32 columns
-// for rows over 8192.
+// The first of these shapes that holds a row (with SHIFT, one from any place in
+// its first vector): 16 lanes of 8 columns, a warp of 16 columns per lane, then
+// whole warps of 16; 512 lanes of 32 columns for rows over 8192.  (Rows of 129 to
+// 256 columns leave half of their warp idle: 65536 x 256 bf16 takes 16.7 us
+// forward and 27.8 backward, 65536 x 512 24.0 and 39.6.)
+// Over 8192 columns one block of 512 threads fits an SM, its ring holds two rows
+// and the bf16 backward spills: 4000 x 9000 bf16 46 us forward and 91 backward
+// (21 and 32 from HBM), 4000 x 9001 54 and 110; fp32 88 and 186 (42 and 64), its
+// column sums from a read of their own.
 template <typename X, bool SHIFT>
 cudaError_t forward(const FwdArgs& a, const Offsets& o, cudaStream_t s) {
   const int n = SHIFT ? a.H + kVec<X> - 1 : a.H;

@@ -36,7 +36,11 @@
 // Measured (GB300): forward at T = 16384, H = 2048, V = 65536 2.8 ms (1.57
 // PFLOP/s); forward and backward at T = 8192, H = 4096, V = 131072 21.8 ms (1.61
 // PFLOP/s of the 8 T V H products; a library's plain bf16 products sustain 1.70
-// under the power cap); tensor pipe 86 - 90% busy in the backward.  Pieces of
+// under the power cap); tensor pipe 86 - 90% busy in the backward.  H = 2048, V =
+// 32000, where reading W takes 19 us and writing dW as long again: forward of 17
+// to 256 tokens 38 - 43 us (nearly empty tiles, two rounds over the SM pairs),
+// backward of 1 to 32 tokens 118 - 132, of 33 to 256 111 - 127 (W is read for the
+// logits and again for dX, in launches of their own).  Pieces of
 // 256 MB of dz: 64 MB are 8% slower (more adds to dX), 512 MB 1% faster.
 // Sweeps of 8 m-tiles over n: 4, 16 and 32 are 1 - 2% slower.
 #include <cstring>

@@ -26,8 +26,12 @@ inline size_t xent_align(size_t x) { return (x + 255) & ~(size_t)255; }
 // fill one K block and a part of one row tile all the same) it is kept as a sum
 // of two bf16 numbers: where one target's rounding is most of an output's error,
 // it could be twice that of the output's own rounding (one token, V = 1000:
-// 0.0030 against 0.0019 relative; from 64 tokens on it averages out, 0.0020).
-// The second half costs 3 us of 18 at 7 x 512, V = 5000.
+// 0.0030 against 0.0019 relative).  Over all rows of 64 tokens and more that
+// comes to 0.0020; a row of dX alone is as far off as before, and so are both
+// outputs of a long batch in which only a few rows count, since the number of
+// those is not known here.  The second half costs 3 us of 18 at 7 x 512,
+// V = 5000, and 18 of 129 at 32 x 2048, V = 32000; among many tokens it would
+// double the products of dX and dW.
 struct XentBackwardPlan {
   size_t dz, acc, total;   // workspace: dz [rows][piece] bf16, dX's sums [slices][rows][Hp] fp32
   int piece, slices, Hp, rows;

@@ -3,11 +3,14 @@ step: layer norm, cross entropy over a vocabulary, and gradient clipping.
 
 As in ``layer``, PyTorch supplies device memory and the stream; every
 computation is a call into libmoe_gb300.so.  Each class owns the statistics
-and the workspace of one problem shape on one device (an object's calls on
-different streams, or from different threads, have to be ordered by the caller:
-they share those; a LayerNorm with ``backward=False`` has none to share), checks
-the tensors it is given against that shape, and raises ``MoEError`` on any
-non-OK return code and for tensors that do not fit.
+and the workspace of one problem shape on one device, checks the tensors it is
+given against that shape, and raises ``MoEError`` on any non-OK return code, for
+tensors that do not fit and while another device is current.
+
+An object's calls on different streams, or from different threads, have to be
+ordered by the caller, since they share its buffers (a LayerNorm with
+``backward=False`` has none to share); and it has to live until work that it put
+on a stream other than the one it was made on is done.
 """
 from __future__ import annotations
 
