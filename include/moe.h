@@ -2,7 +2,8 @@
  * moe.h - C ABI of the GB300 (sm_103a) dropless mixture-of-experts expert
  * layer: router, permutation builder, grouped expert GEMMs (forward and
  * backward) and the MXFP8 quantiser; and of the operators around the layer in
- * a training step: layer norm, vocabulary cross entropy, gradient clipping.
+ * a training step: routing by scores, layer norm, RMS norm, activations kept in
+ * 8 bits, vocabulary cross entropy, gradient clipping.
  *
  * Sources of the operations (web pages on the method, cited by title and
  * section):
@@ -334,6 +335,159 @@ moe_status moe_layer_norm_backward(const moe_norm_dims* dims, const void* dy, co
                                    const void* gamma, const float* mean, const float* rstd,
                                    void* dx, void* dgamma, void* dbeta, void* ws,
                                    size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Routing by scores: what moe_route does for softmax and top-k, with sigmoid
+ * scores, a bias for balance, groups of experts and gates that need not add up
+ * to one.
+ * ---------------------------------------------------------------------- */
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* For T tokens, E experts, top_k of them per token:
+ *   ld, type     elements from one row of the logits to the next (>= E); their type
+ *   groups       the experts lie in `groups` groups of E / groups neighbours, of
+ *   top_groups   which the best `top_groups` stay in the choice; a group counts
+ *   group_top    as the sum of its group_top (1 or 2) largest values.
+ *                Without groups: 1, 1, 1.
+ *   renormalise  gates are divided by their sum over the chosen experts
+ *   scale        then multiplied by this (finite, > 0).
+ * Limits: T >= 0; 1 <= E <= 1024; 1 <= top_k <= 32; groups <= 32 and a divisor
+ * of E; group_top <= E / groups; top_k <= top_groups * E / groups;
+ * T * top_k + 128 * E < 2^31. */
+typedef struct {
+  int T, E, top_k;
+  int64_t ld;
+  moe_type type;
+  moe_score score;
+  int groups, top_groups, group_top;
+  int renormalise;
+  float scale;
+} moe_router_dims;
+
+/* Bytes of moe_router's workspace; 0 on invalid dims. */
+size_t moe_router_workspace_size(const moe_router_dims* dims);
+
+/* s = softmax over E, or 1 / (1 + exp(-l));  u = s + bias (s without one);
+ * of the groups that stay, the top_k largest u are chosen, in this order (ties:
+ * the lower index);  gate_j = scale * s_j [/ sum of the chosen s].
+ * The choice is that of u in 64 bits, the same on every GPU; without a bias
+ * (and with group_top 1 or no groups) it is that of the logits themselves.
+ *   logits  [T, E] of dims->type, aligned to their element.  A logit of -inf
+ *           masks the expert: whatever its bias it comes after all others, with
+ *           gate 0, and a group with fewer than group_top others after all
+ *           groups that have them.  NaN and +inf read as -inf and are reported
+ *           (MOE_ERR_BAD_INPUT), and so is a token of whose chosen experts all
+ *           are masked (its gates are 0).
+ *   bias    float [E], or NULL.  One that is not finite reads as 0 and is reported.
+ *   out     all seven arrays, for moe_forward and moe_backward as moe_route's.
+ *   ws      moe_router_workspace_size bytes. */
+moe_status moe_router(const moe_router_dims* dims, const void* logits, const float* bias,
+                      const moe_route_out* out, void* ws, size_t ws_bytes, int32_t* dev_status,
+                      void* stream);
+
+/* Gradient of the logits, the choice held fixed (the bias has none): with w the
+ * gates and c the scale,
+ *   sigmoid  dl_j = w_j (1 - s_j) (dgate_j [- sum_i w_i dgate_i / c]),
+ *   softmax, renormalised   dl_j = w_j (dgate_j - sum_i w_i dgate_i / c),
+ *   softmax  dl_i = [i chosen] w_i dgate_i - s_i sum_j w_j dgate_j  for every i
+ * ([..] if renormalised); the other experts get 0.
+ *   route    topk_idx (a token's are distinct) and gate are read.
+ *   logits   as the forward read them.
+ *   dlogits  [T, E] of dims->type, contiguous, fully overwritten. */
+moe_status moe_router_backward(const moe_router_dims* dims, const moe_route_out* route,
+                               const void* logits, const float* dgate, void* dlogits,
+                               int32_t* dev_status, void* stream);
+
+/* out[e] = bias[e] + rate, - rate or unchanged where expert e has fewer
+ * assignments than the mean, more, or as many.  counts int32 [E] (moe_route_out);
+ * out may be bias. */
+moe_status moe_balance_bias(int E, const int32_t* counts, float rate, const float* bias, float* out,
+                            void* stream);
+
+/* ------------------------------------------------------------------------
+ * RMS norm of T rows of H elements, with the residual's addition.
+ *   ld_*    elements from one row to the next (>= H): x; residual; h; y in
+ *           the forward and dy in the backward; dh; dx.
+ *   x_type  of x, residual, h, y, dy, dh and dx;  w_type of gamma and dgamma.
+ *   eps     added to the mean of the squares, finite and >= 0.
+ * Limits: T >= 0, H >= 1.  Pointers need only the alignment of their element
+ * type; rows that all start on 16-byte boundaries run fastest. */
+typedef struct {
+  int T, H;
+  int64_t ld_x, ld_residual, ld_h, ld_y, ld_dh, ld_dx;
+  moe_type x_type, w_type;
+  float eps;
+} moe_rms_dims;
+
+/* h = x + residual,  rstd = 1 / sqrt(sum(h^2) / H + eps),  y = h * rstd * gamma.
+ *   residual  NULL: h is x itself, and the pointer h has to be NULL.
+ *   gamma     [H], NULL for 1.
+ *   h, y      NULL leaves one out.  They may be x or residual (same ld), not
+ *             each other.
+ *   q, scales  NULL, or y as MXFP8 (moe_quantize_mxfp8's rule, axis 1): codes
+ *             uint8 [T, H] and scales uint8 [T, H / 32], contiguous; needs H a
+ *             multiple of 32 and q 16-byte aligned.
+ *   rstd      float [T], written for the backward; NULL leaves it out.
+ * y is taken from the sum in fp32 and its codes from y in fp32: each result is
+ * rounded once.  A NaN gives NaN in its row only; a row whose squares leave the
+ * range of fp32 has rstd 0. */
+moe_status moe_rms_norm(const moe_rms_dims* dims, const void* x, const void* residual,
+                        const void* gamma, void* h, void* y, uint8_t* q, uint8_t* scales,
+                        float* rstd, void* stream);
+
+/* Bytes of the backward's workspace; 0 on invalid dims. */
+size_t moe_rms_norm_workspace_size(const moe_rms_dims* dims);
+
+/* With xh = h * rstd and g = gamma * dy:
+ *   dx = rstd * (g - xh * sum(g * xh) / H) + dh  (of x and of residual alike),
+ *   dgamma = sum over rows of dy * xh.
+ *   h       the forward's sum (x, where it had no residual).
+ *   dh      the gradient that reaches h on other ways, NULL for none.
+ *   dgamma  [H], NULL leaves it out.  With T = 0 it is zero.
+ *   dx may be dy, h or dh (same ld).
+ *   ws      moe_rms_norm_workspace_size bytes, 16-byte aligned (may be NULL
+ *           when dgamma is).
+ * Sums over rows are fp32 in a fixed order (same results in every run). */
+moe_status moe_rms_norm_backward(const moe_rms_dims* dims, const void* dy, const void* h,
+                                 const void* dh, const void* gamma, const float* rstd, void* dx,
+                                 void* dgamma, void* ws, size_t ws_bytes, void* stream);
+
+/* MXFP8 rows (moe_quantize_mxfp8, axis 1) back to numbers of `type`:
+ * dst[r, c] = E4M3(q[r, c]) * 2^(scales[r, c / 32] - 127).
+ *   q, scales  uint8 [R, C] and [R, C / 32], contiguous, q 16-byte aligned; C a
+ *              multiple of 32.
+ *   dst        [R, ld], aligned to its element, ld >= C. */
+moe_status moe_dequantize_mxfp8(const uint8_t* q, const uint8_t* scales, int R, int C, int64_t ld,
+                                moe_type type, void* dst, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Activations in 8 bits between a layer's forward and its backward: X and h13
+ * as MXFP8 (blocks of 32 columns), from which `saved` is made again, so that
+ * layers share one `saved` buffer.  Not for MOE_MXFP8 (MOE_ERR_UNSUPPORTED),
+ * whose saved buffer is in 8 bits for the most part.
+ * ---------------------------------------------------------------------- */
+
+/* Device buffers, each 16-byte aligned; row a of h13 is assignment a's. */
+typedef struct {
+  uint8_t* x_q;        /* [T, H] codes */
+  uint8_t* x_scales;   /* [T, H / 32] */
+  uint8_t* h13_q;      /* [T * top_k, 2I] codes */
+  uint8_t* h13_scales; /* [T * top_k, 2I / 32] */
+} moe_checkpoint;
+
+/* Codes of X and of the h13 that moe_forward left in `saved`
+ * (save_for_backward = 1).  X [T, H]; NULL: x_q and x_scales hold its codes
+ * already (the norm in front of the layer can write them). */
+moe_status moe_checkpoint_save(const moe_dims* dims, const void* X, const moe_route_out* route,
+                               const void* saved, size_t saved_bytes, const moe_checkpoint* ckpt,
+                               int32_t* dev_status, void* stream);
+
+/* Writes x_perm, h13 and act of `saved` (moe_saved_layout) for moe_backward,
+ * from the checkpoint and the same routing. */
+moe_status moe_checkpoint_restore(const moe_dims* dims, const moe_checkpoint* ckpt,
+                                  const moe_route_out* route, void* saved, size_t saved_bytes,
+                                  int32_t* dev_status, void* stream);
 
 typedef enum { MOE_INDEX_I32 = 0, MOE_INDEX_I64 = 1 } moe_index_type;
 typedef enum { MOE_REDUCE_NONE = 0, MOE_REDUCE_SUM = 1, MOE_REDUCE_MEAN = 2 } moe_reduction;

@@ -24,7 +24,10 @@ __all__ = [
     "MOE_REDUCE_MEAN", "moe_norm_dims", "moe_xent_dims", "moe_grad_tensor", "moe_layer_norm",
     "moe_layer_norm_workspace_size", "moe_layer_norm_backward", "moe_cross_entropy",
     "moe_cross_entropy_workspace_size", "moe_cross_entropy_backward", "moe_grad_workspace_size",
-    "moe_grad_norm", "moe_clip_grads",
+    "moe_grad_norm", "moe_clip_grads", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "moe_router_dims", "moe_rms_dims",
+    "moe_checkpoint", "moe_router_workspace_size", "moe_router", "moe_router_backward", "moe_balance_bias",
+    "moe_rms_norm", "moe_rms_norm_workspace_size", "moe_rms_norm_backward", "moe_dequantize_mxfp8",
+    "moe_checkpoint_save", "moe_checkpoint_restore",
     "moe_quantize_mxfp8", "moe_quantize_mxfp8_dual", "moe_status_string", "moe_set_debug", "moe_set_gemm_events", "moe_set_gemm_launch_events", "moe_debug_occupy",
     "MoEError",
 ]
@@ -36,6 +39,7 @@ MOE_WS_ROUTE, MOE_WS_FORWARD, MOE_WS_BACKWARD = 0, 1, 2
 MOE_TYPE_F32, MOE_TYPE_BF16 = 0, 1
 MOE_INDEX_I32, MOE_INDEX_I64 = 0, 1
 MOE_REDUCE_NONE, MOE_REDUCE_SUM, MOE_REDUCE_MEAN = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_DEBUG_NEVER_READY = 1
 MOE_DEBUG_SINGLE_CTA = 2
 MOE_DEBUG_SPLIT_BACKWARD = 4
@@ -70,6 +74,21 @@ class moe_norm_dims(ctypes.Structure):
                 ("x_type", _c_int), ("w_type", _c_int), ("eps", _f32)]
 
 
+class moe_router_dims(ctypes.Structure):
+    _fields_ = [("T", _c_int), ("E", _c_int), ("top_k", _c_int), ("ld", _i64), ("type", _c_int), ("score", _c_int),
+                ("groups", _c_int), ("top_groups", _c_int), ("group_top", _c_int), ("renormalise", _c_int),
+                ("scale", _f32)]
+
+
+class moe_rms_dims(ctypes.Structure):
+    _fields_ = [("T", _c_int), ("H", _c_int), ("ld_x", _i64), ("ld_residual", _i64), ("ld_h", _i64), ("ld_y", _i64),
+                ("ld_dh", _i64), ("ld_dx", _i64), ("x_type", _c_int), ("w_type", _c_int), ("eps", _f32)]
+
+
+class moe_checkpoint(ctypes.Structure):
+    _fields_ = [("x_q", _vp), ("x_scales", _vp), ("h13_q", _vp), ("h13_scales", _vp)]
+
+
 class moe_xent_dims(ctypes.Structure):
     _fields_ = [("T", _c_int), ("H", _c_int), ("V", _c_int), ("ld_x", _i64), ("ld_w", _i64),
                 ("ignore_index", _c_int), ("index_type", _c_int)]
@@ -90,6 +109,9 @@ _PR = ctypes.POINTER(moe_route_out)
 _PN = ctypes.POINTER(moe_norm_dims)
 _PX = ctypes.POINTER(moe_xent_dims)
 _PG = ctypes.POINTER(moe_grad_tensor)
+_PO = ctypes.POINTER(moe_router_dims)
+_PM = ctypes.POINTER(moe_rms_dims)
+_PC = ctypes.POINTER(moe_checkpoint)
 _SIGS = {
     "moe_max_rows": (_i64, [_PD]),
     "moe_workspace_size": (_c_size, [_PD, _c_int]),
@@ -115,6 +137,16 @@ _SIGS = {
     "moe_grad_workspace_size": (_c_size, [_c_int]),
     "moe_grad_norm": (_c_int, [_PG, _c_int, _vp, _vp, _c_size, _vp, _vp]),
     "moe_clip_grads": (_c_int, [_PG, _c_int, _f32, _vp, _vp, _c_size, _vp, _vp]),
+    "moe_router_workspace_size": (_c_size, [_PO]),
+    "moe_router": (_c_int, [_PO, _vp, _vp, _PR, _vp, _c_size, _vp, _vp]),
+    "moe_router_backward": (_c_int, [_PO, _PR, _vp, _vp, _vp, _vp, _vp]),
+    "moe_balance_bias": (_c_int, [_c_int, _vp, _f32, _vp, _vp, _vp]),
+    "moe_rms_norm": (_c_int, [_PM, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_rms_norm_workspace_size": (_c_size, [_PM]),
+    "moe_rms_norm_backward": (_c_int, [_PM, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "moe_dequantize_mxfp8": (_c_int, [_vp, _vp, _c_int, _c_int, _i64, _c_int, _vp, _vp]),
+    "moe_checkpoint_save": (_c_int, [_PD, _vp, _PR, _vp, _c_size, _PC, _vp, _vp]),
+    "moe_checkpoint_restore": (_c_int, [_PD, _PC, _PR, _vp, _c_size, _vp, _vp]),
     "moe_status_string": (ctypes.c_char_p, [_c_int]),
     "moe_set_debug": (None, [_c_int, _i64]),
     "moe_set_gemm_events": (None, [_c_int, _vp, _vp]),
@@ -242,6 +274,48 @@ def moe_grad_norm(tensors, count, norm, ws, ws_bytes, dev_status, stream) -> int
 def moe_clip_grads(tensors, count, max_norm, norm, ws, ws_bytes, dev_status, stream) -> int:
     """tensors: a ctypes array of moe_grad_tensor (host memory)."""
     return lib().moe_clip_grads(tensors, count, max_norm, norm, ws, ws_bytes, dev_status, stream)
+
+
+def moe_router_workspace_size(d: moe_router_dims) -> int:
+    return lib().moe_router_workspace_size(ctypes.byref(d))
+
+
+def moe_router(d, logits, bias, out, ws, ws_bytes, dev_status, stream) -> int:
+    return lib().moe_router(ctypes.byref(d), logits, bias, ctypes.byref(out), ws, ws_bytes, dev_status, stream)
+
+
+def moe_router_backward(d, route, logits, dgate, dlogits, dev_status, stream) -> int:
+    return lib().moe_router_backward(ctypes.byref(d), ctypes.byref(route), logits, dgate, dlogits, dev_status, stream)
+
+
+def moe_balance_bias(E, counts, rate, bias, out, stream) -> int:
+    return lib().moe_balance_bias(E, counts, rate, bias, out, stream)
+
+
+def moe_rms_norm(d, x, residual, gamma, h, y, q, scales, rstd, stream) -> int:
+    return lib().moe_rms_norm(ctypes.byref(d), x, residual, gamma, h, y, q, scales, rstd, stream)
+
+
+def moe_rms_norm_workspace_size(d: moe_rms_dims) -> int:
+    return lib().moe_rms_norm_workspace_size(ctypes.byref(d))
+
+
+def moe_rms_norm_backward(d, dy, h, dh, gamma, rstd, dx, dgamma, ws, ws_bytes, stream) -> int:
+    return lib().moe_rms_norm_backward(ctypes.byref(d), dy, h, dh, gamma, rstd, dx, dgamma, ws, ws_bytes, stream)
+
+
+def moe_dequantize_mxfp8(q, scales, R, C, ld, type, dst, stream) -> int:
+    return lib().moe_dequantize_mxfp8(q, scales, R, C, ld, type, dst, stream)
+
+
+def moe_checkpoint_save(d, X, route, saved, saved_bytes, ckpt, dev_status, stream) -> int:
+    return lib().moe_checkpoint_save(ctypes.byref(d), X, ctypes.byref(route), saved, saved_bytes, ctypes.byref(ckpt),
+                                     dev_status, stream)
+
+
+def moe_checkpoint_restore(d, ckpt, route, saved, saved_bytes, dev_status, stream) -> int:
+    return lib().moe_checkpoint_restore(ctypes.byref(d), ctypes.byref(ckpt), ctypes.byref(route), saved, saved_bytes,
+                                        dev_status, stream)
 
 
 def moe_status_string(code: int) -> str:

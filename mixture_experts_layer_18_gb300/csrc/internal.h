@@ -191,6 +191,41 @@ cudaError_t launch_layer_norm_backward(const NormDesc& d, const void* dy, const 
                                        void* dx, void* dgamma, void* dbeta, float* partial,
                                        cudaStream_t s);
 
+// score_route.cu
+size_t router_workspace_bytes(const moe_router_dims& d);
+cudaError_t launch_router(const moe_router_dims& d, const void* logits, const float* bias, const moe_route_out& o,
+                          int32_t* hist, int32_t* status, cudaStream_t s);
+cudaError_t launch_router_backward(const moe_router_dims& d, const moe_route_out& o, const void* logits,
+                                   const float* dgate, void* dlogits, int32_t* status, cudaStream_t s);
+cudaError_t launch_balance_bias(const int32_t* counts, int E, float rate, const float* bias, float* out,
+                                cudaStream_t s);
+
+// rms.cu, rms_backward.cu (partial: [norm_partial_blocks(T)][H] floats)
+cudaError_t launch_rms_norm(const moe_rms_dims& d, const void* x, const void* res, const void* gamma, void* h,
+                            void* y, uint8_t* q, uint8_t* sf, float* rstd, cudaStream_t s);
+cudaError_t launch_rms_norm_backward(const moe_rms_dims& d, const void* dy, const void* h, const void* dh,
+                                     const void* gamma, const float* rstd, void* dx, void* dgamma, float* partial,
+                                     cudaStream_t s);
+
+// checkpoint.cu
+struct CheckpointDesc {
+  int T, H, I, E, k, elem_bytes;
+  const void* X;
+  void* x_perm;
+  void* h13;
+  void* act;
+  uint8_t *x_q, *x_s, *h_q, *h_s;
+  const float* gate;           // null: `act` is not gated
+  const int32_t* row_of_assign;
+  const int32_t* assign_of_row;
+  const int32_t* padded_offsets;
+  int32_t* status;
+};
+cudaError_t launch_checkpoint_save(const CheckpointDesc& d, cudaStream_t s);
+cudaError_t launch_checkpoint_restore(const CheckpointDesc& d, cudaStream_t s);
+cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* sf, int R, int C, int64_t ld, int type, void* dst,
+                              cudaStream_t s);
+
 // clip.cu
 size_t grad_workspace_bytes(int count);
 cudaError_t launch_grad_clip(const moe_grad_tensor* t, int count, bool clip, float max_norm,

@@ -318,6 +318,27 @@ moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_E
   } while (0)
 
 
+// ----------------------------------------------------------- checkpoints
+moe_status checkpoint_check(const moe_dims* d, const moe_route_out* r, const void* saved, size_t saved_bytes,
+                            const moe_checkpoint* c, const int32_t* dev_status) {
+  if (!dims_ok(d) || !d->save_for_backward || !route_ok(r, d->T) || !c || !aligned16(saved) || !aligned16(dev_status))
+    return MOE_ERR_INVALID_ARG;
+  if (d->mode == MOE_MXFP8) return MOE_ERR_UNSUPPORTED;
+  if (saved_bytes < saved_layout(d).total) return MOE_ERR_INVALID_ARG;
+  if (d->T > 0 && (!aligned16(c->x_q) || !aligned16(c->x_scales) || !aligned16(c->h13_q) || !aligned16(c->h13_scales)))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+CheckpointDesc checkpoint_desc(const moe_dims* d, const moe_route_out* r, void* saved, const moe_checkpoint* c,
+                               int32_t* dev_status) {
+  const moe_saved_layout sl = saved_layout(d);
+  char* sv = static_cast<char*>(saved);
+  return CheckpointDesc{d->T, d->H, d->I, d->E, d->top_k, elem_bytes(d), nullptr, sv + sl.x_perm, sv + sl.h13,
+                        sv + sl.act, c->x_q, c->x_scales, c->h13_q, c->h13_scales,
+                        d->mode == MOE_BF16 ? r->gate : nullptr, r->row_of_assign, r->assign_of_row,
+                        r->padded_offsets, dev_status};
+}
+
 // ---------------------------------------------------------------- MXFP8
 // Every GEMM operand is quantised along that GEMM's contraction axis into
 // E4M3 codes plus scale atoms laid out for the tensor cores (quant.cu,
@@ -936,6 +957,25 @@ moe_status moe_quantize_mxfp8_dual(const void* src, int R, int C, int ld,
     return MOE_ERR_INVALID_ARG;
   MOE_TRY(launch_quantize_dual(src, R, C, ld, rows_limit, q_row, s_row, q_col, s_col,
                                static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_checkpoint_save(const moe_dims* d, const void* X, const moe_route_out* r, const void* saved,
+                               size_t saved_bytes, const moe_checkpoint* c, int32_t* dev_status, void* stream) {
+  const moe_status st = checkpoint_check(d, r, saved, saved_bytes, c, dev_status);
+  if (st != MOE_OK) return st;
+  if (X && !aligned16(X)) return MOE_ERR_INVALID_ARG;
+  CheckpointDesc k = checkpoint_desc(d, r, const_cast<void*>(saved), c, dev_status);
+  k.X = X;
+  MOE_TRY(launch_checkpoint_save(k, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_checkpoint_restore(const moe_dims* d, const moe_checkpoint* c, const moe_route_out* r, void* saved,
+                                  size_t saved_bytes, int32_t* dev_status, void* stream) {
+  const moe_status st = checkpoint_check(d, r, saved, saved_bytes, c, dev_status);
+  if (st != MOE_OK) return st;
+  MOE_TRY(launch_checkpoint_restore(checkpoint_desc(d, r, saved, c, dev_status), static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -9,12 +9,16 @@ from __future__ import annotations
 
 import torch
 
-from . import (MOE_BF16, MOE_F32, MOE_FP8_BWD, MOE_MXFP8, MOE_OK, MOE_WS_BACKWARD,
-               MOE_WS_FORWARD, MOE_WS_ROUTE, MoEError, moe_backward, moe_dims, moe_forward,
+from . import (MOE_BF16, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_F32, MOE_FP8_BWD, MOE_MXFP8,
+               MOE_OK, MOE_WS_BACKWARD, MOE_WS_FORWARD, MOE_WS_ROUTE, MoEError, moe_backward,
+               moe_checkpoint, moe_checkpoint_restore, moe_checkpoint_save, moe_dims, moe_forward,
                moe_max_rows, moe_route, moe_route_backward, moe_route_out, moe_saved_layout_of,
                moe_workspace_size)
 
 MODES = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "fp8_bwd": MOE_FP8_BWD}
+
+
+_current_device = torch._C._cuda_getDevice
 
 
 def _ptr(t):
@@ -104,21 +108,35 @@ class MoELayer:
         if rc != MOE_OK:
             raise MoEError(rc, "moe_route")
 
-    def forward(self, X, W13, W2, Y, stream=None, save=None):
+    def _route(self, route):
+        """The routing of a call: the layer's own, or that of a Router of the same
+        tokens, experts and top_k (it has to be on this device)."""
+        if route is None:
+            return self.route_out
+        if (route.T, route.E, route.k) != (self.T, self.E, self.k):
+            raise MoEError(MOE_ERR_INVALID_ARG, f"route: expected T, E, top_k = {self.T}, {self.E}, {self.k}; got "
+                                                f"{route.T}, {route.E}, {route.k}")
+        if route.device != self.gate.device:
+            raise MoEError(MOE_ERR_INVALID_ARG, f"route: expected {self.gate.device}; got {route.device}")
+        return route.route_out
+
+    def forward(self, X, W13, W2, Y, stream=None, save=None, route=None):
         """save: None = the layer's setting; False = inference / checkpointed
-        first pass (h13 not kept); True = keep h13 for moe_backward."""
+        first pass (h13 not kept); True = keep h13 for moe_backward.
+        route: a training.Router that holds the routing, in place of the
+        layer's own (``route`` above)."""
         dims = self.dims
         if save is not None and bool(save) != bool(self.dims.save_for_backward):
             dims = moe_dims(self.dims.T, self.dims.H, self.dims.E, self.dims.I, self.dims.top_k,
                             self.dims.mode, 1 if save else 0)
-        rc = moe_forward(dims, _ptr(X), _ptr(W13), _ptr(W2), self.route_out, _ptr(Y),
+        rc = moe_forward(dims, _ptr(X), _ptr(W13), _ptr(W2), self._route(route), _ptr(Y),
                          _ptr(self.saved), self.saved.numel(), _ptr(self.ws_fwd),
                          self.ws_fwd.numel(), _ptr(self.status), _stream(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_forward")
 
-    def backward(self, dY, W13, W2, dX, dW13, dW2, dgate, stream=None):
-        rc = moe_backward(self.dims, _ptr(dY), _ptr(W13), _ptr(W2), self.route_out,
+    def backward(self, dY, W13, W2, dX, dW13, dW2, dgate, stream=None, route=None):
+        rc = moe_backward(self.dims, _ptr(dY), _ptr(W13), _ptr(W2), self._route(route),
                           _ptr(self.saved), self.saved.numel(), _ptr(dX), _ptr(dW13), _ptr(dW2),
                           _ptr(dgate), _ptr(self.ws_bwd), self.ws_bwd.numel(),
                           _ptr(self.status), _stream(stream))
@@ -131,6 +149,43 @@ class MoELayer:
         if rc != MOE_OK:
             raise MoEError(rc, "moe_route_backward")
 
+    # -------------------------------------------------------- checkpoints
+    def checkpoint(self):
+        """Buffers that keep one forward's activations in 8 bits (not in mxfp8
+        mode)."""
+        return Checkpoint(self)
+
+    def _checkpoint(self, checkpoint, X=None):
+        if (checkpoint.T, checkpoint.H, checkpoint.I, checkpoint.k) != (self.T, self.H, self.I, self.k):
+            raise MoEError(MOE_ERR_INVALID_ARG, "checkpoint: made for a layer of other sizes")
+        if checkpoint.device != self.gate.device:
+            raise MoEError(MOE_ERR_INVALID_ARG, f"checkpoint: expected {self.gate.device}; got {checkpoint.device}")
+        if _current_device() != self.gate.device.index:
+            raise MoEError(MOE_ERR_INVALID_ARG, f"called for {self.gate.device}, but another device is current")
+        if X is not None and (X.dtype != self.dtype or tuple(X.shape) != (self.T, self.H) or not X.is_contiguous()
+                              or X.device != self.gate.device):
+            raise MoEError(MOE_ERR_INVALID_ARG, f"X: expected contiguous {self.dtype} [{self.T}, {self.H}] on "
+                                                f"{self.gate.device}")
+        return checkpoint.pointers
+
+    def save(self, checkpoint, X=None, stream=None, route=None):
+        """After ``forward``: X and h13 into the checkpoint, in 8 bits.  X None:
+        ``checkpoint.x`` holds its codes already (RMSNorm.forward(encoded=) wrote
+        them).  Another forward may then use the layer's buffers."""
+        rc = moe_checkpoint_save(self.dims, None if X is None else _ptr(X), self._route(route), _ptr(self.saved),
+                                 self.saved.numel(), self._checkpoint(checkpoint, X), _ptr(self.status),
+                                 _stream(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_checkpoint_save")
+
+    def restore(self, checkpoint, stream=None, route=None):
+        """Before ``backward``: the saved activations of the checkpoint's
+        forward, whose routing ``route`` (or the layer's own) still has to hold."""
+        rc = moe_checkpoint_restore(self.dims, self._checkpoint(checkpoint), self._route(route), _ptr(self.saved),
+                                    self.saved.numel(), _ptr(self.status), _stream(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_checkpoint_restore")
+
     # --------------------------------------------------------- allocation
     def empty_io(self):
         """Output tensors of one forward + backward: Y, dX, dW13, dW2, dgate."""
@@ -142,3 +197,19 @@ class MoELayer:
             dW2=torch.empty((self.E, self.I, self.H), dtype=dt, device=dev),
             dgate=torch.empty((self.T, self.k), dtype=torch.float32, device=dev),
         )
+
+
+class Checkpoint:
+    """One forward's activations in 8 bits: the layer's input ``x`` [T, H], and
+    ``h13`` [T * top_k, 2I] in the order of the assignments (training.MXRows)."""
+
+    def __init__(self, layer):
+        from .training import MXRows
+        if layer.mode == "mxfp8":
+            raise MoEError(MOE_ERR_UNSUPPORTED, "checkpoint: the mxfp8 mode saves most activations in 8 bits")
+        self.T, self.H, self.I, self.k = layer.T, layer.H, layer.I, layer.k
+        self.device = layer.gate.device
+        self.x, self.h13 = MXRows(self.T, self.H, self.device), MXRows(self.T * self.k, 2 * self.I, self.device)
+        self._kept = (self.x, self.h13)          # (whatever becomes of the names)
+        self.pointers = moe_checkpoint(_ptr(self.x.codes), _ptr(self.x.scales), _ptr(self.h13.codes),
+                                       _ptr(self.h13.scales))

@@ -1,5 +1,6 @@
 """Caller-side buffers of the operators around the expert layer in a training
-step: layer norm, cross entropy over a vocabulary, and gradient clipping.
+step: routing by scores, layer norm, RMS norm, rows in MXFP8, cross entropy over
+a vocabulary, and gradient clipping.
 
 As in ``layer``, PyTorch supplies device memory and the stream; every
 computation is a call into libmoe_gb300.so.  Each class owns the statistics
@@ -17,15 +18,19 @@ from __future__ import annotations
 import torch
 
 from . import (MOE_ERR_INVALID_ARG, MOE_INDEX_I32, MOE_INDEX_I64, MOE_OK, MOE_REDUCE_MEAN,
-               MOE_REDUCE_NONE, MOE_REDUCE_SUM, MOE_TYPE_BF16, MOE_TYPE_F32, MOE_WS_BACKWARD,
-               MOE_WS_FORWARD, MoEError, moe_clip_grads, moe_cross_entropy,
-               moe_cross_entropy_backward, moe_cross_entropy_workspace_size, moe_grad_norm,
-               moe_grad_tensor, moe_grad_workspace_size, moe_layer_norm, moe_layer_norm_backward,
-               moe_layer_norm_workspace_size, moe_norm_dims, moe_xent_dims)
+               MOE_REDUCE_NONE, MOE_REDUCE_SUM, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_TYPE_BF16,
+               MOE_TYPE_F32, MOE_WS_BACKWARD, MOE_WS_FORWARD, MoEError, moe_balance_bias, moe_clip_grads,
+               moe_cross_entropy, moe_cross_entropy_backward, moe_cross_entropy_workspace_size,
+               moe_dequantize_mxfp8, moe_grad_norm, moe_grad_tensor, moe_grad_workspace_size,
+               moe_layer_norm, moe_layer_norm_backward, moe_layer_norm_workspace_size, moe_norm_dims,
+               moe_quantize_mxfp8, moe_rms_dims, moe_rms_norm, moe_rms_norm_backward,
+               moe_rms_norm_workspace_size, moe_route_out, moe_router, moe_router_backward,
+               moe_router_dims, moe_router_workspace_size, moe_xent_dims)
 from .layer import _ptr
 
 TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
 INDEX_TYPES = {torch.int32: MOE_INDEX_I32, torch.int64: MOE_INDEX_I64}
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 REDUCTIONS = {"none": MOE_REDUCE_NONE, "sum": MOE_REDUCE_SUM, "mean": MOE_REDUCE_MEAN}
 
 
@@ -179,6 +184,189 @@ class LayerNorm(_Op):
         w = dict(dtype=self.weight_dtype, device=self.device)
         return dict(y=torch.empty((self.T, self.H), **x), dx=torch.empty((self.T, self.H), **x),
                     dgamma=torch.empty(self.H, **w), dbeta=torch.empty(self.H, **w))
+
+
+class RMSNorm(_Op):
+    """RMS norm of [T, H] rows with the residual's addition, float32 or bfloat16,
+    with weights of either type.  All row tensors may be slices of wider buffers."""
+
+    def __init__(self, T, H, dtype=torch.bfloat16, weight_dtype=None, eps=1e-6, device="cuda", backward=True):
+        weight_dtype = dtype if weight_dtype is None else weight_dtype
+        _require(dtype in TYPES and weight_dtype in TYPES, "RMSNorm: float32 or bfloat16")
+        _require_int32("RMSNorm", T, H)
+        self.T, self.H, self.dtype, self.weight_dtype, self.eps = T, H, dtype, weight_dtype, eps
+        self._device(device)
+        self.shape = torch.Size((T, H))
+        self._described = (None, None)
+        need = moe_rms_norm_workspace_size(self._dims(H, H, H, H, H, H))
+        _require(need > 0, "RMSNorm: invalid sizes")
+        self.rstd = torch.empty(T, dtype=torch.float32, device=self.device) if backward else None
+        self.ws = torch.empty(need if backward else 0, dtype=torch.uint8, device=self.device)
+        self._keep(self.rstd, self.ws)
+        self._rstd = _ptr(self.rstd)
+
+    def _dims(self, *lds):
+        """As LayerNorm's."""
+        known = self._described
+        if known[0] != lds:
+            known = self._described = (lds, moe_rms_dims(self.T, self.H, *lds, TYPES[self.dtype],
+                                                         TYPES[self.weight_dtype], self.eps))
+        return known[1]
+
+    def _rows_or_none(self, name, t):
+        return (None, self.H) if t is None else self._rows(name, t, self.shape, self.dtype)
+
+    def forward(self, x, gamma, y=None, residual=None, h=None, encoded=None, stream=None):
+        """h = x + residual, y = h / rms(h) * gamma; gamma may be None (1).  Of h
+        (only with a residual), y and encoded (an MXRows: y in 8 bits) those that
+        are given are written."""
+        x, ld_x = self._rows("x", x, self.shape, self.dtype)
+        residual, ld_r = self._rows_or_none("residual", residual)
+        h, ld_h = self._rows_or_none("h", h)
+        y, ld_y = self._rows_or_none("y", y)
+        gamma = self._fits_or_none("gamma", gamma, self.shape[1:], self.weight_dtype)
+        q, scales = (None, None) if encoded is None else encoded._pointers("encoded", self)
+        _require(h is None or residual is not None, "RMSNorm: h is x itself without a residual")
+        rc = moe_rms_norm(self._dims(ld_x, ld_r, ld_h, ld_y, self.H, self.H), x, residual, gamma, h, y, q, scales,
+                          self._rstd, self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_rms_norm")
+
+    def backward(self, dy, h, gamma, dx, dgamma=None, dh=None, stream=None):
+        """dx (of x and of residual) and dgamma (None leaves it out) of the last
+        forward, whose sum is h; dh: the gradient that reaches h on other ways."""
+        _require(self.rstd is not None, "RMSNorm: built with backward=False")
+        dy, ld_dy = self._rows("dy", dy, self.shape, self.dtype)
+        h, ld_h = self._rows("h", h, self.shape, self.dtype)
+        dh, ld_dh = self._rows_or_none("dh", dh)
+        dx, ld_dx = self._rows("dx", dx, self.shape, self.dtype)
+        gamma = self._fits_or_none("gamma", gamma, self.shape[1:], self.weight_dtype)
+        dgamma = self._fits_or_none("dgamma", dgamma, self.shape[1:], self.weight_dtype)
+        rc = moe_rms_norm_backward(self._dims(self.H, self.H, ld_h, ld_dy, ld_dh, ld_dx), dy, h, dh, gamma,
+                                   self._rstd, dx, dgamma, self.ws.data_ptr(), self.ws.numel(),
+                                   self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_rms_norm_backward")
+
+    def empty_io(self):
+        """Output tensors: y, h, dx, dgamma."""
+        x = dict(dtype=self.dtype, device=self.device)
+        return dict(y=torch.empty((self.T, self.H), **x), h=torch.empty((self.T, self.H), **x),
+                    dx=torch.empty((self.T, self.H), **x),
+                    dgamma=torch.empty(self.H, dtype=self.weight_dtype, device=self.device))
+
+
+class MXRows(_Op):
+    """[rows, cols] numbers as MXFP8: ``codes`` (E4M3, uint8) and a scale per 32
+    columns, ``scales`` (E8M0, uint8)."""
+
+    def __init__(self, rows, cols, device="cuda"):
+        _require_int32("MXRows", rows, cols)
+        _require(rows >= 0 and cols >= 0 and cols % 32 == 0, "MXRows: columns in blocks of 32")
+        self.rows, self.cols = rows, cols
+        self._device(device)
+        u8 = dict(dtype=torch.uint8, device=self.device)
+        self.codes, self.scales = torch.empty((rows, cols), **u8), torch.empty((rows, cols // 32), **u8)
+        self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self._keep(self.codes, self.scales, self.status)
+        self._at = (_ptr(self.codes), _ptr(self.scales))
+
+    def _pointers(self, name, op):
+        """The addresses, for an operator whose rows they are to be."""
+        if (self.rows, self.cols) != (op.T, op.H) or self.index != op.index:
+            raise MoEError(MOE_ERR_INVALID_ARG, f"{name}: expected [{op.T}, {op.H}] on {op.device}; got "
+                                                f"[{self.rows}, {self.cols}] on {self.device}")
+        return self._at
+
+    def encode(self, x, stream=None):
+        """From bfloat16 rows that start on 16-byte boundaries."""
+        x, ld = self._rows("x", x, (self.rows, self.cols), torch.bfloat16)
+        _require(ld < 1 << 31, "MXRows: rows less than 2^31 elements apart")
+        rc = moe_quantize_mxfp8(x, self.rows, self.cols, ld, 1, None, 0, *self._at, self.status.data_ptr(),
+                                self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_quantize_mxfp8")
+
+    def decode(self, out, stream=None):
+        """The values into bfloat16 or float32 rows."""
+        dtype = getattr(out, "dtype", None)
+        _require(dtype in TYPES, "MXRows: float32 or bfloat16")
+        out, ld = self._rows("out", out, (self.rows, self.cols), dtype)
+        rc = moe_dequantize_mxfp8(*self._at, self.rows, self.cols, ld, TYPES[dtype], out, self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_dequantize_mxfp8")
+
+
+class Router(_Op):
+    """Routing of T tokens to top_k of E experts by softmax or sigmoid scores,
+    with a bias for balance, groups of experts, and gates that are renormalised
+    or not, times ``scale``.  After ``forward`` the arrays of moe_route_out
+    (``topk_idx``, ``gate``, ``counts``, ...) hold the routing, which
+    ``MoELayer.forward`` and ``backward`` take as ``route``."""
+
+    def __init__(self, T, E, top_k, score="softmax", groups=1, top_groups=1, group_top=1, renormalise=True,
+                 scale=1.0, dtype=torch.float32, device="cuda"):
+        _require(dtype in TYPES, "Router: float32 or bfloat16 logits")
+        _require(score in SCORES, "Router: softmax or sigmoid")
+        _require_int32("Router", T, E, top_k, groups, top_groups, group_top)
+        self.T, self.E, self.k, self.dtype = T, E, top_k, dtype
+        self._how = (TYPES[dtype], SCORES[score], groups, top_groups, group_top, 1 if renormalise else 0, scale)
+        self._device(device)
+        self._described = (None, None)
+        need = moe_router_workspace_size(self._dims(E))
+        _require(need > 0, "Router: invalid sizes")
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.topk_idx = torch.empty((T, top_k), **i32)
+        self.gate = torch.empty((T, top_k), dtype=torch.float32, device=self.device)
+        self.counts = torch.empty(E, **i32)
+        self.offsets = torch.empty(E + 1, **i32)
+        self.padded_offsets = torch.empty(E + 1, **i32)
+        self.row_of_assign = torch.empty(T * top_k, **i32)
+        self.assign_of_row = torch.empty(T * top_k + 128 * E, **i32)
+        self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        self.status = torch.zeros(4, **i32)
+        arrays = (self.topk_idx, self.gate, self.counts, self.offsets, self.padded_offsets, self.row_of_assign,
+                  self.assign_of_row)
+        self._keep(*arrays, self.ws, self.status)
+        self.route_out = moe_route_out(*map(_ptr, arrays))
+        self._shape, self._counts, self._status = torch.Size((T, E)), self.counts.data_ptr(), self.status.data_ptr()
+        self._ws = (self.ws.data_ptr(), need)
+
+    def _dims(self, ld):
+        """As LayerNorm's."""
+        known = self._described
+        if known[0] != ld:
+            known = self._described = (ld, moe_router_dims(self.T, self.E, self.k, ld, *self._how))
+        return known[1]
+
+    def forward(self, logits, bias=None, stream=None):
+        """logits [T, E] (a slice of a wider buffer too); bias [E] float32 or None."""
+        logits, ld = self._rows("logits", logits, self._shape, self.dtype)
+        bias = self._fits_or_none("bias", bias, self._shape[1:], torch.float32)
+        rc = moe_router(self._dims(ld), logits, bias, self.route_out, *self._ws, self._status,
+                        self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_router")
+
+    def backward(self, logits, dgate, dlogits, stream=None):
+        """dlogits [T, E] of the last forward's logits, from dgate [T, top_k]."""
+        logits, ld = self._rows("logits", logits, self._shape, self.dtype)
+        dgate = self._fits("dgate", dgate, (self.T, self.k), torch.float32)
+        dlogits = self._fits("dlogits", dlogits, self._shape, self.dtype)
+        rc = moe_router_backward(self._dims(ld), self.route_out, logits, dgate, dlogits, self._status,
+                                 self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_router_backward")
+
+    def update_bias(self, bias, rate, out=None, stream=None):
+        """Moves the bias by ``rate`` towards an even load, by the last forward's
+        counts: in place, or into ``out``."""
+        shape = self._shape[1:]
+        bias = self._fits("bias", bias, shape, torch.float32)
+        out = bias if out is None else self._fits("out", out, shape, torch.float32)
+        rc = moe_balance_bias(self.E, self._counts, rate, bias, out, self._current(stream))
+        if rc != MOE_OK:
+            raise MoEError(rc, "moe_balance_bias")
 
 
 class CrossEntropy(_Op):

@@ -1,6 +1,6 @@
 """Float64 definitions of the operators around the expert layer in a training
-step (test infrastructure only): layer norm, softmax cross entropy over a
-vocabulary, the global gradient norm and clipping.  Plain numpy, written from
+step (test infrastructure only): routing by scores, layer norm, RMS norm, softmax
+cross entropy over a vocabulary, the global gradient norm and clipping.  Plain numpy, written from
 the formulas; nothing here is shared with the CUDA path."""
 from __future__ import annotations
 
@@ -75,3 +75,86 @@ def clip_grads(tensors, max_norm):
     n = grad_norm(tensors)
     c = max_norm / n if n > max_norm else 1.0
     return n, [np.asarray(t, np.float64) * c for t in tensors]
+
+
+def _readable(logits):
+    """NaN and +inf read as -inf (a masked expert)."""
+    l = np.asarray(logits, np.float64)
+    return np.where(np.isnan(l) | (l == np.inf), -np.inf, l)
+
+
+def scores(logits, score):
+    """s [T, E]; 0 for masked experts."""
+    l = _readable(logits)
+    if score == "sigmoid":
+        with np.errstate(over="ignore"):
+            return 1.0 / (1.0 + np.exp(-l))
+    top = l.max(1, keepdims=True)
+    e = np.exp(l - np.where(np.isfinite(top), top, 0.0))
+    return e / np.maximum(e.sum(1, keepdims=True), 1e-300)
+
+
+def route_by_scores(logits, bias, k, score="softmax", groups=1, top_groups=1, group_top=1, renormalise=True,
+                    scale=1.0):
+    """(idx, gate) [T, k], by sorting with Python."""
+    l = _readable(logits)
+    T, E = l.shape
+    size = E // groups
+    s = scores(l, score)
+    b = np.zeros(E) if bias is None else np.where(np.isfinite(bias), np.asarray(bias, np.float64), 0.0)
+    by_logit = bias is None and (groups == 1 or group_top == 1)
+    u = l if by_logit else np.where(np.isfinite(l), s + b, -np.inf)
+    idx = np.zeros((T, k), np.int64)
+    for t in range(T):
+        value = [sum(sorted(u[t, g * size:(g + 1) * size])[::-1][:group_top]) for g in range(groups)]
+        stay = sorted(range(groups), key=lambda g: (-value[g], g))[:top_groups]
+        eligible = [e for e in range(E) if e // size in stay]
+        idx[t] = sorted(eligible, key=lambda e: (-u[t, e], e))[:k]
+    ls = np.take_along_axis(l, idx, 1)
+    if renormalise:
+        x = -np.logaddexp(0, -ls) if score == "sigmoid" else ls
+        top = x.max(1, keepdims=True)
+        w = np.exp(x - np.where(np.isfinite(top), top, 0.0))
+        w = w / np.maximum(w.sum(1, keepdims=True), 1e-300)
+    else:
+        w = np.take_along_axis(s, idx, 1)
+    return idx, scale * w
+
+
+def route_by_scores_backward(logits, idx, gate, dgate, score="softmax", renormalise=True, scale=1.0):
+    """dlogits [T, E] with the choice held fixed."""
+    l, dg = _readable(logits), np.asarray(dgate, np.float64)
+    inner = (gate * dg).sum(1, keepdims=True)
+    out = np.zeros_like(l)
+    d = gate * (dg - inner / scale) if renormalise else gate * dg
+    if score == "sigmoid":
+        with np.errstate(over="ignore"):
+            d = d / (1.0 + np.exp(np.take_along_axis(l, idx, 1)))
+    elif not renormalise:
+        out = -scores(l, score) * inner
+    np.put_along_axis(out, idx, np.take_along_axis(out, idx, 1) + d, 1)
+    return out
+
+
+def balance_bias(counts, rate, bias):
+    counts = np.asarray(counts, np.int64)
+    return np.asarray(bias, np.float64) + rate * np.sign(counts.sum() - counts * len(counts))
+
+
+def rms_norm(x, residual, gamma, eps):
+    """(h, y, rstd)."""
+    h = np.asarray(x, np.float64)
+    if residual is not None:
+        h = h + np.asarray(residual, np.float64)
+    rstd = 1.0 / np.sqrt((h * h).mean(1) + eps)
+    y = h * rstd[:, None]
+    return h, y if gamma is None else y * np.asarray(gamma, np.float64), rstd
+
+
+def rms_norm_backward(dy, h, gamma, rstd, dh=None):
+    """(dx, dgamma)."""
+    dy, h = np.asarray(dy, np.float64), np.asarray(h, np.float64)
+    xh = h * np.asarray(rstd, np.float64)[:, None]
+    g = dy if gamma is None else dy * np.asarray(gamma, np.float64)
+    dx = np.asarray(rstd)[:, None] * (g - xh * (g * xh).mean(1)[:, None])
+    return dx if dh is None else dx + np.asarray(dh, np.float64), (dy * xh).sum(0)

@@ -1,0 +1,312 @@
+"""Routing by scores on the GPU against its float64 definition.
+
+The choice and the permutation are exact.  Gates and gradients: U = 2^-24 is the
+unit roundoff of fp32.  Renormalised gates come from x = log s, whose error is
+below U (2 |x| + 4); the difference to the largest, its exponential, the sum of up
+to 32, the quotient and the scale add 2 |x| + 20 units, so a gate is within
+U (4 max |x| + 24) of its value.  A softmax gate that is not renormalised divides
+by a sum of exponentials that are off by (4 + 2 |x|) U, weighted with themselves
+(at most log E on average), added up in at most 32 + 5 steps, and its own
+exponential is off by (2 + |x|) U: U (80 + 2 |x|) with |x| the distance to the
+largest logit.  Gradients carry the gates' error, twice where a sum of their
+products enters, and a dozen roundings of their own."""
+import numpy as np
+import pytest
+
+from oracle import moe_oracle as M
+from oracle import training_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def _device(a, dtype=None):
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def _gate_tol(l, idx, gate, score, renorm):
+    """Relative tolerance of the gates [T, k]."""
+    ls = np.take_along_axis(l, idx, 1)
+    fin = np.isfinite(ls)
+    if renorm:
+        x = np.where(fin, -np.logaddexp(0, -np.where(fin, ls, 0)) if score == "sigmoid" else ls, 0)
+        return U * (4 * np.abs(x).max(1, keepdims=True) + 24) + 0 * gate
+    if score == "sigmoid":
+        return np.full_like(gate, 8 * U)
+    top = l.max(1, keepdims=True)
+    return U * (80 + 2 * np.where(fin, np.where(np.isfinite(top), top, 0) - np.where(fin, ls, 0), 0))
+
+
+def _check(l, bias, k, router, dgate=None, dlogits=None, **how):
+    """The router's arrays against the definition for float32 logits l (numpy)."""
+    E = l.shape[1]
+    idx, gate = O.route_by_scores(l, bias, k, **how)
+    got = router.topk_idx.cpu().numpy()
+    assert np.array_equal(got, idx), np.argwhere((got != idx).any(1))[:4].ravel()
+    r = O._readable(l)
+    score, renorm, scale = how.get("score", "softmax"), how.get("renormalise", True), how.get("scale", 1.0)
+    tol = _gate_tol(r, idx, gate, score, renorm)
+    # (below the smallest normal number a gate may be flushed)
+    assert (np.abs(router.gate.double().cpu().numpy() - gate) <= tol * gate + scale * 2e-38).all()
+    m = M.permute(idx, E)
+    for name in ("counts", "offsets", "padded_offsets", "row_of_assign"):
+        assert np.array_equal(getattr(router, name).cpu().numpy(), m[name]), name
+    a = router.assign_of_row.cpu().numpy()
+    n = int(m["padded_offsets"][-1])
+    assert np.array_equal(a[:n], m["assign_of_row"][:n]) and (a[n:] == -1).all()
+    if dlogits is None:
+        return
+    dg = np.asarray(dgate, np.float64)
+    want = O.route_by_scores_backward(l, idx, gate, dg, score, renorm, scale)
+    out = dlogits.double().cpu().numpy()
+    stored = 2.0 ** -8 if str(dlogits.dtype) == "torch.bfloat16" else U
+    size = (np.abs(gate * dg)).sum(1, keepdims=True)            # of the sum of products
+    t = np.zeros_like(want)
+    own = np.abs(gate * dg) + (gate * size / scale if renorm else 0)
+    np.put_along_axis(t, idx, own, 1)
+    if score == "softmax" and not renorm:
+        t = t + O.scores(l, score) * size
+    k_u = 2 * tol.max(1, keepdims=True) + 100 * U
+    assert (np.abs(out - want) <= stored * np.abs(want) + (1 + stored) * k_u * t + 2e-38).all(), np.abs(out - want).max()
+
+
+def _run(l, bias, k, dtype=None, pad=0, seed=0, **how):
+    import torch
+    from mixture_experts_layer_18_gb300.training import Router
+    T, E = l.shape
+    dt = torch.float32 if dtype is None else getattr(torch, dtype)
+    wide = torch.full((T, E + pad), 77.0, dtype=dt, device="cuda")
+    x = wide[:, :E]
+    x.copy_(_device(l.astype(np.float32)))
+    l = x.float().cpu().numpy()                                  # as stored
+    r = Router(T, E, k, dtype=dt, **how)
+    for a in (r.topk_idx, r.gate, r.counts, r.offsets, r.padded_offsets, r.row_of_assign, r.assign_of_row):
+        a.fill_(-7)
+    dg = np.random.default_rng(seed + 1).standard_normal((T, k)).astype(np.float32)
+    dl = torch.full((T, E), 5.0, dtype=dt, device="cuda")
+    b = None if bias is None else _device(np.asarray(bias, np.float32))
+    r.forward(x, b)
+    r.backward(x, _device(dg), dl)
+    torch.cuda.synchronize()
+    return l, r, dg, dl
+
+
+# every lane width, one expert, odd counts, groups that lie across lanes; a few and
+# many tokens (one warp each, blocks of 32 warps, several tokens per warp)
+CASES = [
+    (1, 1, 1, {}), (1, 256, 8, dict(score="sigmoid", groups=8, top_groups=4, group_top=2)),
+    (5, 7, 7, dict(score="sigmoid")), (33, 32, 32, dict(renormalise=False)), (64, 33, 3, {}),
+    (257, 60, 6, dict(renormalise=False)), (1000, 64, 4, dict(groups=4, top_groups=3, group_top=1)),
+    (700, 96, 5, dict(score="sigmoid", groups=6, top_groups=2, group_top=2, scale=2.5)),
+    (2049, 128, 8, dict(renormalise=False, scale=0.5)), (513, 160, 6, dict(groups=8, top_groups=3, group_top=2)),
+    (5000, 256, 8, dict(score="sigmoid", groups=8, top_groups=4, group_top=2, scale=2.5)),
+    (611, 257, 9, dict(score="sigmoid", renormalise=False)), (300, 512, 16, dict(groups=32, top_groups=5, group_top=1)),
+    (97, 1000, 31, dict(score="sigmoid", groups=10, top_groups=7, group_top=2)), (40, 1024, 32, dict(score="sigmoid")),
+    (700, 24, 2, dict(groups=12, top_groups=1, group_top=2, renormalise=False)),
+]
+
+
+@pytest.mark.parametrize("T,E,k,how", CASES)
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("dtype,pad", [("float32", 0), ("bfloat16", 3), ("float32", 5)])
+def test_router_matches_definition(T, E, k, how, biased, dtype, pad):
+    rng = np.random.default_rng(T + E)
+    l = rng.standard_normal((T, E)) * 1.5
+    bias = (1e-3 * rng.integers(-80, 81, E)).astype(np.float32) if biased else None
+    l, r, dg, dl = _run(l, bias, k, dtype, pad, **how)
+    _check(l, bias, k, r, dg, dl, **how)
+    assert r.device_status() == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_close_values_are_chosen_in_64_bits(score, groups):
+    """Values apart by less than fp32 can tell: the bias makes up for the score's
+    difference up to its own last bits."""
+    rng = np.random.default_rng(11)
+    T, E = 400, 64
+    l = (rng.integers(-3, 4, (T, E)) + rng.integers(0, 9, (T, E)) * 2.0 ** -22).astype(np.float32)
+    level = O.scores(l[:1], score)[0]
+    bias = (0.5 - level).astype(np.float32)                      # token 0: all values within 2^-24 of 1/2
+    l[1::2] = l[0]
+    l[1::2] += rng.integers(0, 3, (T // 2, E)).astype(np.float32) * np.float32(2.0 ** -22)
+    how = dict(score=score, groups=groups, top_groups=max(1, groups // 2), group_top=2 if groups > 1 else 1)
+    l, r, dg, dl = _run(l, bias, 6, **how)
+    _check(l, bias, 6, r, dg, dl, **how)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [None, 0.0, 0.25])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_ties_go_to_the_lower_index(score, bias, groups):
+    """Equal logits (a router of zeros, logits of few values) with equal biases."""
+    rng = np.random.default_rng(5)
+    l = rng.integers(0, 2, (300, 40)).astype(np.float32)
+    l[:50] = 0.0
+    l[50:60] = -0.0
+    l[60:70, ::2] = -0.0
+    b = None if bias is None else np.full(40, bias, np.float32)
+    how = dict(score=score, groups=groups, top_groups=max(1, groups // 2), group_top=2 if groups > 1 else 1)
+    l, r, dg, dl = _run(l, b, 7, **how)
+    _check(l, b, 7, r, dg, dl, **how)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_masked_experts(score, renorm):
+    """-inf and the type's lowest value in masked places, tokens with fewer
+    experts than top_k, with none, and groups left empty; large logits."""
+    rng = np.random.default_rng(6)
+    l = rng.standard_normal((200, 32)).astype(np.float32)
+    l[:60][rng.random((60, 32)) < 0.5] = -np.inf
+    l[60:90, 8:] = -np.inf
+    l[90:100, 2:] = -np.inf
+    l[100:130][rng.random((30, 32)) < 0.5] = np.finfo(np.float32).min
+    l[130:150] *= 200
+    how = dict(score=score, renormalise=renorm)
+    for bias, more in ((None, {}), (rng.standard_normal(32).astype(np.float32), {}),
+                       (None, dict(groups=4, top_groups=2, group_top=1))):
+        x, r, dg, dl = _run(l, bias, 4, **how, **more)
+        if bias is None:
+            _check(x, bias, 4, r, dg, dl, **how, **more)
+        else:
+            # (scores of the lowest value are 0 in 64 bits, like those of logits below -745)
+            _check(x, bias, 4, r, dg, dl, **how, **more)
+        assert r.device_status() == 0
+
+
+def test_bad_logits_are_reported():
+    """A token of masked experts only, NaN, +inf, a bias that is not finite: read
+    as masked (as 0), reported, and the other tokens are as without them."""
+    from mixture_experts_layer_18_gb300 import MOE_ERR_BAD_INPUT
+    rng = np.random.default_rng(7)
+    base = rng.standard_normal((50, 32)).astype(np.float32)
+    b = (0.1 * rng.standard_normal(32)).astype(np.float32)
+    for bad in ("row", "nan", "inf", "bias"):
+        for score in ("softmax", "sigmoid"):
+            l, bias = base.copy(), b.copy()
+            if bad == "row":
+                l[7] = -np.inf
+            elif bad == "bias":
+                bias[3], bias[9] = np.nan, np.inf
+            else:
+                l[7, 5] = np.nan if bad == "nan" else np.inf
+            l, r, dg, dl = _run(l, bias, 4, score=score)
+            _check(l, bias, 4, r, dg, dl, score=score)
+            assert r.device_status() == MOE_ERR_BAD_INPUT
+            if bad == "row":
+                assert r.topk_idx[7].tolist() == [0, 1, 2, 3] and not r.gate[7].any() and not dl[7].any()
+
+
+def test_no_tokens():
+    import torch
+    from mixture_experts_layer_18_gb300.training import Router
+    r = Router(0, 16, 2)
+    for a in (r.counts, r.offsets, r.padded_offsets, r.assign_of_row):
+        a.fill_(9)
+    x = torch.zeros((0, 16), device="cuda")
+    r.forward(x)
+    r.backward(x, torch.zeros((0, 2), device="cuda"), torch.zeros((0, 16), device="cuda"))
+    torch.cuda.synchronize()
+    assert not r.counts.any() and not r.offsets.any() and not r.padded_offsets.any() and (r.assign_of_row == -1).all()
+
+
+def test_many_tokens_are_placed_in_order():
+    """More assignments per block than one round of the permutation takes."""
+    rng = np.random.default_rng(8)
+    l = rng.standard_normal((70001, 16)).astype(np.float32)
+    l[:, 3] += 3
+    x = _device(l)
+    import torch
+    from mixture_experts_layer_18_gb300.training import Router
+    r = Router(70001, 16, 4)
+    r.forward(x)
+    idx = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :4].cpu().numpy()
+    assert np.array_equal(r.topk_idx.cpu().numpy(), idx)
+    m = M.permute(idx, 16)
+    assert np.array_equal(r.row_of_assign.cpu().numpy(), m["row_of_assign"])
+    assert np.array_equal(r.counts.cpu().numpy(), m["counts"])
+
+
+def test_the_softmax_router_is_the_layers():
+    """Without the extras: the layer's own router, array by array."""
+    import torch
+    from mixture_experts_layer_18_gb300.layer import MoELayer
+    from mixture_experts_layer_18_gb300.training import Router
+    g = torch.Generator(device="cuda").manual_seed(3)
+    l = torch.randn((1003, 48), generator=g, device="cuda")
+    L, r = MoELayer(1003, 64, 48, 64, 5, backward=False), Router(1003, 48, 5)
+    L.route(l)
+    r.forward(l)
+    torch.cuda.synchronize()
+    for name in ("topk_idx", "counts", "offsets", "padded_offsets", "row_of_assign", "assign_of_row"):
+        assert torch.equal(getattr(L, name), getattr(r, name)), name
+    assert (L.gate - r.gate).abs().max() <= 60 * U
+
+
+def test_balance_bias():
+    import torch
+    from mixture_experts_layer_18_gb300.training import Router
+    rng = np.random.default_rng(9)
+    l = rng.standard_normal((640, 20)).astype(np.float32)
+    b = (1e-3 * rng.integers(-9, 9, 20)).astype(np.float32)
+    r = Router(640, 20, 2, score="sigmoid")
+    t, out = _device(b), torch.empty(20, device="cuda")
+    r.forward(_device(l), t)
+    r.update_bias(t, 1e-3, out=out)
+    want = O.balance_bias(r.counts.cpu().numpy(), np.float64(np.float32(1e-3)), b)
+    assert np.array_equal(t.cpu().numpy(), b)
+    assert (np.abs(out.double().cpu().numpy() - want) <= U * np.abs(want)).all()
+    r.counts.fill_(64)                                            # an even load: unchanged
+    r.update_bias(t, 1e-3)
+    assert np.array_equal(t.cpu().numpy(), b)
+    r.counts.copy_(torch.arange(20, dtype=torch.int32) * 100_000_000)     # sums past 32 bits
+    r.update_bias(t, 1e-3)
+    assert (t[:10].cpu().numpy() > b[:10]).all() and (t[10:].cpu().numpy() < b[10:]).all()
+
+
+def test_captured_router_and_a_second_stream():
+    """Replays follow the inputs; on a stream of its own the call waits for none."""
+    import torch
+    from mixture_experts_layer_18_gb300.training import Router
+    rng = np.random.default_rng(10)
+    how = dict(score="sigmoid", groups=4, top_groups=2, group_top=2)
+    l = [rng.standard_normal((777, 64)).astype(np.float32) for _ in range(3)]
+    b = (0.01 * rng.standard_normal(64)).astype(np.float32)
+    r = Router(777, 64, 6, **how)
+    x, t, dg, dl = _device(l[0]), _device(b), _device(rng.standard_normal((777, 6)).astype(np.float32)), \
+        torch.empty((777, 64), device="cuda")
+    r.forward(x, t)
+    r.backward(x, dg, dl)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r.forward(x, t)
+        r.backward(x, dg, dl)
+    for v in l[1:]:
+        x.copy_(_device(v))
+        graph.replay()
+        torch.cuda.synchronize()
+        _check(v, b, 6, r, dg.cpu().numpy(), dl, **how)
+    s = torch.cuda.Stream()
+    x.copy_(_device(l[0]))
+    s.wait_stream(torch.cuda.current_stream())
+    r.forward(x, t, stream=s)
+    r.backward(x, dg, dl, stream=s)
+    s.synchronize()
+    _check(l[0], b, 6, r, dg.cpu().numpy(), dl, **how)
+
+
+def test_bad_index_in_the_backward():
+    from mixture_experts_layer_18_gb300 import MOE_ERR_BAD_INDEX
+    l, r, dg, dl = _run(np.random.default_rng(1).standard_normal((9, 12)).astype(np.float32), None, 2)
+    keep = dl.clone()
+    r.topk_idx[4, 1] = 12
+    r.topk_idx[5, 0] = -3
+    r.backward(_device(l), _device(dg), dl)
+    assert r.device_status() == MOE_ERR_BAD_INDEX
+    rows = [i for i in range(9) if i not in (4, 5)]
+    assert (dl[rows] == keep[rows]).all()
