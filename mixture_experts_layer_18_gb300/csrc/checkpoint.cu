@@ -77,8 +77,8 @@ struct CkptArgs {
   uint8_t* h_s;
   const float* gate;        // restore, null where `act` is not gated
   const int32_t* row_of_assign;
-  const int32_t* assign_of_row;
   const int32_t* padded_offsets;
+  const int32_t* counts;
   int64_t n_assign;
   int T, H, I, E, k;
   int32_t* status;
@@ -156,11 +156,20 @@ __global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(const __grid_con
   X* act = static_cast<X*>(a.act);
   constexpr int kStep = 2;                 // steps of 256 columns of each half of h13 in a unit
   const int nx = (a.H + kUnit - 1) / kUnit, nh = (a.I + 256 * kStep - 1) / (256 * kStep);
-  const int64_t ux = (int64_t)a.T * nx, all = ux + a.n_assign * nh;
+  const int64_t up = (int64_t)a.E * kAlign, ux = up + (int64_t)a.T * nx, all = ux + a.n_assign * nh;
   for (int64_t u = global_warp(); u < all; u += grid_warps()) {
+    if (u < up) {                          // the i-th row behind an expert's, as the forward leaves it
+      const int e = (int)(u / kAlign);
+      const int64_t r = (int64_t)a.padded_offsets[e] + a.counts[e] + u % kAlign;
+      if (r >= a.padded_offsets[e + 1] || r < 0 || r >= rows) continue;
+      zero_row(x_perm + r * a.H, a.H, lane);
+      zero_row(h13 + r * 2 * a.I, 2 * a.I, lane);
+      zero_row(act + r * a.I, a.I, lane);
+      continue;
+    }
     if (u < ux) {
-      const int64_t t = u / nx;
-      const int c0 = (int)(u - t * nx) * kUnit;
+      const int64_t t = (u - up) / nx;
+      const int c0 = (int)(u - up - t * nx) * kUnit;
       int my = -1;                         // lane j < k: the row of slot j
       if (lane < a.k) {
         my = a.row_of_assign[t * a.k + lane];
@@ -231,20 +240,6 @@ __global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(const __grid_con
       store8(act + (int64_t)r * a.I + c, x);
     }
   }
-  // pad rows, as the forward leaves them
-  for (int64_t rb = global_warp() * 32; rb < rows; rb += grid_warps() * 32) {
-    const int64_t r = rb + lane;
-    const int n = r < rows ? a.assign_of_row[r] : 0;
-    if (r < rows && n >= a.n_assign) report(a.status, MOE_ERR_BAD_INDEX);
-    unsigned m = __ballot_sync(kAll, r < rows && (n < 0 || n >= a.n_assign));
-    while (m) {
-      const int64_t p = rb + __ffs(m) - 1;
-      m &= m - 1;
-      zero_row(x_perm + p * a.H, a.H, lane);
-      zero_row(h13 + p * 2 * a.I, 2 * a.I, lane);
-      zero_row(act + p * a.I, a.I, lane);
-    }
-  }
 }
 
 // Rows of codes back to numbers; VEC: rows of dst start on 16-byte boundaries.
@@ -293,8 +288,8 @@ unsigned blocks_for(int64_t units) {
 }
 
 CkptArgs ckpt_args(const CheckpointDesc& d) {
-  return CkptArgs{d.X, d.x_perm, d.h13, d.act, d.x_q, d.x_s, d.h_q, d.h_s, d.gate, d.row_of_assign, d.assign_of_row,
-                  d.padded_offsets, (int64_t)d.T * d.k, d.T, d.H, d.I, d.E, d.k, d.status};
+  return CkptArgs{d.X, d.x_perm, d.h13, d.act, d.x_q, d.x_s, d.h_q, d.h_s, d.gate, d.row_of_assign, d.padded_offsets,
+                  d.counts, (int64_t)d.T * d.k, d.T, d.H, d.I, d.E, d.k, d.status};
 }
 
 }  // namespace
@@ -311,7 +306,8 @@ cudaError_t launch_checkpoint_save(const CheckpointDesc& d, cudaStream_t s) {
 cudaError_t launch_checkpoint_restore(const CheckpointDesc& d, cudaStream_t s) {
   if (d.T == 0) return cudaSuccess;
   const CkptArgs a = ckpt_args(d);
-  const int64_t units = (int64_t)d.T * ((d.H + kUnit - 1) / kUnit) + a.n_assign * ((d.I + 511) / 512);
+  const int64_t units = (int64_t)d.E * kAlign + (int64_t)d.T * ((d.H + kUnit - 1) / kUnit) +
+                        a.n_assign * ((d.I + 511) / 512);
   return d.elem_bytes == 2
              ? launch_overlapped(ckpt_restore_kernel<__nv_bfloat16>, blocks_for(units), kThreads, 0, s, a)
              : launch_overlapped(ckpt_restore_kernel<float>, blocks_for(units), kThreads, 0, s, a);

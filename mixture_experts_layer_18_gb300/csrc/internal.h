@@ -217,8 +217,8 @@ struct CheckpointDesc {
   uint8_t *x_q, *x_s, *h_q, *h_s;
   const float* gate;           // null: `act` is not gated
   const int32_t* row_of_assign;
-  const int32_t* assign_of_row;
   const int32_t* padded_offsets;
+  const int32_t* counts;
   int32_t* status;
 };
 cudaError_t launch_checkpoint_save(const CheckpointDesc& d, cudaStream_t s);

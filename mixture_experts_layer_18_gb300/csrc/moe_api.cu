@@ -335,8 +335,8 @@ CheckpointDesc checkpoint_desc(const moe_dims* d, const moe_route_out* r, void* 
   char* sv = static_cast<char*>(saved);
   return CheckpointDesc{d->T, d->H, d->I, d->E, d->top_k, elem_bytes(d), nullptr, sv + sl.x_perm, sv + sl.h13,
                         sv + sl.act, c->x_q, c->x_scales, c->h13_q, c->h13_scales,
-                        d->mode == MOE_BF16 ? r->gate : nullptr, r->row_of_assign, r->assign_of_row,
-                        r->padded_offsets, dev_status};
+                        d->mode == MOE_BF16 ? r->gate : nullptr, r->row_of_assign, r->padded_offsets,
+                        r->counts, dev_status};
 }
 
 // ---------------------------------------------------------------- MXFP8

@@ -6,12 +6,17 @@
 //   best groups stay; the k largest u in them are chosen (ties: the lower
 //   index), and gate_j = scale s_j, or scale s_j / sum of the chosen s.
 //
-// The choice is that of u in 64 bits, whatever the GPU: values are computed in
-// fp32 and compared, and a token in which two values that a comparison decides
-// between lie within the error of fp32 (kNear) is done again in 64 bits by its
-// warp.  (About one token in a thousand with 256 sigmoid scores; fp64 for all
-// would take 30 times the time that the logits take from HBM.)  Without a bias
-// u orders as the logits do, which are compared themselves.
+// The choice is that of u in 64 bits, whatever the GPU, found in three steps:
+//   - keys of 32 bits that hold the leading bits of u in fp32 and the expert's
+//     index, all different, so that a round of the choice is one warp maximum
+//     (about 250 instructions a token where comparing values and indices took 750);
+//   - where two values that the choice turns on are not told apart by these bits and
+//     the error of fp32 (near_of): the token's values in full fp32, and those that
+//     are still too close as pairs of fp32 numbers (choose32);
+//   - where more than a warp's worth of values are too close, or pairs of fp32 numbers
+//     do not tell: all of the token in 64 bits (choose64).  fp64 for every value would
+//     take 30 times the time that the logits take from HBM.
+// Without a bias u orders as the logits do, which are compared themselves.
 //
 // One warp per token, C neighbouring experts per lane, so that a group is a
 // segment of lanes and the logits arrive in vectors.
@@ -48,7 +53,7 @@ __device__ __forceinline__ F warp_sum(F v) {
   return v;
 }
 
-// exp(x) by one MUFU instruction: relative error below 2^-22 + |x| 2^-23.
+// exp(x) by one MUFU instruction: relative error below 2^-22 + 1.4 |x| 2^-24.
 __device__ __forceinline__ float fast_exp(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504088896341f));
@@ -61,7 +66,8 @@ struct ScoreArgs {
   int64_t ld;
   int T, E, k, per_block;
   int groups, group_size, top_groups, group_top;
-  int sigmoid, renorm;
+  int seg, seg_log;         // lanes of a group where it is 2^seg_log whole lanes, else 0
+  int sigmoid, renorm, vec;
   float scale;
   int32_t* idx;
   float* gate;
@@ -171,162 +177,790 @@ __device__ __noinline__ int choose64(const ScoreArgs& a, const X* row) {
   return mine;
 }
 
+// A lane's C neighbouring logits of a row as they lie in memory: by vectors of up
+// to 16 bytes, where rows start on their boundaries and E is whole vectors, else by
+// elements.
+template <typename X, int C>
+struct Logits {
+  static constexpr int kBytes = C * (int)sizeof(X), kVec = kBytes < 16 ? kBytes : 16;
+  static constexpr int N = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const X* row, int E, bool vec) {
+    const int e0 = (threadIdx.x & 31) * C;
+    if (vec && kBytes >= 4) {
+#pragma unroll
+      for (int i = 0; i < kBytes / kVec; ++i) {
+        if (e0 + i * (kVec / (int)sizeof(X)) >= E) continue;
+        const X* p = row + e0 + i * (kVec / (int)sizeof(X));
+        if constexpr (kVec == 16) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+          w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        } else if constexpr (kVec == 8) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+          w[0] = v.x; w[N - 1] = v.y;
+        } else {
+          w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < C; ++q) {
+        if (e0 + q >= E) continue;
+        if constexpr (sizeof(X) == 4) {
+          w[q] = __float_as_uint(row[e0 + q]);
+        } else {
+          const uint32_t v = __bfloat16_as_ushort(row[e0 + q]);
+          w[q / 2] = q & 1 ? (w[q / 2] & 0xffffu) | v << 16 : v;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int q) const {
+    return sizeof(X) == 4 ? __uint_as_float(w[q % N]) : q & 1 ? bf16_hi(w[(q / 2) % N]) : bf16_lo(w[(q / 2) % N]);
+  }
+};
+
 // Largest distance of two fp32 values u that may be in the other order (or
-// equal) in 64 bits.  Sigmoid: fast_exp's error enters as s (1 - s) (2^-22 +
-// |l| 2^-23), at most 2^-24 + 2^-25; the sum, the reciprocal and the bias round
-// by 2^-24, 2^-23 and 2^-24 |u|: below 2^-22 (1 + |u|) each, 2^-21 a pair, taken
-// twice.  Softmax: as much relative to the largest score, and the sum's own
-// relative error (fast_exp's, and C + 5 additions): below 2^-19.
-__device__ __forceinline__ float near_of(bool sigmoid, float largest_s, float u) {
-  return (sigmoid ? 0x1p-20f : 0x1p-18f * largest_s) + 0x1p-20f * fabsf(u);
+// equal) in 64 bits; `s` bounds the scores (1, or the largest of the softmax), `u`
+// the values.  In units of 2^-24: fast_exp is off by 4 + 1.4 |x| relative to its value.
+// Sigmoid: that enters as s (1 - s), at most 1 + 0.3; 1 + exp rounds by 1, the
+// reciprocal by 2, the bias' addition by |u|: below 5 + |u| each.  Softmax, relative to
+// the largest score: 4 + 0.9 of the exponential (its argument rounds too), 4 + 2.4 ln E of
+// the sum's terms, C + 4 of their addition, 3 of the quotient: below 32 + C.
+template <int C>
+__device__ __forceinline__ float near_of(bool sigmoid, float s, float u) {
+  return (sigmoid ? 10 * 0x1p-24f : (64 + 2 * C) * 0x1p-24f * s) + 0x1p-23f * fabsf(u);
 }
 
+// The best two keys of a lane with their places (of equal ones the first).
+template <int C>
+struct BestTwo {
+  uint32_t m1, m2;
+  int q1, q2;
+  __device__ __forceinline__ void take(const uint32_t (&key)[C]) {
+    m1 = key[0];
+    q1 = 0;
+    m2 = 0;
+    q2 = 0;
+#pragma unroll
+    for (int q = 1; q < C; ++q) {
+      const bool a = key[q] > m1, b = key[q] > m2;
+      m2 = a ? m1 : b ? key[q] : m2;
+      q2 = a ? q1 : b ? q : q2;
+      m1 = a ? key[q] : m1;
+      q1 = a ? q : q1;
+    }
+  }
+  // takes the best away; the next after the second is looked for again
+  __device__ __forceinline__ void pop(const uint32_t (&key)[C]) {
+    const uint32_t last = m1;
+    const int at = q1;
+    m1 = m2;
+    q1 = q2;
+    m2 = 0;
+    if (m1 == 0) {
+#pragma unroll
+      for (int q = C - 1; q >= 0; --q)
+        if ((key[q] < last || (key[q] == last && q > at)) && key[q] >= m1) {
+          m1 = key[q];
+          q1 = q;
+        }
+    }
+  }
+};
+
+// ------------------------------------------------- pairs of fp32 numbers
+// h + l with |l| at most half a unit of h: 46 to 48 significant bits from fp32
+// instructions (the sums and products of Dekker and Knuth), for the values that fp32
+// cannot order.  (fp64 took 7 to 9 us for two values and 43 for a row of 256.)
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair sum_of(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair normal(float h, float l) {            // |h| >= |l|
+  const float s = __fadd_rn(h, l);
+  return {s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = sum_of(a.h, b.h), t = sum_of(a.l, b.l);
+  const Pair u = normal(s.h, __fadd_rn(s.l, t.h));
+  return normal(u.h, __fadd_rn(u.l, t.l));
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const float p = __fmul_rn(a.h, b.h);
+  float e = __fmaf_rn(a.h, b.h, -p);
+  e = __fmaf_rn(a.h, b.l, e);
+  e = __fmaf_rn(a.l, b.h, e);
+  return normal(p, e);
+}
+__device__ __forceinline__ Pair inverse(Pair d) {
+  const float y = __frcp_rn(d.h);
+  const float e = __fmaf_rn(-d.l, y, __fmaf_rn(-d.h, y, 1.f));
+  return normal(y, __fmul_rn(y, e));
+}
+// exp(x), -80 <= x <= 0, relative error below 2^-40: x - n ln 2 (ln 2 in three parts,
+// the first of 15 bits, so that its product with n is exact), a 16th of that in the
+// Taylor series up to the 7th power (the rest is below 2^-59), squared four times.
+__device__ __forceinline__ Pair exp_of(Pair x) {
+  const float n = rintf(x.h * 1.44269504f);
+  Pair r = sum_of(x.h, -n * 0x1.62e4p-1f);
+  r = add(r, {x.l, 0.f});
+  const float p = __fmul_rn(n, -0x1.7f7d1cp-20f), pe = __fmaf_rn(n, -0x1.7f7d1cp-20f, -p);
+  r = add(r, normal(p, __fmaf_rn(n, -0x1.ef357ap-45f, pe)));
+  r.h *= 0.0625f;
+  r.l *= 0.0625f;
+  const float t = fmaf(fmaf(1.f / 5040, r.h, 1.f / 720), r.h, 1.f / 120);
+  Pair y = normal(0x1.555556p-5f, fmaf(r.h, t, -0x1.555556p-30f));    // 1/24 + ...
+  y = add(mul(y, r), {0x1.555556p-3f, -0x1.555556p-28f});              // 1/6
+  y = add(mul(y, r), {0.5f, 0.f});
+  y = add(mul(y, r), {1.f, 0.f});
+  y = add(mul(y, r), {1.f, 0.f});
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y = mul(y, y);
+  const float f = __uint_as_float((uint32_t)(127 + (int)n) << 23);     // n >= -116
+  return {y.h * f, y.l * f};
+}
+// What a candidate is compared by: its value, and how far off that may be.
+struct Exact {
+  Pair u;
+  float off;                // infinite: not known to this precision
+};
+__device__ __forceinline__ Exact exact_of(float s_h, float s_l, float b, bool known) {
+  const Pair t = sum_of(s_h, b);
+  const Pair u = normal(t.h, __fadd_rn(t.l, s_l));
+  return {u, known ? 0x1p-39f * s_h + 0x1p-44f * fabsf(u.h) : INFINITY};
+}
+
+// A token's softmax (largest logit and sum of exponentials relative to it); u:
+// this lane's logits.
+template <int C>
+__device__ __forceinline__ void softmax_of(const float (&u)[C], float* top, float* sum) {
+  float m = u[0];
+#pragma unroll
+  for (int q = 1; q < C; ++q) m = fmaxf(m, u[q]);
+  m = value_of(__reduce_max_sync(kAll, key_of(m)));
+  m = m > -INFINITY ? m : 0.f;
+  float s = 0.f;
+#pragma unroll
+  for (int q = 0; q < C; ++q) s += fast_exp(u[q] - m);
+  *top = m;
+  *sum = warp_sum(s);
+}
+__device__ __forceinline__ float score_of(const ScoreArgs& a, float l, float top, float inv_sum) {
+  return a.sigmoid ? __fdividef(1.f, 1.f + fast_exp(-l)) : fast_exp(l - top) * inv_sum;
+}
+
+// u of one candidate of each lane (logit l, bias b) of this row.
+template <typename X, int C>
+__device__ __noinline__ Exact exact_value(const ScoreArgs& a, const X* row, float l, float b, float top) {
+  if (a.sigmoid) {
+    const Pair e = exp_of({fmaxf(-fabsf(l), -80.f), 0.f});
+    const Pair inv = inverse(add({1.f, 0.f}, e)), s = l >= 0.f ? inv : mul(e, inv);
+    return exact_of(s.h, s.l, b, fabsf(l) < 80.f);
+  }
+  Pair sum{0.f, 0.f};
+  bool bad = false;
+#pragma unroll 1
+  for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+    const Pair x = sum_of(logit(a, row, e, &bad), -top);
+    if (x.h > -80.f) sum = add(sum, exp_of(x));
+  }
+#pragma unroll 1
+  for (int o = 16; o; o >>= 1) sum = add(sum, {__shfl_xor_sync(kAll, sum.h, o), __shfl_xor_sync(kAll, sum.l, o)});
+  const Pair x = sum_of(l, -top);
+  const Pair s = mul(exp_of(x.h > -80.f ? x : Pair{-80.f, 0.f}), inverse(sum));
+  return exact_of(s.h, s.l, b, x.h > -80.f);
+}
+
+// The order of n candidates, one per lane (expert e, logit l, bias b): from fp32, and
+// where that does not tell from pairs of it.  Returns the lane's expert in that order;
+// -1 to all lanes if pairs do not tell either.
+template <typename X, int C>
+__device__ __noinline__ int order(const ScoreArgs& a, const X* row, int e, float l, float b, int n, float top, float inv,
+                                  uint2* slot) {
+  const int lane = threadIdx.x & 31;
+  const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
+  const bool on = lane < n && l > -INFINITY;
+  const float v = !on || by_logit ? l : score_of(a, l, top, inv) + b;
+  int better = 0;
+  bool unsure = false;
+  for (int i = 0; i < n; ++i) {
+    const float ov = __shfl_sync(kAll, v, i), ol = __shfl_sync(kAll, l, i), ob = __shfl_sync(kAll, b, i);
+    const int oe = __shfl_sync(kAll, e, i);
+    const bool other = ol > -INFINITY;
+    const float gap = by_logit ? 0.f : near_of<C>(a.sigmoid, inv, fmaxf(fabsf(v), fabsf(ov)));
+    if (oe == e) continue;
+    if ((ol == l && ob == b) || (!on && !other)) better += oe < e;
+    else if (!on || !other) better += other;               // masked ones last
+    else if (fabsf(ov - v) > gap || by_logit) better += ov > v || (ov == v && oe < e);
+    else unsure = true;
+  }
+  if (__any_sync(kAll, lane < n && unsure)) {
+    const Exact x = exact_value<X, C>(a, row, l, b, top);
+    better = 0;
+    unsure = false;
+    for (int i = 0; i < n; ++i) {
+      const float oh = __shfl_sync(kAll, x.u.h, i), olow = __shfl_sync(kAll, x.u.l, i);
+      const float off = __shfl_sync(kAll, x.off, i) + x.off;
+      const float ol = __shfl_sync(kAll, l, i), ob = __shfl_sync(kAll, b, i);
+      const int oe = __shfl_sync(kAll, e, i);
+      const bool other = ol > -INFINITY;
+      if (oe == e) continue;
+      const float d = (oh - x.u.h) + (olow - x.u.l);
+      if ((ol == l && ob == b) || (!on && !other)) better += oe < e;
+      else if (!on || !other) better += other;
+      else if (fabsf(d) > off) better += d > 0.f;
+      else unsure = true;
+    }
+    if (__any_sync(kAll, lane < n && unsure)) return -1;
+  }
+  __syncwarp();
+  if (lane < n) slot[better].y = e;
+  __syncwarp();
+  return lane < n ? slot[lane].y : 0;
+}
+
+// Whether this lane's group `own` is among the best: l0, b0, l1, b1 are logits and
+// biases of its best one or two (live: none masked), lane g << log has group g's.
+template <typename X, int C>
+__device__ __noinline__ bool better_groups(const ScoreArgs& a, const X* row, float l0, float b0, float l1, float b1,
+                                           bool live, int own, int log, float top, bool unsure, bool* sure) {
+  if (!live) l0 = b0 = 0.f;
+  if (!live || a.group_top == 1) l1 = b1 = 0.f;
+  const Exact x0 = exact_value<X, C>(a, row, l0, b0, top);
+  Pair mine = x0.u;
+  float off = x0.off;
+  if (a.group_top == 2) {
+    const Exact x1 = exact_value<X, C>(a, row, l1, b1, top);
+    mine = add(x0.u, x1.u);
+    off += x1.off + 0x1p-44f * (fabsf(x0.u.h) + fabsf(x1.u.h));
+  }
+  int better = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    // (every lane takes part in every exchange: none of them behind a condition)
+    const int at = g << log;
+    const bool ol = __shfl_sync(kAll, (int)live, at);
+    const float oh = __shfl_sync(kAll, mine.h, at), olow = __shfl_sync(kAll, mine.l, at);
+    const float oo = __shfl_sync(kAll, off, at) + off;
+    const float m0 = __shfl_sync(kAll, l0, at), m1 = __shfl_sync(kAll, l1, at);
+    const float n0 = __shfl_sync(kAll, b0, at), n1 = __shfl_sync(kAll, b1, at);
+    const bool same = m0 == l0 && m1 == l1 && n0 == b0 && n1 == b1;
+    if (g == own || own >= a.groups) continue;
+    const float d = (oh - mine.h) + (olow - mine.l);
+    if (!ol || !live) better += ol != live ? ol : g < own;
+    else if (same) better += g < own;
+    else if (fabsf(d) > oo) better += d > 0.f;
+    else unsure = true;
+  }
+  *sure = !__any_sync(kAll, unsure);
+  return own < a.groups && better < a.top_groups;
+}
+
+// Which groups stay (lane g: group g), from the values of their best in pairs of
+// fp32; *sure: whether these tell.
+template <typename X, int C>
+__device__ __noinline__ bool exact_groups(const ScoreArgs& a, const X* row, const uint32_t (&key)[C],
+                                          float top, float inv, bool* sure) {
+  const int lane = threadIdx.x & 31;
+  const unsigned below = (1u << lane) - 1u;
+  bool bad = false;
+  float v[3] = {-INFINITY, -INFINITY, -INFINITY};          // lane g: its best three, the last known by value
+  float lg[3] = {}, bg[3] = {};
+  for (int g = 0; g < a.groups; ++g) {
+    uint32_t gone = 0;
+    for (int r = 0; r <= a.group_top; ++r) {
+      uint32_t m = 0;
+      int at = 0;
+#pragma unroll
+      for (int q = C - 1; q >= 0; --q) {
+        const int x = lane * C + q;
+        if (x >= g * a.group_size && x < (g + 1) * a.group_size && !(gone >> q & 1u) && key[q] >= m && key[q]) {
+          m = key[q];
+          at = q;
+        }
+      }
+      const uint32_t f = __reduce_max_sync(kAll, m);
+      const unsigned who = __ballot_sync(kAll, m == f && f);
+      const bool win = (who >> lane & 1u) && !(who & below);
+      if (win) gone |= 1u << at;
+      const int x = __shfl_sync(kAll, lane * C + at, who ? __ffs(who) - 1 : 0);
+      if (lane == g) {
+        const float lx = f ? logit(a, row, x, &bad) : -INFINITY, bx = f ? bias_of(a, x) : 0.f;
+        if (r == 0) { v[0] = f ? value_of(f) : -INFINITY; lg[0] = lx; bg[0] = bx; }
+        else if (r == 1) { v[1] = f ? value_of(f) : -INFINITY; lg[1] = lx; bg[1] = bx; }
+        else { v[2] = f ? value_of(f) : -INFINITY; lg[2] = lx; bg[2] = bx; }
+      }
+    }
+  }
+  // the group's best are certain if the next one lies apart or is the same
+  const int t = a.group_top;
+  const float last = t == 1 ? v[0] : v[1], next = t == 1 ? v[1] : v[2];
+  const float ll = t == 1 ? lg[0] : lg[1], bl = t == 1 ? bg[0] : bg[1], ln = t == 1 ? lg[1] : lg[2], bn = t == 1 ? bg[1] : bg[2];
+  bool unsure = lane < a.groups && next > -INFINITY && !(last - next > near_of<C>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(next)))) &&
+                !(ll == ln && bl == bn);
+  const bool live = lane < a.groups && last > -INFINITY;     // (a group with a masked one among its best counts as -inf)
+  return better_groups<X, C>(a, row, lg[0], bg[0], lg[1], bg[1], live, lane, 0, top, unsure, sure);
+}
+
+// The choice for one token from all bits of its values: rounds of a warp maximum
+// over (value, lower index).  Values that fp32 cannot order are taken in pairs of it:
+// those of the candidates, which are the k chosen and all that come close to the
+// last of them.
 template <typename X, int C, bool GROUPED>
-__global__ void __launch_bounds__(1024) score_route_kernel(const __grid_constant__ ScoreArgs a) {
+__device__ __noinline__ int choose32(const ScoreArgs& a, const X* row, uint2* slot) {
+  const int lane = threadIdx.x & 31;
+  const unsigned below = (1u << lane) - 1u;
+  const bool by_logit = !a.bias && (!GROUPED || a.group_top == 1);
+  bool bad = false;
+  float u[C], top = 0.f, sum = 1.f;
+#pragma unroll
+  for (int q = 0; q < C; ++q) u[q] = lane * C + q < a.E ? logit(a, row, lane * C + q, &bad) : -INFINITY;
+  if (!a.sigmoid && !by_logit) softmax_of(u, &top, &sum);
+  const float inv = 1.f / sum;
+  uint32_t key[C];
+#pragma unroll
+  for (int q = 0; q < C; ++q) {
+    const int e = lane * C + q;
+    key[q] = e >= a.E ? 0 : key_of(by_logit || !(u[q] > -INFINITY) ? u[q] : score_of(a, u[q], top, inv) + bias_of(a, e));
+  }
+  if (GROUPED) {
+    float mine = -INFINITY;              // lane g: the value of group g
+    uint32_t part = 0;                   // the largest of its addends
+    for (int g = 0; g < a.groups; ++g) {
+      uint32_t m1 = 0, m2 = 0;
+#pragma unroll
+      for (int q = 0; q < C; ++q) {
+        const int e = lane * C + q;
+        if (e >= g * a.group_size && e < (g + 1) * a.group_size) {
+          m2 = max(m2, min(m1, key[q]));
+          m1 = max(m1, key[q]);
+        }
+      }
+      const uint32_t b1 = __reduce_max_sync(kAll, m1);
+      float v = value_of(b1), x = fabsf(v);
+      if (a.group_top > 1) {
+        const unsigned who = __ballot_sync(kAll, m1 == b1);
+        const float second = value_of(__reduce_max_sync(kAll, lane == __ffs(who) - 1 ? m2 : m1));
+        v += second;
+        x = fmaxf(x, fabsf(second));
+      }
+      if (lane == g) {
+        mine = v;
+        part = __float_as_uint(x < INFINITY ? x : 0.f);
+      }
+    }
+    int better = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const float v = __shfl_sync(kAll, mine, g);
+      better += v > mine || (v == mine && g < lane);
+    }
+    bool stays = lane < a.groups && better < a.top_groups, sure = true;
+    if (!by_logit && a.top_groups < a.groups) {
+      const float lo = -value_of(__reduce_max_sync(kAll, stays ? key_of(-mine) : 0x007fffffu));   // (-inf)
+      const float hi = value_of(__reduce_max_sync(kAll, lane < a.groups && !stays ? key_of(mine) : 0x007fffffu));
+      const float big = __uint_as_float(__reduce_max_sync(kAll, part));
+      if (hi > -INFINITY && !(lo - hi > 2.f * near_of<C>(a.sigmoid, inv, 2.f * big))) {
+        stays = exact_groups<X, C>(a, row, key, top, inv, &sure);
+        if (!sure) return choose64<X, C>(a, row);
+      }
+    }
+    const unsigned stay = __ballot_sync(kAll, stays);
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      const int e = lane * C + q;
+      if (e < a.E && !(stay >> (e / a.group_size) & 1u)) key[q] = 0;
+    }
+  }
+  BestTwo<C> best;
+  best.take(key);
+  // (a lane with nothing left has 0 and wins nothing, as long as others have some)
+  float last = -INFINITY;                  // the k-th value
+  int n = 0;
+  for (; n < 32; ++n) {
+    const uint32_t m = __reduce_max_sync(kAll, best.m1);
+    if (n >= a.k) {
+      const float v = m ? value_of(m) : -INFINITY;
+      if (by_logit || !(v > -INFINITY) || last - v > near_of<C>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(v)))) break;
+    }
+    const bool eq = best.m1 == m;
+    if (!(__ballot_sync(kAll, eq) & below) && eq) {
+      slot[n] = make_uint2(m, lane * C + best.q1);
+      best.pop(key);
+    }
+    if (n == a.k - 1) last = value_of(m);
+    __syncwarp();
+  }
+  __syncwarp();
+  const uint2 sel = lane < n ? slot[lane] : make_uint2(0, 0);
+  int sel_e = sel.y;
+  if (by_logit) return sel_e;
+  bool unused = false;
+  const float l = sel.x ? logit(a, row, sel_e, &unused) : -INFINITY, b = sel.x ? bias_of(a, sel_e) : 0.f;
+  bool more = false;                       // close ones that found no place among the candidates
+  if (n == 32) {
+    const float lk = __shfl_sync(kAll, l, a.k - 1), bk = __shfl_sync(kAll, b, a.k - 1);
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      const float w = key[q] ? value_of(key[q]) : -INFINITY;
+      if (w > -INFINITY && !(fabsf(last - w) > near_of<C>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(w)))) &&
+          !(u[q] == lk && bias_of(a, lane * C + q) == bk))
+        more = true;
+    }
+  }
+  if (__any_sync(kAll, more)) return choose64<X, C>(a, row);
+  const int e = order<X, C>(a, row, sel_e, l, b, n, top, inv, slot);
+  return __any_sync(kAll, e < 0) ? choose64<X, C>(a, row) : e;
+}
+
+// Rows of the tokens [t0, t1) of one block: run[e] is the row of expert e's next
+// assignment.  A token chooses an expert at most once, so the rank of an
+// assignment is the number of earlier tokens with the same expert: a bit per token
+// and expert, set in any order, counted up to the token's own.
+struct PlaceArgs {
+  const int32_t* idx;
+  const int32_t* hist;       // [nb][E]
+  int T, k, E, nb, per_block, words;
+  int64_t max_rows, sure;    // rows at or past `sure` belong to no expert, whatever the routing
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* padded;
+  int32_t* row_of;
+  int32_t* assign_of;
+};
+
+__device__ __forceinline__ void place_tokens(const PlaceArgs& a, int64_t t0, int64_t t1, int* run, uint32_t* bits) {
+  const int round = 32 * a.words;
+  for (int64_t base = t0; base < t1; base += round) {
+    const int n = (int)min((int64_t)round, t1 - base), words = (n + 31) >> 5;
+    for (int i = threadIdx.x; i < words * a.E; i += blockDim.x) bits[i] = 0;
+    __syncthreads();
+    const int32_t* idx = a.idx + base * a.k;
+    for (int i = threadIdx.x; i < n * a.k; i += blockDim.x) {
+      const int t = i / a.k;
+      atomicOr(&bits[(t >> 5) * a.E + idx[i]], 1u << (t & 31));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n * a.k; i += blockDim.x) {
+      const int t = i / a.k, e = idx[i];
+      int row = run[e];
+      for (int w = 0; w < t >> 5; ++w) row += __popc(bits[w * a.E + e]);
+      row += __popc(bits[(t >> 5) * a.E + e] & ((1u << (t & 31)) - 1u));
+      a.row_of[base * a.k + i] = row;
+      a.assign_of[row] = (int)(base * a.k + i);
+    }
+    __syncthreads();
+    if (base + round < t1) {
+      for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+        for (int w = 0; w < words; ++w) run[e] += __popc(bits[w * a.E + e]);
+      __syncthreads();
+    }
+  }
+}
+
+// Exclusive sums over the experts of their counts and of these rounded up to
+// kAlign: off and start [E + 1] in shared memory, by the whole block (sm: 32).
+__device__ __forceinline__ void scan_experts(const int* cnt, int E, int* off, int* start, unsigned long long* sm) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  unsigned long long before = 0;            // counts in the upper half, rows in the lower (both below 2^31)
+  for (int c0 = 0; c0 < E; c0 += blockDim.x) {
+    const int e = c0 + threadIdx.x, n = e < E ? cnt[e] : 0;
+    const unsigned long long own = (unsigned long long)n << 32 | (unsigned)((n + kAlign - 1) / kAlign * kAlign);
+    unsigned long long x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(kAll, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sm[w] = x;
+    __syncthreads();
+    unsigned long long all = 0;
+    x += before - own;
+    for (int i = 0; i < nw; ++i) {
+      if (i < w) x += sm[i];
+      all += sm[i];
+    }
+    if (e < E) {
+      off[e] = (int)(x >> 32);
+      start[e] = (int)x;
+    }
+    before += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    off[E] = (int)(before >> 32);
+    start[E] = (int)before;
+  }
+  __syncthreads();
+}
+
+// assign_of_row = -1 in [r0, r1), by blocks `b` of `nb`.
+__device__ __forceinline__ void no_assignment(const PlaceArgs& a, int64_t r0, int64_t r1, int b, int nb) {
+  const int64_t v0 = (r0 + 3) / 4 * 4;
+  if (b == 0 && threadIdx.x < 4 && r0 + threadIdx.x < min(v0, r1)) a.assign_of[r0 + threadIdx.x] = -1;
+  for (int64_t r = v0 + ((int64_t)b * blockDim.x + threadIdx.x) * 4; r < r1; r += (int64_t)nb * blockDim.x * 4) {
+    if (r + 4 <= r1) {
+      *reinterpret_cast<int4*>(a.assign_of + r) = make_int4(-1, -1, -1, -1);
+    } else {
+      for (int64_t i = r; i < r1; ++i) a.assign_of[i] = -1;
+    }
+  }
+}
+
+// Rows without an assignment up to row `end`: those behind each expert's, and behind the last.
+__device__ __forceinline__ void fill_rows(const PlaceArgs& a, const int* cnt, const int* start, int64_t end, int b,
+                                          int nb) {
+  const int w = threadIdx.x >> 5, nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+  for (int e = b * nw + w; e < a.E; e += nb * nw)
+    for (int r = start[e] + cnt[e] + lane; r < start[e + 1]; r += 32) a.assign_of[r] = -1;
+  no_assignment(a, start[a.E], end, b, nb);
+}
+
+// Threads of a block at most: the keys of wider rows take more registers.
+template <int C>
+constexpr int kRouteThreads = C <= 4 ? 1024 : C <= 8 ? 768 : C <= 16 ? 512 : 256;
+
+// FUSED: the first block has all tokens (few of them) and places them too,
+// without a second launch; the others fill the rows from p.sure on, which no routing reaches.
+template <typename X, int C, bool GROUPED, bool FUSED>
+__global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __grid_constant__ ScoreArgs a,
+                                                           const __grid_constant__ PlaceArgs p) {
   __shared__ int hist[kMaxE];
+  __shared__ uint2 slots[32][33];
+  __shared__ unsigned long long scan[32];
+  extern __shared__ uint32_t dyn[];
   let_next_start();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   wait_for_previous();
-  const int lane = threadIdx.x & 31;
+  if (FUSED && blockIdx.x > 0) {
+    no_assignment(p, p.sure, p.max_rows, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  uint2* slot = slots[threadIdx.x >> 5];
   const int64_t t0 = (int64_t)blockIdx.x * a.per_block;
   const int64_t t1 = min((int64_t)a.T, t0 + a.per_block);
   const bool by_logit = !a.bias && (!GROUPED || a.group_top == 1);
-  float bias[C];
-  bool bad = false;
+  constexpr uint32_t kIndex = 32 * C - 1;               // the bits of a key that hold the index
+  constexpr float kLead = 32.f * C * 0x1p-23f;          // what they take from the value, relative to it
+  constexpr bool kLossless = sizeof(X) == 2;            // a bf16 logit is all leading bits
+  auto leading = [](uint32_t key) {
+    const uint32_t k = key & ~kIndex;
+    return k > 0x007fffffu ? value_of(k) : -INFINITY;   // (-inf, and none)
+  };
+  int64_t t = t0 + (threadIdx.x >> 5);
+  float bias[C], bias_most = 0.f;
+  bool bad = false, unused = false;
 #pragma unroll
-  for (int q = 0; q < C; ++q) {
-    const int e = lane * C + q;
-    bias[q] = e < a.E ? bias_of(a, e) : 0.f;
-    if (a.bias && e < a.E && !(fabsf(a.bias[e]) < INFINITY)) bad = true;
-  }
-  for (int64_t t = t0 + (threadIdx.x >> 5); t < t1; t += blockDim.x >> 5) {
-    const X* row = static_cast<const X*>(a.logits) + t * a.ld;
-    float u[C];
+  for (int q = 0; q < C; ++q) bias[q] = 0.f;
+  if (a.bias && t < t1) {
 #pragma unroll
     for (int q = 0; q < C; ++q) {
       const int e = lane * C + q;
-      u[q] = e < a.E ? logit(a, row, e, &bad) : -INFINITY;
+      const float b = e < a.E ? a.bias[e] : 0.f;
+      if (fabsf(b) < INFINITY) bias[q] = b;
+      else bad = true;
+      bias_most = fmaxf(bias_most, fabsf(bias[q]));
     }
-    // the softmax' largest logit and sum
-    float top = 0.f, sum = 1.f;
-    if (!a.sigmoid && (!by_logit || !a.renorm)) {
-      top = u[0];
+    bias_most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(bias_most)));
+  }
+  Logits<X, C> next;
+  if (t < t1) next.load(static_cast<const X*>(a.logits) + t * a.ld, a.E, a.vec);
+  for (; t < t1; t += nw) {
+    const X* row = static_cast<const X*>(a.logits) + t * a.ld;
+    const Logits<X, C> raw = next;
+    if (t + nw < t1) next.load(row + nw * a.ld, a.E, a.vec);
+    float u[C], finite = 0.f;
 #pragma unroll
-      for (int q = 1; q < C; ++q) top = fmaxf(top, u[q]);
-      top = warp_max(top);
-      top = top > -INFINITY ? top : 0.f;
-      sum = 0.f;
-#pragma unroll
-      for (int q = 0; q < C; ++q) sum += fast_exp(u[q] - top);
-      sum = warp_sum(sum);
+    for (int q = 0; q < C; ++q) {
+      u[q] = lane * C + q < a.E ? raw.get(q) : 0.f;
+      finite = fmaf(u[q], 0.f, finite);               // NaN after an infinity or a NaN
     }
-    uint32_t key[C];
-    if (by_logit) {
-#pragma unroll
-      for (int q = 0; q < C; ++q) key[q] = key_of(u[q]);
-    } else {
-      const float inv = 1.f / sum;
+    const bool plain = !__any_sync(kAll, finite != 0.f);   // (E < 32 C: with zeros behind the last)
+    if (!plain || a.E < 32 * C) {
 #pragma unroll
       for (int q = 0; q < C; ++q) {
-        const float s = a.sigmoid ? __fdividef(1.f, 1.f + fast_exp(-u[q])) : fast_exp(u[q] - top) * inv;
-        key[q] = key_of(u[q] > -INFINITY ? s + bias[q] : -INFINITY);
+        const bool there = lane * C + q < a.E;
+        if (there && !(u[q] < INFINITY)) bad = true;       // NaN and +inf read as -inf
+        if (!there || !(u[q] < INFINITY)) u[q] = -INFINITY;
       }
     }
+    float top = 0.f, sum = 1.f;
+    if (!a.sigmoid && (!by_logit || !a.renorm)) softmax_of(u, &top, &sum);
+    const float inv = a.sigmoid ? 1.f : __fdividef(1.f, sum);
+    // the keys: leading bits of the value, then the index, downwards
+    uint32_t key[C], f1 = 0, f2 = 0;         // (f1, f2: the lane's best two values, all bits)
 #pragma unroll
-    for (int q = 0; q < C; ++q)
-      if (lane * C + q >= a.E) key[q] = 0;
+    for (int q = 0; q < C; ++q) {
+      float v = u[q];
+      if (!by_logit) {
+        v = score_of(a, v, top, inv) + bias[q];
+        if (!plain && !(u[q] > -INFINITY)) v = -INFINITY;
+      }
+      uint32_t k = key_of(v);
+      if (a.E < 32 * C && lane * C + q >= a.E) k = 0;
+      if (GROUPED) {
+        f2 = max(f2, min(f1, k));
+        f1 = max(f1, k);
+      }
+      key[q] = k ? (k & ~kIndex) | (kIndex - q - lane * C) : 0;
+    }
     bool again = false;
+    uint32_t m1 = 0, m2 = 0;                 // the lane's best two keys
+    auto best_two = [&]() {
+      m1 = key[0];
+      m2 = 0;
+#pragma unroll
+      for (int q = 1; q < C; ++q) {
+        m2 = max(m2, min(m1, key[q]));
+        m1 = max(m1, key[q]);
+      }
+    };
+    if (!GROUPED || a.seg) best_two();
     if (GROUPED) {
-      float mine = -INFINITY;              // lane i: the value of group i
+      float mine = -INFINITY;              // lanes of group g (seg > 0) or lane g: its value
+      uint32_t g1 = f1, g2 = f2;
+      if (a.seg) {                         // a group is a whole number of lanes, a power of two
+        for (int o = 1; o < a.seg; o <<= 1) {
+          const uint32_t n1 = __shfl_xor_sync(kAll, g1, o), n2 = __shfl_xor_sync(kAll, g2, o);
+          g2 = max(min(g1, n1), max(g2, n2));
+          g1 = max(g1, n1);
+        }
+        if (lane < a.groups << a.seg_log) mine = a.group_top == 1 ? value_of(g1) : value_of(g1) + value_of(g2);
+      } else {
+        for (int g = 0; g < a.groups; ++g) {
+          uint32_t b1 = 0, b2 = 0;
+#pragma unroll
+          for (int q = 0; q < C; ++q) {
+            const int e = lane * C + q;
+            if (e >= g * a.group_size && e < (g + 1) * a.group_size) {
+              b2 = max(b2, min(b1, key[q]));
+              b1 = max(b1, key[q]);
+            }
+          }
+          const uint32_t f = __reduce_max_sync(kAll, b1);
+          float v = leading(f);
+          if (a.group_top > 1) v += leading(__reduce_max_sync(kAll, b1 == f ? b2 : b1));
+          if (lane == g) mine = v;
+        }
+      }
+      const int own = a.seg ? lane >> a.seg_log : lane;
+      int better = 0;
       for (int g = 0; g < a.groups; ++g) {
-        uint32_t m1 = 0, m2 = 0;
+        const float v = __shfl_sync(kAll, mine, a.seg ? g << a.seg_log : g);
+        better += v > mine || (v == mine && g < own);
+      }
+      bool stays = own < a.groups && better < a.top_groups;
+      if (a.top_groups < a.groups) {
+        const float lo = -value_of(__reduce_max_sync(kAll, stays ? key_of(-mine) : 0x007fffffu));   // (-inf)
+        const float hi = value_of(__reduce_max_sync(kAll, own < a.groups && !stays ? key_of(mine) : 0x007fffffu));
+        // (from leading bits a value is up to kLead of itself lower)
+        const float most = bias_most + (a.sigmoid ? 1.f : inv);
+        const float gap = by_logit ? 0.f : 2.f * near_of<C>(a.sigmoid, inv, 2.f * most) + (a.seg ? 0.f : 2.f * kLead * most);
+        again = hi > -INFINITY && !(lo - hi > gap || (by_logit && (kLossless || a.seg)));
+        if (again && a.seg && !by_logit) {
+          // the group's best by their keys, if no third one comes near the last of them
+          uint32_t b1 = m1, b2 = m2;
+          for (int o = 1; o < a.seg; o <<= 1) {
+            const uint32_t n1 = __shfl_xor_sync(kAll, b1, o), n2 = __shfl_xor_sync(kAll, b2, o);
+            b2 = max(min(b1, n1), max(b2, n2));
+            b1 = max(b1, n1);
+          }
+          const float last = leading(a.group_top == 1 ? b1 : b2);
+          const float floor = last - near_of<C>(a.sigmoid, inv, last) - kLead * fabsf(last);
+          int count = 0;
+#pragma unroll
+          for (int q = 0; q < C; ++q) count += leading(key[q]) >= floor;
+          for (int o = 1; o < a.seg; o <<= 1) count += __shfl_xor_sync(kAll, count, o);
+          const bool live = own < a.groups && last > -INFINITY;
+          const int e0 = kIndex - (b1 & kIndex), e1 = kIndex - (b2 & kIndex);
+          bool sure;
+          stays = better_groups<X, C>(a, row, live ? logit(a, row, e0, &bad) : 0.f, live ? bias_of(a, e0) : 0.f,
+                                      live && b2 ? logit(a, row, e1, &bad) : 0.f, live && b2 ? bias_of(a, e1) : 0.f, live, own,
+                                      a.seg_log, top, live && count > a.group_top, &sure);
+          again = !sure;
+        }
+      }
+      if (a.seg) {
+        if (!stays) m1 = m2 = 0;
+      } else {
+        const unsigned stay = __ballot_sync(kAll, stays);
 #pragma unroll
         for (int q = 0; q < C; ++q) {
           const int e = lane * C + q;
-          if (e >= g * a.group_size && e < (g + 1) * a.group_size) {
-            m2 = max(m2, min(m1, key[q]));
-            m1 = max(m1, key[q]);
-          }
+          if (e < a.E && !(stay >> (e / a.group_size) & 1u)) key[q] = 0;
         }
-        const uint32_t best = __reduce_max_sync(kAll, m1);
-        float v = value_of(best);
-        if (a.group_top > 1) {
-          const unsigned who = __ballot_sync(kAll, m1 == best);
-          v += value_of(__reduce_max_sync(kAll, lane == __ffs(who) - 1 ? m2 : m1));
-        }
-        if (lane == g) mine = v;
-      }
-      int better = 0;
-      for (int g = 0; g < a.groups; ++g) {
-        const float v = __shfl_sync(kAll, mine, g);
-        better += v > mine || (v == mine && g < lane);
-      }
-      const bool stays = lane < a.groups && better < a.top_groups;
-      const unsigned stay = __ballot_sync(kAll, stays);
-      if (!by_logit && a.top_groups < a.groups) {
-        const float lo = -warp_max(stays ? -mine : -INFINITY);
-        const float hi = warp_max(lane < a.groups && !stays ? mine : -INFINITY);
-        again = hi > -INFINITY && !(lo - hi > 2.f * near_of(a.sigmoid, 1.f / sum, fmaxf(fabsf(lo), fabsf(hi))));
-      }
-#pragma unroll
-      for (int q = 0; q < C; ++q) {
-        const int e = lane * C + q;
-        if (e < a.E && !(stay >> (e / a.group_size) & 1u)) key[q] = 0;
+        best_two();
       }
     }
-    // k rounds of a warp maximum, and one more for the value that just missed
+    // rounds of a warp maximum: k, and more while the next may be as good as the k-th
     uint32_t sel = 0;
-    int sel_e = 0;
-    const int rounds = a.k + (by_logit || a.k == 32 ? 0 : 1);
-    for (int j = 0; j < rounds; ++j) {
-      uint32_t m = key[0];
-#pragma unroll
-      for (int q = 1; q < C; ++q) m = max(m, key[q]);
-      const uint32_t best = __reduce_max_sync(kAll, m);
-      const int who = __ffs(__ballot_sync(kAll, m == best)) - 1;
-      int at = 0;
-      if (lane == who) {
-        bool open = true;
-#pragma unroll
-        for (int q = 0; q < C; ++q)
-          if (open && key[q] == best) {
-            key[q] = 0;
-            at = q;
-            open = false;
-          }
+    float last = -INFINITY;
+    int n = 0;
+    for (; n < 32; ++n) {
+      const uint32_t m = __reduce_max_sync(kAll, m1);
+      if (n >= a.k) {
+        const float v = leading(m);
+        const float gap = by_logit ? 0.f : near_of<C>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(v))) + kLead * fabsf(v);
+        if ((by_logit && kLossless) || !(v > -INFINITY) || last - v > gap) break;
+      } else if (n == a.k - 1) {
+        last = leading(m);
       }
-      at = __shfl_sync(kAll, at, who);
-      if (lane == j) {
-        sel = best;
-        sel_e = who * C + at;
+      if (lane == n) sel = m;
+      if (m1 == m) {
+        m1 = m2;
+        m2 = 0;
+        if (m1 == 0) {                       // the third, and so on
+#pragma unroll
+          for (int q = 0; q < C; ++q)
+            if (key[q] < m) m1 = max(m1, key[q]);
+        }
       }
     }
+    int sel_e = sel ? kIndex - (sel & kIndex) : 0;
     float l = -INFINITY;
-    bool unused = false;
-    if (lane < rounds && sel) l = logit(a, row, sel_e, &unused);
-    if (!by_logit) {
-      const float v = sel ? value_of(sel) : -INFINITY, b = sel ? bias_of(a, sel_e) : 0.f;
-      const float pv = __shfl_up_sync(kAll, v, 1), pl = __shfl_up_sync(kAll, l, 1), pb = __shfl_up_sync(kAll, b, 1);
-      const bool close = lane > 0 && lane < rounds && v > -INFINITY && !(pl == l && pb == b) &&
-                         !(pv - v > near_of(a.sigmoid, 1.f / sum, fmaxf(fabsf(pv), fabsf(v))));
-      again = again || __any_sync(kAll, close) || a.k == 32;
-      if (again) {
-        sel_e = choose64<X, C>(a, row);
+    if (sel) l = logit(a, row, sel_e, &unused);
+    if (!(by_logit && kLossless)) {
+      // is the order of neighbours certain?  (Equal ones are in it.)
+      const float v = leading(sel), pv = __shfl_up_sync(kAll, v, 1), pl = __shfl_up_sync(kAll, l, 1);
+      float b = 0.f;
+      if (a.bias && sel) b = bias_of(a, sel_e);
+      const float pb = __shfl_up_sync(kAll, b, 1);
+      const float gap = by_logit ? 0.f : near_of<C>(a.sigmoid, inv, fmaxf(fabsf(pv), fabsf(v))) + kLead * fabsf(v);
+      const bool close = lane > 0 && v > -INFINITY && !(pv - v > gap) && !(pl == l && pb == b);
+      if (again || n == 32) {
+        sel_e = choose32<X, C, GROUPED>(a, row, slot);
+        if (lane < a.k) l = logit(a, row, sel_e, &unused);
+      } else if (__any_sync(kAll, close) || n > a.k) {
+        const int e = order<X, C>(a, row, sel_e, l, b, n, top, inv, slot);
+        sel_e = __any_sync(kAll, e < 0) ? choose64<X, C>(a, row) : e;
         if (lane < a.k) l = logit(a, row, sel_e, &unused);
       }
     }
     if (lane >= a.k) l = -INFINITY;
-    // gates, relative to the largest chosen score where they are renormalised
+    // gates
     const bool none = !__any_sync(kAll, l > -INFINITY);
-    float w;
+    float w = !(l > -INFINITY) ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - top);
     if (a.renorm) {
-      const float x = a.sigmoid ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;      // log s (+ a constant)
-      const float m = warp_max(x);
-      w = l > -INFINITY ? expf(x - m) : 0.f;
-      w = w / warp_sum(w);
-    } else {
-      w = !(l > -INFINITY) ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - top) / sum;
+      // relative to the largest chosen score where sigmoids are small (their sum may be 0), and for the softmax
+      if (!a.sigmoid || !__any_sync(kAll, l > -60.f)) {
+        const float x = a.sigmoid ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;      // log s (+ a constant)
+        const float m = value_of(__reduce_max_sync(kAll, key_of(x)));
+        w = l > -INFINITY ? expf(x - m) : 0.f;
+      }
+      float all = w;
+      if (a.k > 8) {
+        all += __shfl_xor_sync(kAll, all, 16);
+        all += __shfl_xor_sync(kAll, all, 8);
+      }
+#pragma unroll
+      for (int o = 4; o; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
+      w = w / all;
+    } else if (!a.sigmoid) {
+      w = w / sum;
     }
     if (none) bad = true;
     if (lane < a.k) {
@@ -337,132 +971,71 @@ __global__ void __launch_bounds__(1024) score_route_kernel(const __grid_constant
   }
   if (bad) report(a.status, MOE_ERR_BAD_INPUT);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * a.E + e] = hist[e];
+  if constexpr (FUSED) {
+    int* off = reinterpret_cast<int*>(dyn);
+    int* start = off + a.E + 1;
+    int* run = start + a.E + 1;
+    scan_experts(hist, a.E, off, start, scan);
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
+      if (e < a.E) {
+        run[e] = start[e];
+        p.counts[e] = hist[e];
+      }
+      p.offsets[e] = off[e];
+      p.padded[e] = start[e];
+    }
+    __syncthreads();
+    place_tokens(p, 0, a.T, run, reinterpret_cast<uint32_t*>(run + a.E));
+    fill_rows(p, hist, start, gridDim.x > 1 ? p.sure : p.max_rows, 0, 1);
+  } else {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * a.E + e] = hist[e];
+  }
 }
 
 // ---------------------------------------------------------- permutation
-struct PlaceArgs {
-  const int32_t* idx;
-  const int32_t* hist;       // [nb][E]
-  int n_assign, E, nb, per_block;      // per_block: assignments of one router block
-  int64_t max_rows;
-  int32_t* counts;
-  int32_t* offsets;
-  int32_t* padded;
-  int32_t* row_of;
-  int32_t* assign_of;
-  int32_t* status;
-};
-
-// Exclusive sum over the block's threads; `sm` has 33 ints.  *total: the sum.
-__device__ __forceinline__ int block_scan(int v, int* sm, int* total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kAll, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) sm[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    int y = lane < nw ? sm[lane] : 0;
-    const int own = y;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int z = __shfl_up_sync(kAll, y, o);
-      if (lane >= o) y += z;
-    }
-    sm[lane] = y - own;
-    if (lane == 31) sm[32] = y;
-  }
-  __syncthreads();
-  *total = sm[32];
-  return sm[w] + x - v;
-}
-
 // Blocks [0, nb): rows of this block's assignments.  Every block adds the
 // router's histograms up by itself (their sum over all blocks gives the rows'
 // start of each expert, that over the blocks before it its own share), which
 // saves a launch between the two.  Blocks from nb on: the rows without an assignment.
 __global__ void __launch_bounds__(1024) place_kernel(const __grid_constant__ PlaceArgs a) {
-  __shared__ int run[kMaxE], cnt[kMaxE], start[kMaxE + 1], sm[33];
-  extern __shared__ uint16_t warps[];      // [32][E]
+  __shared__ int cnt[kMaxE], run[kMaxE], off[kMaxE + 1], start[kMaxE + 1];
+  __shared__ unsigned long long scan[32];
+  extern __shared__ uint32_t dyn[];
   let_next_start();
-  wait_for_previous();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int b = blockIdx.x;
-  int total = 0, before = 0;
-  if ((int)threadIdx.x < a.E) {
-#pragma unroll 8
-    for (int i = 0; i < a.nb; ++i) {
-      const int c = a.hist[(int64_t)i * a.E + threadIdx.x];
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = run[e] = 0;
+  __syncthreads();
+  wait_for_previous();
+  // threads (slice, expert): each adds up some of the histograms
+  const int slices = (int)blockDim.x / a.E;                  // (E <= 1024 threads)
+  const int e = threadIdx.x % a.E, slice = threadIdx.x / a.E;
+  if (slice < slices) {
+    int total = 0, before = 0;
+#pragma unroll 16
+    for (int i = slice; i < a.nb; i += slices) {
+      const int c = a.hist[(int64_t)i * a.E + e];
       total += c;
       before += i < b ? c : 0;
     }
-  }
-  int rows, all;
-  const int padded = (total + kAlign - 1) / kAlign * kAlign;
-  const int first = block_scan(padded, sm, &rows);
-  const int off = block_scan(total, sm, &all);
-  if ((int)threadIdx.x < a.E) {
-    run[threadIdx.x] = first + before;
-    cnt[threadIdx.x] = total;
-    start[threadIdx.x] = first;
-    if (b == 0) {
-      a.counts[threadIdx.x] = total;
-      a.offsets[threadIdx.x] = off;
-      a.padded[threadIdx.x] = first;
-    }
-  }
-  if (threadIdx.x == 0) {
-    start[a.E] = rows;
-    if (b == 0) {
-      a.offsets[a.E] = all;
-      a.padded[a.E] = rows;
-    }
+    atomicAdd(&cnt[e], total);
+    atomicAdd(&run[e], before);
   }
   __syncthreads();
+  scan_experts(cnt, a.E, off, start, scan);
+  if (b == 0)
+    for (int i = threadIdx.x; i <= a.E; i += blockDim.x) {
+      if (i < a.E) a.counts[i] = cnt[i];
+      a.offsets[i] = off[i];
+      a.padded[i] = start[i];
+    }
   if (b >= a.nb) {
-    const int pb = b - a.nb, npb = gridDim.x - a.nb;
-    for (int e = pb * 32 + w; e < a.E; e += npb * 32)
-      for (int r = start[e] + cnt[e] + lane; r < start[e + 1]; r += 32) a.assign_of[r] = -1;
-    for (int64_t r = rows + (int64_t)pb * 1024 + threadIdx.x; r < a.max_rows; r += (int64_t)npb * 1024)
-      a.assign_of[r] = -1;
+    fill_rows(a, cnt, start, a.max_rows, b - a.nb, gridDim.x - a.nb);
     return;
   }
-  const int64_t a0 = (int64_t)b * a.per_block, a1 = min((int64_t)a.n_assign, a0 + a.per_block);
-  for (int64_t base = a0; base < a1; base += 1024) {
-    // ranks within a warp by lane, of warps by their number, so that an
-    // expert's rows follow the order of the assignments
-    for (int i = threadIdx.x; i < 32 * a.E; i += 1024) warps[i] = 0;
-    __syncthreads();
-    const int64_t i = base + threadIdx.x;
-    const int e = i < a1 ? a.idx[i] : -1;
-    const unsigned same = __match_any_sync(kAll, e);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    if (e >= 0 && rank == 0) warps[w * a.E + e] = (uint16_t)__popc(same);
-    __syncthreads();
-    if ((int)threadIdx.x < a.E) {
-      int at = 0;
-#pragma unroll 8
-      for (int v = 0; v < 32; ++v) {
-        const int c = warps[v * a.E + threadIdx.x];
-        warps[v * a.E + threadIdx.x] = (uint16_t)at;
-        at += c;
-      }
-      cnt[threadIdx.x] = run[threadIdx.x];
-      run[threadIdx.x] += at;
-    }
-    __syncthreads();
-    if (e >= 0) {
-      const int row = cnt[e] + warps[w * a.E + e] + rank;
-      a.row_of[i] = row;
-      a.assign_of[row] = (int)i;
-    }
-    __syncthreads();
-  }
+  for (int i = threadIdx.x; i < a.E; i += blockDim.x) run[i] += start[i];
+  __syncthreads();
+  const int64_t t0 = (int64_t)b * a.per_block;
+  place_tokens(a, t0, min((int64_t)a.T, t0 + a.per_block), run, dyn);
 }
 
 // -------------------------------------------------------------- backward
@@ -473,7 +1046,7 @@ struct ScoreBwdArgs {
   const float* dgate;
   void* dlogits;
   int64_t ld;
-  int T, E, k, sigmoid, renorm;
+  int T, E, k, sigmoid, renorm, vec;
   float scale;
   int32_t* status;
 };
@@ -505,7 +1078,11 @@ __global__ void __launch_bounds__(256) score_route_backward_kernel(const __grid_
     if (a.sigmoid || a.renorm) {
       d = a.renorm ? w * (dw - inner / a.scale) : w * dw;
       if (a.sigmoid && e >= 0) d *= 1.f / (1.f + expf(to_f(row[e])));      // 1 - s
-      for (int c = lane; c < a.E; c += 32) put(out + c, 0.f);
+      if (a.vec) {
+        for (int c = lane; c < a.E * (int)sizeof(X) / 16; c += 32) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
+      } else {
+        for (int c = lane; c < a.E; c += 32) put(out + c, 0.f);
+      }
     } else {
       float top = -INFINITY, sum = 0.f;
       for (int c = lane; c < a.E; c += 32) {
@@ -554,26 +1131,51 @@ __global__ void __launch_bounds__(256) balance_bias_kernel(const int32_t* counts
 }
 
 // Blocks of the router: one of up to 32 warps per SM for many tokens, of four
-// tokens (a warp each) for few.
-constexpr int kMostBlocks = 152;
+// tokens (a warp each) for few; one block that places its tokens too for at most
+// kFusedTokens.
+constexpr int kMostBlocks = 152, kFusedTokens = 32;
 int tokens_per_block(int T) {
   const int per = (int)(((int64_t)T + kMostBlocks - 1) / kMostBlocks);
-  return per < 4 ? 4 : per;
+  return T <= kFusedTokens ? kFusedTokens : per < 4 ? 4 : per;
 }
 
+// Words of 32 tokens that a round of the placement takes: what a block has, up to
+// 28 KB of bits.
+int place_words(int per_block, int E) {
+  const int need = (per_block + 31) / 32, most = 7168 / E;
+  return need < most ? need : most;
+}
+
+template <typename X, int C, bool GROUPED>
+cudaError_t run_score(ScoreArgs a, const PlaceArgs& p, int blocks, cudaStream_t s) {
+  constexpr int kVec = C * (int)sizeof(X) < 16 ? C * (int)sizeof(X) : 16;
+  a.vec = kVec >= 4 && ((uintptr_t)a.logits & (kVec - 1)) == 0 && a.ld * sizeof(X) % kVec == 0 &&
+          a.E * sizeof(X) % kVec == 0;
+  a.seg = a.group_size % C ? 0 : a.group_size / C;
+  if (a.seg & (a.seg - 1)) a.seg = 0;
+  for (a.seg_log = 0; 1 << a.seg_log < a.seg;) ++a.seg_log;
+  const int warps = blocks == 1 ? a.T : a.per_block, most = kRouteThreads<C>;
+  if (blocks == 1) {
+    const int threads = warps < 8 ? 256 : 32 * warps > most ? most : 32 * warps;
+    const int smem = ((3 + p.words) * a.E + 2) * 4;
+    return launch_overlapped(score_route_kernel<X, C, GROUPED, true>, 1 + (unsigned)((p.max_rows - p.sure) / 4096),
+                             threads, smem, s, a, p);
+  }
+  const int threads = 32 * warps > most ? most : 32 * warps;
+  return launch_overlapped(score_route_kernel<X, C, GROUPED, false>, blocks, threads, 0, s, a, p);
+}
 template <typename X, int C>
-cudaError_t run_score(const ScoreArgs& a, int blocks, int threads, cudaStream_t s) {
-  return a.groups > 1 ? launch_overlapped(score_route_kernel<X, C, true>, blocks, threads, 0, s, a)
-                      : launch_overlapped(score_route_kernel<X, C, false>, blocks, threads, 0, s, a);
+cudaError_t run_score(const ScoreArgs& a, const PlaceArgs& p, int blocks, cudaStream_t s) {
+  return a.groups > 1 ? run_score<X, C, true>(a, p, blocks, s) : run_score<X, C, false>(a, p, blocks, s);
 }
 template <typename X>
-cudaError_t run_score(const ScoreArgs& a, int blocks, int threads, cudaStream_t s) {
-  if (a.E <= 32) return run_score<X, 1>(a, blocks, threads, s);
-  if (a.E <= 64) return run_score<X, 2>(a, blocks, threads, s);
-  if (a.E <= 128) return run_score<X, 4>(a, blocks, threads, s);
-  if (a.E <= 256) return run_score<X, 8>(a, blocks, threads, s);
-  if (a.E <= 512) return run_score<X, 16>(a, blocks, threads, s);
-  return run_score<X, 32>(a, blocks, threads, s);
+cudaError_t run_score(const ScoreArgs& a, const PlaceArgs& p, int blocks, cudaStream_t s) {
+  if (a.E <= 32) return run_score<X, 1>(a, p, blocks, s);
+  if (a.E <= 64) return run_score<X, 2>(a, p, blocks, s);
+  if (a.E <= 128) return run_score<X, 4>(a, p, blocks, s);
+  if (a.E <= 256) return run_score<X, 8>(a, p, blocks, s);
+  if (a.E <= 512) return run_score<X, 16>(a, p, blocks, s);
+  return run_score<X, 32>(a, p, blocks, s);
 }
 
 }  // namespace
@@ -589,33 +1191,27 @@ cudaError_t launch_router(const moe_router_dims& d, const void* logits, const fl
   const int per = tokens_per_block(d.T);
   const int nb = (int)(((int64_t)d.T + per - 1) / per);
   const int64_t max_rows = (int64_t)d.T * d.top_k + (int64_t)kAlign * d.E;
+  const int words = place_words(per, d.E);
+  const int64_t n = (int64_t)d.T * d.top_k, sure = n + (kAlign - 1) * (n < d.E ? n : d.E);
+  const PlaceArgs p{o.topk_idx, hist, d.T, d.top_k, d.E, nb, per, words, max_rows, sure, o.counts, o.offsets,
+                    o.padded_offsets, o.row_of_assign, o.assign_of_row};
   if (nb > 0) {
     const ScoreArgs a{logits, bias, d.ld, d.T, d.E, d.top_k, per, d.groups, d.E / d.groups, d.top_groups,
-                      d.group_top, d.score == MOE_SCORE_SIGMOID, d.renormalise != 0, d.scale, o.topk_idx, o.gate,
-                      hist, status};
-    const int threads = 32 * (per < 32 ? per : 32);
-    const cudaError_t e = d.type == MOE_TYPE_BF16 ? run_score<__nv_bfloat16>(a, nb, threads, s)
-                                                  : run_score<float>(a, nb, threads, s);
-    if (e != cudaSuccess) return e;
+                      d.group_top, 0, 0, d.score == MOE_SCORE_SIGMOID, d.renormalise != 0, 0, d.scale, o.topk_idx,
+                      o.gate, hist, status};
+    const cudaError_t e = d.type == MOE_TYPE_BF16 ? run_score<__nv_bfloat16>(a, p, nb, s) : run_score<float>(a, p, nb, s);
+    if (e != cudaSuccess || nb == 1) return e;
   }
-  const PlaceArgs p{o.topk_idx, hist, d.T * d.top_k, d.E, nb, per * d.top_k, max_rows, o.counts, o.offsets,
-                    o.padded_offsets, o.row_of_assign, o.assign_of_row, status};
   const int64_t fill = ((int64_t)kAlign * d.E + 8191) / 8192;
-  static CtxCache<int> cache;
-  int set;
-  const cudaError_t e = cache.get(&set, [](int* v) {
-    *v = 1;
-    return cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * kMaxE * 2);
-  });
-  if (e != cudaSuccess) return e;
-  return launch_overlapped(place_kernel, nb + (unsigned)fill, 1024, 32 * d.E * sizeof(uint16_t), s, p);
+  return launch_overlapped(place_kernel, nb + (unsigned)fill, 1024, words * d.E * 4, s, p);
 }
 
 cudaError_t launch_router_backward(const moe_router_dims& d, const moe_route_out& o, const void* logits,
                                    const float* dgate, void* dlogits, int32_t* status, cudaStream_t s) {
   if (d.T == 0) return cudaSuccess;
+  const int vec = ((uintptr_t)dlogits & 15) == 0 && d.E * (d.type == MOE_TYPE_BF16 ? 2 : 4) % 16 == 0;
   const ScoreBwdArgs a{logits, o.topk_idx, o.gate, dgate, dlogits, d.ld, d.T, d.E, d.top_k,
-                       d.score == MOE_SCORE_SIGMOID, d.renormalise != 0, d.scale, status};
+                       d.score == MOE_SCORE_SIGMOID, d.renormalise != 0, vec, d.scale, status};
   const int blocks = (d.T - 1) / 8 + 1, most = kMostBlocks * 8;
   const int grid = blocks < most ? blocks : most;
   return d.type == MOE_TYPE_BF16

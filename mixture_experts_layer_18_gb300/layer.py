@@ -19,6 +19,7 @@ MODES = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "fp8_bwd": MOE_FP
 
 
 _current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _ptr(t):
@@ -26,8 +27,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    # (torch.cuda.current_stream() without the Stream object)
+    return _current_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
 class MoELayer:
@@ -63,13 +64,19 @@ class MoELayer:
                                   **u8)
         self.layout = moe_saved_layout_of(self.dims)
         self.saved = torch.empty(self.layout.total, **u8)
+        self._views = {}
         self.status = torch.zeros(4, **i32)
 
     # ------------------------------------------------------------- views
     def _view(self, offset, rows, cols):
-        es = 4 if self.dtype == torch.float32 else 2
-        n = rows * cols * es
-        return self.saved[offset:offset + n].view(self.dtype).view(rows, cols)
+        """Rows of `saved`; made once for each buffer that is there."""
+        if self._views.get("of") is not self.saved:
+            self._views = {"of": self.saved}
+        known = self._views.get((offset, cols))
+        if known is None:
+            n = rows * cols * (4 if self.dtype == torch.float32 else 2)
+            known = self._views[(offset, cols)] = self.saved[offset:offset + n].view(self.dtype).view(rows, cols)
+        return known
 
     @property
     def x_perm(self):
