@@ -60,6 +60,8 @@ __device__ __forceinline__ float fast_exp(float x) {
   return r;
 }
 
+__host__ __device__ __forceinline__ int padded4(int E) { return (E + 3) & ~3; }
+
 struct ScoreArgs {
   const void* logits;
   const float* bias;
@@ -71,7 +73,7 @@ struct ScoreArgs {
   float scale;
   int32_t* idx;
   float* gate;
-  int32_t* hist;            // [blocks][E]
+  int32_t* hist;            // [blocks][padded4(E)]
   int32_t* status;
 };
 
@@ -353,14 +355,9 @@ __device__ __forceinline__ float score_of(const ScoreArgs& a, float l, float top
   return a.sigmoid ? __fdividef(1.f, 1.f + fast_exp(-l)) : fast_exp(l - top) * inv_sum;
 }
 
-// u of one candidate of each lane (logit l, bias b) of this row.
-template <typename X, int C>
-__device__ __noinline__ Exact exact_value(const ScoreArgs& a, const X* row, float l, float b, float top) {
-  if (a.sigmoid) {
-    const Pair e = exp_of({fmaxf(-fabsf(l), -80.f), 0.f});
-    const Pair inv = inverse(add({1.f, 0.f}, e)), s = l >= 0.f ? inv : mul(e, inv);
-    return exact_of(s.h, s.l, b, fabsf(l) < 80.f);
-  }
+// 1 / (the sum of this row's exponentials relative to top), by a whole warp.
+template <typename X>
+__device__ __noinline__ Pair softmax_scale(const ScoreArgs& a, const X* row, float top) {
   Pair sum{0.f, 0.f};
   bool bad = false;
 #pragma unroll 1
@@ -370,9 +367,17 @@ __device__ __noinline__ Exact exact_value(const ScoreArgs& a, const X* row, floa
   }
 #pragma unroll 1
   for (int o = 16; o; o >>= 1) sum = add(sum, {__shfl_xor_sync(kAll, sum.h, o), __shfl_xor_sync(kAll, sum.l, o)});
-  const Pair x = sum_of(l, -top);
-  const Pair s = mul(exp_of(x.h > -80.f ? x : Pair{-80.f, 0.f}), inverse(sum));
-  return exact_of(s.h, s.l, b, x.h > -80.f);
+  return inverse(sum);
+}
+
+// u of one candidate of each lane (logit l, bias b; a softmax' largest logit and scale).
+__device__ __noinline__ Exact exact_value(bool sigmoid, float l, float b, float top, Pair scale) {
+  const Pair x = sigmoid ? Pair{-fabsf(l), 0.f} : sum_of(l, -top);
+  const bool known = x.h > -80.f;
+  const Pair e = exp_of(known ? x : Pair{-80.f, 0.f});
+  const Pair inv = sigmoid ? inverse(add({1.f, 0.f}, e)) : scale;
+  const Pair s = sigmoid && l >= 0.f ? inv : mul(e, inv);
+  return exact_of(s.h, s.l, b, known);
 }
 
 // The order of n candidates, one per lane (expert e, logit l, bias b): from fp32, and
@@ -399,7 +404,7 @@ __device__ __noinline__ int order(const ScoreArgs& a, const X* row, int e, float
     else unsure = true;
   }
   if (__any_sync(kAll, lane < n && unsure)) {
-    const Exact x = exact_value<X, C>(a, row, l, b, top);
+    const Exact x = exact_value(a.sigmoid, l, b, top, a.sigmoid ? Pair{} : softmax_scale(a, row, top));
     better = 0;
     unsure = false;
     for (int i = 0; i < n; ++i) {
@@ -424,24 +429,23 @@ __device__ __noinline__ int order(const ScoreArgs& a, const X* row, int e, float
 }
 
 // Whether this lane's group `own` is among the best: l0, b0, l1, b1 are logits and
-// biases of its best one or two (live: none masked), lane g << log has group g's.
-template <typename X, int C>
-__device__ __noinline__ bool better_groups(const ScoreArgs& a, const X* row, float l0, float b0, float l1, float b1,
-                                           bool live, int own, int log, float top, bool unsure, bool* sure) {
+// biases of its best one or two (live: none masked), lane base + (g << log) has group
+// g's.  *unsure: whether these do not tell.
+__device__ __noinline__ bool better_groups(const ScoreArgs& a, float l0, float b0, float l1, float b1, bool live, int own,
+                                           int base, int log, float top, Pair scale, bool* unsure) {
   if (!live) l0 = b0 = 0.f;
   if (!live || a.group_top == 1) l1 = b1 = 0.f;
-  const Exact x0 = exact_value<X, C>(a, row, l0, b0, top);
+  const Exact x0 = exact_value(a.sigmoid, l0, b0, top, scale), x1 = exact_value(a.sigmoid, l1, b1, top, scale);
   Pair mine = x0.u;
   float off = x0.off;
   if (a.group_top == 2) {
-    const Exact x1 = exact_value<X, C>(a, row, l1, b1, top);
     mine = add(x0.u, x1.u);
     off += x1.off + 0x1p-44f * (fabsf(x0.u.h) + fabsf(x1.u.h));
   }
   int better = 0;
   for (int g = 0; g < a.groups; ++g) {
     // (every lane takes part in every exchange: none of them behind a condition)
-    const int at = g << log;
+    const int at = base + (g << log);
     const bool ol = __shfl_sync(kAll, (int)live, at);
     const float oh = __shfl_sync(kAll, mine.h, at), olow = __shfl_sync(kAll, mine.l, at);
     const float oo = __shfl_sync(kAll, off, at) + off;
@@ -453,9 +457,8 @@ __device__ __noinline__ bool better_groups(const ScoreArgs& a, const X* row, flo
     if (!ol || !live) better += ol != live ? ol : g < own;
     else if (same) better += g < own;
     else if (fabsf(d) > oo) better += d > 0.f;
-    else unsure = true;
+    else *unsure = true;
   }
-  *sure = !__any_sync(kAll, unsure);
   return own < a.groups && better < a.top_groups;
 }
 
@@ -502,7 +505,10 @@ __device__ __noinline__ bool exact_groups(const ScoreArgs& a, const X* row, cons
   bool unsure = lane < a.groups && next > -INFINITY && !(last - next > near_of<C>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(next)))) &&
                 !(ll == ln && bl == bn);
   const bool live = lane < a.groups && last > -INFINITY;     // (a group with a masked one among its best counts as -inf)
-  return better_groups<X, C>(a, row, lg[0], bg[0], lg[1], bg[1], live, lane, 0, top, unsure, sure);
+  const bool stays = better_groups(a, lg[0], bg[0], lg[1], bg[1], live, lane, 0, 0, top,
+                                   a.sigmoid ? Pair{} : softmax_scale(a, row, top), &unsure);
+  *sure = !__any_sync(kAll, unsure);
+  return stays;
 }
 
 // The choice for one token from all bits of its values: rounds of a warp maximum
@@ -621,7 +627,7 @@ __device__ __noinline__ int choose32(const ScoreArgs& a, const X* row, uint2* sl
 // and expert, set in any order, counted up to the token's own.
 struct PlaceArgs {
   const int32_t* idx;
-  const int32_t* hist;       // [nb][E]
+  const int32_t* hist;       // [nb][padded4(E)]
   int T, k, E, nb, per_block, words;
   int64_t max_rows, sure;    // rows at or past `sure` belong to no expert, whatever the routing
   int32_t* counts;
@@ -662,36 +668,43 @@ __device__ __forceinline__ void place_tokens(const PlaceArgs& a, int64_t t0, int
 
 // Exclusive sums over the experts of their counts and of these rounded up to
 // kAlign: off and start [E + 1] in shared memory, by the whole block (sm: 32).
-__device__ __forceinline__ void scan_experts(const int* cnt, int E, int* off, int* start, unsigned long long* sm) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  unsigned long long before = 0;            // counts in the upper half, rows in the lower (both below 2^31)
+__device__ __forceinline__ void scan_experts(const int* cnt, int E, int* off, int* start, int2* sm) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int2 before = make_int2(0, 0);
   for (int c0 = 0; c0 < E; c0 += blockDim.x) {
-    const int e = c0 + threadIdx.x, n = e < E ? cnt[e] : 0;
-    const unsigned long long own = (unsigned long long)n << 32 | (unsigned)((n + kAlign - 1) / kAlign * kAlign);
-    unsigned long long x = own;
+    const int used = (min(E - c0, (int)blockDim.x) + 31) >> 5;        // warps with experts
+    const int e = c0 + threadIdx.x, n = e < E ? cnt[e] : 0, p = (n + kAlign - 1) / kAlign * kAlign;
+    int x = n, y = p;
+    if (w < used) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(kAll, x, o);
-      if (lane >= o) x += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kAll, x, o), v = __shfl_up_sync(kAll, y, o);
+        if (lane >= o) {
+          x += u;
+          y += v;
+        }
+      }
+      if (lane == 31) sm[w] = make_int2(x, y);
     }
-    if (lane == 31) sm[w] = x;
     __syncthreads();
-    unsigned long long all = 0;
-    x += before - own;
-    for (int i = 0; i < nw; ++i) {
-      if (i < w) x += sm[i];
-      all += sm[i];
+    if (w < used) {
+      int2 all = lane < used ? sm[lane] : make_int2(0, 0), mine = lane < w ? all : make_int2(0, 0);
+      all.x = __reduce_add_sync(kAll, all.x);
+      all.y = __reduce_add_sync(kAll, all.y);
+      mine.x = __reduce_add_sync(kAll, mine.x);
+      mine.y = __reduce_add_sync(kAll, mine.y);
+      if (e < E) {
+        off[e] = before.x + mine.x + x - n;
+        start[e] = before.y + mine.y + y - p;
+      }
+      before.x += all.x;
+      before.y += all.y;
     }
-    if (e < E) {
-      off[e] = (int)(x >> 32);
-      start[e] = (int)x;
-    }
-    before += all;
-    __syncthreads();
+    if (c0 + (int)blockDim.x < E) __syncthreads();    // (sm is written again; all warps are used but in the last part)
   }
   if (threadIdx.x == 0) {
-    off[E] = (int)(before >> 32);
-    start[E] = (int)before;
+    off[E] = before.x;
+    start[E] = before.y;
   }
   __syncthreads();
 }
@@ -729,7 +742,7 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
                                                            const __grid_constant__ PlaceArgs p) {
   __shared__ int hist[kMaxE];
   __shared__ uint2 slots[32][33];
-  __shared__ unsigned long long scan[32];
+  __shared__ int2 scan[32];
   extern __shared__ uint32_t dyn[];
   let_next_start();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
@@ -877,11 +890,11 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
           for (int o = 1; o < a.seg; o <<= 1) count += __shfl_xor_sync(kAll, count, o);
           const bool live = own < a.groups && last > -INFINITY;
           const int e0 = kIndex - (b1 & kIndex), e1 = kIndex - (b2 & kIndex);
-          bool sure;
-          stays = better_groups<X, C>(a, row, live ? logit(a, row, e0, &bad) : 0.f, live ? bias_of(a, e0) : 0.f,
-                                      live && b2 ? logit(a, row, e1, &bad) : 0.f, live && b2 ? bias_of(a, e1) : 0.f, live, own,
-                                      a.seg_log, top, live && count > a.group_top, &sure);
-          again = !sure;
+          bool unsure = live && count > a.group_top;
+          stays = better_groups(a, live ? logit(a, row, e0, &bad) : 0.f, live ? bias_of(a, e0) : 0.f,
+                                live && b2 ? logit(a, row, e1, &bad) : 0.f, live && b2 ? bias_of(a, e1) : 0.f, live, own, 0,
+                                a.seg_log, top, a.sigmoid ? Pair{} : softmax_scale(a, row, top), &unsure);
+          again = __any_sync(kAll, unsure);
         }
       }
       if (a.seg) {
@@ -988,8 +1001,359 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
     place_tokens(p, 0, a.T, run, reinterpret_cast<uint32_t*>(run + a.E));
     fill_rows(p, hist, start, gridDim.x > 1 ? p.sure : p.max_rows, 0, 1);
   } else {
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * a.E + e] = hist[e];
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * padded4(a.E) + e] = hist[e];
   }
+}
+
+// Many tokens: eight lanes per token, four tokens per warp, so that what a token
+// takes besides its elements (rounds, gates, addresses) is paid once for four.
+// E <= 8 CL, top_k <= 8, a group is a power of two of lanes or all there is; rows by
+// vectors.  Of fp32 logits a key's index is that within the lane, which leaves more bits
+// to the value.
+constexpr int kManyThreads = 512;
+
+__device__ __forceinline__ uint32_t max8(uint32_t v) {          // over a token's lanes
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// As order(), for up to 16 candidates of each of four tokens: lane sl of a token
+// has candidates sl and sl + 8 (n: how many the token has).  Returns whether its
+// order is known; e[0]: the lane's expert in that order.
+template <typename X, int CL>
+__device__ __noinline__ bool order8(const ScoreArgs& a, const X* row, int (&e)[2], const float (&l)[2], const float (&b)[2],
+                                    int n, float top, float inv, int* slot) {
+  const int sl = threadIdx.x & 7, first = threadIdx.x & 24;
+  const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
+  float v[2];
+  bool on[2];
+  int better[2] = {0, 0};
+  bool unsure = false;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    on[r] = sl + 8 * r < n && l[r] > -INFINITY;
+    v[r] = !on[r] || by_logit ? l[r] : score_of(a, l[r], top, inv) + b[r];
+  }
+  const int most = (int)__reduce_max_sync(kAll, (unsigned)n);
+  for (int i = 0; i < most; ++i) {
+    const int at = first + (i & 7);
+    const float ov = __shfl_sync(kAll, i < 8 ? v[0] : v[1], at), ol = __shfl_sync(kAll, i < 8 ? l[0] : l[1], at);
+    const float ob = __shfl_sync(kAll, i < 8 ? b[0] : b[1], at);
+    const int oe = __shfl_sync(kAll, i < 8 ? e[0] : e[1], at);
+    const bool other = ol > -INFINITY;
+    if (i >= n) continue;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (sl + 8 * r >= n || oe == e[r]) continue;
+      const float gap = near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(v[r]), fabsf(ov)));
+      if ((ol == l[r] && ob == b[r]) || (!on[r] && !other)) better[r] += oe < e[r];
+      else if (!on[r] || !other) better[r] += other;               // masked ones last
+      else if (by_logit || fabsf(ov - v[r]) > gap) better[r] += ov > v[r] || (ov == v[r] && oe < e[r]);
+      else unsure = true;
+    }
+  }
+  unsigned open = __ballot_sync(kAll, unsure);
+  if (open) {
+    Pair scale{};
+    if (!a.sigmoid) {
+      for (int t = 0; t < 32; t += 8)                        // a token at a time, by the whole warp
+        if (open >> t & 0xffu) {
+          const X* r = reinterpret_cast<const X*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(row), t));
+          const Pair p = softmax_scale(a, r, __shfl_sync(kAll, top, t));
+          if (first == t) scale = p;
+        }
+    }
+    const Exact x0 = exact_value(a.sigmoid, l[0], b[0], top, scale), x1 = exact_value(a.sigmoid, l[1], b[1], top, scale);
+    better[0] = better[1] = 0;
+    unsure = false;
+    for (int i = 0; i < most; ++i) {
+      const int at = first + (i & 7);
+      const float oh = __shfl_sync(kAll, i < 8 ? x0.u.h : x1.u.h, at), olow = __shfl_sync(kAll, i < 8 ? x0.u.l : x1.u.l, at);
+      const float oo = __shfl_sync(kAll, i < 8 ? x0.off : x1.off, at), ol = __shfl_sync(kAll, i < 8 ? l[0] : l[1], at);
+      const float ob = __shfl_sync(kAll, i < 8 ? b[0] : b[1], at), ov = __shfl_sync(kAll, i < 8 ? v[0] : v[1], at);
+      const int oe = __shfl_sync(kAll, i < 8 ? e[0] : e[1], at);
+      const bool other = ol > -INFINITY;
+      if (i >= n) continue;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (sl + 8 * r >= n || oe == e[r]) continue;
+        const Exact& x = r ? x1 : x0;
+        const float gap = near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(v[r]), fabsf(ov)));
+        const float d = (oh - x.u.h) + (olow - x.u.l);
+        if ((ol == l[r] && ob == b[r]) || (!on[r] && !other)) better[r] += oe < e[r];
+        else if (!on[r] || !other) better[r] += other;
+        else if (by_logit || fabsf(ov - v[r]) > gap) better[r] += ov > v[r] || (ov == v[r] && oe < e[r]);
+        else if (fabsf(d) > oo + x.off) better[r] += d > 0.f;
+        else unsure = true;
+      }
+    }
+    open = __ballot_sync(kAll, unsure);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    if (sl + 8 * r < n) slot[first * 2 + better[r]] = e[r];
+  __syncwarp();
+  if (sl < n) e[0] = slot[first * 2 + sl];
+  return !(open >> first & 0xffu);
+}
+
+template <typename X, int CL, bool GROUPED>
+__global__ void __launch_bounds__(kManyThreads, 1) score_many_kernel(const __grid_constant__ ScoreArgs a) {
+  constexpr bool kLossless = sizeof(X) == 2;            // a bf16 logit is all leading bits:
+  constexpr uint32_t kIndex = (kLossless ? 8 : 1) * CL - 1;    // a key then holds the expert's index, else that in the lane
+  constexpr float kLead = (kIndex + 1) * 0x1p-23f;      // what it takes from the value, relative to it
+  constexpr int V = CL * (int)sizeof(X) < 16 ? CL : 16 / (int)sizeof(X);
+  __shared__ int hist[8 * CL];
+  __shared__ __align__(16) float bias[8 * (CL + 4)];    // (rows of lanes apart by 4 banks)
+  __shared__ uint2 slots[kManyThreads / 32][33];
+  let_next_start();
+  for (int e = threadIdx.x; e < 8 * CL; e += kManyThreads) hist[e] = 0;
+  wait_for_previous();
+  bool bad = false, unused = false;
+  const bool by_logit = !a.bias && (!GROUPED || a.group_top == 1);
+  for (int e = threadIdx.x; e < 8 * CL; e += kManyThreads) {
+    float b = 0.f;
+    if (a.bias && e < a.E) {
+      b = bias_of(a, e);
+      if (!(fabsf(a.bias[e]) < INFINITY)) bad = true;
+    }
+    bias[e / CL * (CL + 4) + e % CL] = b;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, sl = lane & 7, first = lane & 24;
+  const unsigned below = ((1u << sl) - 1u) << first;
+  uint2* slot = slots[threadIdx.x >> 5];
+  const float* my_bias = bias + sl * (CL + 4);
+  const uint32_t index0 = kIndex - (kLossless ? sl * CL : 0);   // a key's index of the lane's first expert
+  float bias_most = 0.f;
+  if (a.bias) {
+#pragma unroll
+    for (int q = 0; q < CL; ++q) bias_most = fmaxf(bias_most, fabsf(my_bias[q]));
+    bias_most = __uint_as_float(max8(__float_as_uint(bias_most)));
+  }
+  auto leading = [](uint32_t key) {
+    const uint32_t k = key & ~kIndex;
+    return k > 0x007fffffu ? value_of(k) : -INFINITY;   // (-inf, and none)
+  };
+  const int64_t t0 = (int64_t)blockIdx.x * a.per_block, t1 = min((int64_t)a.T, t0 + a.per_block);
+  for (int64_t tb = t0 + (threadIdx.x >> 5) * 4; tb < t1; tb += kManyThreads / 8) {
+    const int64_t t = min(tb + (lane >> 3), t1 - 1);    // (past the end: the last token again, not stored)
+    const bool mine_on = tb + (lane >> 3) < t1;
+    const X* row = static_cast<const X*>(a.logits) + t * a.ld;
+    float u[CL], finite = 0.f;
+#pragma unroll
+    for (int i = 0; i < CL / V; ++i) {
+      const int e = sl * CL + i * V;
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (e < a.E) {
+        if constexpr (V * sizeof(X) == 16) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + e));
+          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + e));
+          w[0] = x.x; w[1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        u[i * V + j] = sizeof(X) == 4 ? __uint_as_float(w[j & 3]) : j & 1 ? bf16_hi(w[(j / 2) & 3]) : bf16_lo(w[(j / 2) & 3]);
+    }
+#pragma unroll
+    for (int q = 0; q < CL; ++q) finite = fmaf(u[q], 0.f, finite);    // NaN after an infinity or a NaN
+    const bool plain = !__any_sync(kAll, finite != 0.f) && a.E == 8 * CL;
+    if (!plain) {
+#pragma unroll
+      for (int q = 0; q < CL; ++q) {
+        const bool there = sl * CL + q < a.E;
+        if (there && !(u[q] < INFINITY)) bad = true;    // NaN and +inf read as -inf
+        if (!there || !(u[q] < INFINITY)) u[q] = -INFINITY;
+      }
+    }
+    float top = 0.f, sum = 1.f;
+    if (!a.sigmoid && (!by_logit || !a.renorm)) {
+      float m = u[0];
+#pragma unroll
+      for (int q = 1; q < CL; ++q) m = fmaxf(m, u[q]);
+      top = value_of(max8(key_of(m)));
+      top = top > -INFINITY ? top : 0.f;
+      sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < CL; ++q) {
+        const float x = fast_exp(u[q] - top);
+        sum += x;
+        if (!by_logit) u[q] = plain || u[q] > -INFINITY ? x : -INFINITY;
+      }
+      sum = sum8(sum);
+    }
+    const float inv = a.sigmoid ? 1.f : __fdividef(1.f, sum);
+    uint32_t key[CL], f1 = 0, f2 = 0;                   // (f1, f2: the lane's best two values, all bits)
+    uint32_t m1 = 0, m2 = 0, m3 = 0;                    // its best three keys
+#pragma unroll
+    for (int i = 0; i < CL; i += 4) {
+      const float4 b4 = *reinterpret_cast<const float4*>(my_bias + i);
+      const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = i + j;
+        float v = u[q];
+        if (!by_logit) {
+          v = a.sigmoid ? __fdividef(1.f, 1.f + fast_exp(-v)) : v * inv;
+          v += bb[j];
+          if (!plain && !(u[q] > -INFINITY)) v = -INFINITY;
+        }
+        uint32_t k = key_of(v);
+        if (!plain && sl * CL + q >= a.E) k = 0;
+        if (GROUPED) {
+          f2 = max(f2, min(f1, k));
+          f1 = max(f1, k);
+        }
+        k = k ? (k & ~kIndex) | (index0 - q) : 0;
+        key[q] = k;
+        m3 = max(m3, min(m2, k));
+        m2 = max(m2, min(m1, k));
+        m1 = max(m1, k);
+      }
+    }
+    bool again = false;                                 // (the same in a token's lanes)
+    if (GROUPED) {
+      uint32_t g1 = f1, g2 = f2;
+      for (int o = 1; o < a.seg; o <<= 1) {
+        const uint32_t n1 = __shfl_xor_sync(kAll, g1, o), n2 = __shfl_xor_sync(kAll, g2, o);
+        g2 = max(min(g1, n1), max(g2, n2));
+        g1 = max(g1, n1);
+      }
+      const int own = sl >> a.seg_log;
+      float mine = -INFINITY;
+      if (own < a.groups) mine = a.group_top == 1 ? value_of(g1) : value_of(g1) + value_of(g2);
+      int better = 0;
+      for (int g = 0; g < a.groups; ++g) {
+        const float v = __shfl_sync(kAll, mine, first + (g << a.seg_log));
+        better += v > mine || (v == mine && g < own);
+      }
+      bool stays = own < a.groups && better < a.top_groups;
+      if (!by_logit && a.top_groups < a.groups) {
+        const float lo = -value_of(max8(stays ? key_of(-mine) : 0x007fffffu));   // (-inf)
+        const float hi = value_of(max8(own < a.groups && !stays ? key_of(mine) : 0x007fffffu));
+        const float most = bias_most + (a.sigmoid ? 1.f : inv);
+        again = hi > -INFINITY && !(lo - hi > 2.f * near_of<CL>(a.sigmoid, inv, 2.f * most));
+        if (a.seg == 1 && a.sigmoid && __any_sync(kAll, again)) {
+          // a lane's own best, if no third one comes near the last of them
+          const float last = leading(a.group_top == 1 ? m1 : m2), next = leading(a.group_top == 1 ? m2 : m3);
+          const bool live = own < a.groups && last > -INFINITY;
+          bool unsure = live && next > -INFINITY && !(last - next > near_of<CL>(a.sigmoid, inv, last) + kLead * fabsf(last));
+          const int q0 = (index0 - (m1 & kIndex)) & (CL - 1), q1 = (index0 - (m2 & kIndex)) & (CL - 1);
+          const bool two = live && a.group_top == 2;
+          const bool s = better_groups(a, live ? logit(a, row, sl * CL + q0, &unused) : 0.f, live ? my_bias[q0] : 0.f,
+                                       two ? logit(a, row, sl * CL + q1, &unused) : 0.f, two ? my_bias[q1] : 0.f, live, own,
+                                       first, 0, top, Pair{}, &unsure);
+          const unsigned open = __ballot_sync(kAll, unsure);
+          if (again && !(open >> first & 0xffu)) {
+            stays = s;
+            again = false;
+          }
+        }
+      }
+      if (!stays) m1 = m2 = m3 = 0;
+    }
+    // rounds of a maximum over the token's lanes: k, and more while the next may be as good as the k-th
+    uint32_t sel[2] = {0, 0};
+    int se[2] = {0, 0}, n = 0;
+    float last = -INFINITY;
+    bool stop = false;
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t m = max8(m1);
+      if (i >= a.k) {
+        const float v = leading(m);
+        const float gap = by_logit ? 0.f : near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(v))) + kLead * fabsf(v);
+        stop = stop || (by_logit && kLossless) || !(v > -INFINITY) || last - v > gap;
+        if (!__any_sync(kAll, !stop)) break;
+      } else if (i == a.k - 1) {
+        last = leading(m);
+      }
+      const unsigned who = __ballot_sync(kAll, m1 == m);
+      const int e = (kLossless ? 0 : (__ffs(who >> first & 0xffu) - 1) * CL) + (int)(kIndex - (m & kIndex));
+      if (!stop) {
+        ++n;
+        if (sl == (i & 7)) {
+          if (i < 8) { sel[0] = m; se[0] = e; }
+          else { sel[1] = m; se[1] = e; }
+        }
+        if (m1 == m && !(who & below)) {
+          m1 = m2;
+          m2 = m3;
+          m3 = 0;
+          if (m1 == 0) {                       // the fourth, and so on
+#pragma unroll
+            for (int q = 0; q < CL; ++q)
+              if (key[q] < m) m1 = max(m1, key[q]);
+          }
+        }
+      }
+    }
+    // (equal keys of two lanes came by their place in the lane: masked ones are chosen again)
+    if (!kLossless && !(last > -INFINITY)) again = true;
+    float l[2] = {-INFINITY, -INFINITY};
+    if (sel[0]) l[0] = logit(a, row, se[0], &unused);
+    const bool full = n == 16;                 // (there may be more)
+    if (!(by_logit && kLossless)) {
+      // is the order of neighbours certain?
+      const float v = leading(sel[0]), pv = __shfl_up_sync(kAll, v, 1, 8), pl = __shfl_up_sync(kAll, l[0], 1, 8);
+      float b[2] = {0.f, 0.f};
+      if (a.bias && sel[0]) b[0] = bias[se[0] / CL * (CL + 4) + se[0] % CL];
+      const float pb = __shfl_up_sync(kAll, b[0], 1, 8);
+      const float gap = by_logit ? 0.f : near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(pv), fabsf(v))) + kLead * fabsf(v);
+      const int pe = __shfl_up_sync(kAll, se[0], 1, 8);
+      const bool close = sl > 0 && v > -INFINITY && !(pv - v > gap) && !(pl == l[0] && pb == b[0] && pe < se[0]);
+      bool known = true;
+      if (__any_sync(kAll, close || n > a.k)) {
+        if (sel[1]) {
+          l[1] = logit(a, row, se[1], &unused);
+          if (a.bias) b[1] = bias[se[1] / CL * (CL + 4) + se[1] % CL];
+        }
+        known = order8<X, CL>(a, row, se, l, b, n, top, inv, reinterpret_cast<int*>(slot));
+      }
+      unsigned open = __ballot_sync(kAll, !known || again || full);
+      for (int o = 0; o < 32; o += 8)                    // what is left, a token at a time by the whole warp
+        if (open >> o & 0xffu) {
+          const X* r = reinterpret_cast<const X*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(row), o));
+          const int x = choose32<X, (CL + 3) / 4, GROUPED>(a, r, slot);
+          const int e = __shfl_sync(kAll, x, sl);
+          if (first == o) se[0] = e;
+        }
+      if (sl < a.k) l[0] = logit(a, row, se[0], &unused);
+    }
+    const float lg = sl < a.k ? l[0] : -INFINITY;
+    // gates, as above
+    const bool none = !(__ballot_sync(kAll, lg > -INFINITY) >> first & 0xffu);
+    float w = !(lg > -INFINITY) ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-lg)) : expf(lg - top);
+    if (a.renorm) {
+      const bool small = !(__ballot_sync(kAll, lg > -60.f) >> first & 0xffu);
+      if (!a.sigmoid || __any_sync(kAll, small)) {
+        const float x = a.sigmoid ? fminf(lg, 0.f) - log1pf(expf(-fabsf(lg))) : lg;
+        const float m = value_of(max8(key_of(x)));
+        if (!a.sigmoid || small) w = lg > -INFINITY ? expf(x - m) : 0.f;
+      }
+      w = w / sum8(w);
+    } else if (!a.sigmoid) {
+      w = w / sum;
+    }
+    if (none && mine_on) bad = true;
+    if (mine_on && sl < a.k) {
+      a.idx[t * a.k + sl] = se[0];
+      a.gate[t * a.k + sl] = none ? 0.f : a.scale * w;
+      atomicAdd(&hist[se[0]], 1);
+    }
+  }
+  if (bad) report(a.status, MOE_ERR_BAD_INPUT);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kManyThreads) a.hist[(int64_t)blockIdx.x * padded4(a.E) + e] = hist[e];
 }
 
 // ---------------------------------------------------------- permutation
@@ -999,26 +1363,34 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
 // saves a launch between the two.  Blocks from nb on: the rows without an assignment.
 __global__ void __launch_bounds__(1024) place_kernel(const __grid_constant__ PlaceArgs a) {
   __shared__ int cnt[kMaxE], run[kMaxE], off[kMaxE + 1], start[kMaxE + 1];
-  __shared__ unsigned long long scan[32];
+  __shared__ int2 scan[32];
   extern __shared__ uint32_t dyn[];
   let_next_start();
   const int b = blockIdx.x;
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = run[e] = 0;
   __syncthreads();
   wait_for_previous();
-  // threads (slice, expert): each adds up some of the histograms
-  const int slices = (int)blockDim.x / a.E;                  // (E <= 1024 threads)
-  const int e = threadIdx.x % a.E, slice = threadIdx.x / a.E;
+  // threads (slice, four experts): each adds up some of the histograms, all loads at once
+  const int four = padded4(a.E) / 4, slices = (int)blockDim.x / four, slice = threadIdx.x / four;
+  const int e4 = threadIdx.x % four * 4;
   if (slice < slices) {
-    int total = 0, before = 0;
-#pragma unroll 16
+    int4 total = make_int4(0, 0, 0, 0), before = total;
+#pragma unroll 10
     for (int i = slice; i < a.nb; i += slices) {
-      const int c = a.hist[(int64_t)i * a.E + e];
-      total += c;
-      before += i < b ? c : 0;
+      const int4 c = *reinterpret_cast<const int4*>(a.hist + (int64_t)i * padded4(a.E) + e4);
+      total.x += c.x; total.y += c.y; total.z += c.z; total.w += c.w;
+      if (i < b) {
+        before.x += c.x; before.y += c.y; before.z += c.z; before.w += c.w;
+      }
     }
-    atomicAdd(&cnt[e], total);
-    atomicAdd(&run[e], before);
+    // (elements behind E are not written: they belong to no expert)
+    const int t[4] = {total.x, total.y, total.z, total.w}, f[4] = {before.x, before.y, before.z, before.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e4 + i < a.E) {
+        atomicAdd(&cnt[e4 + i], t[i]);
+        if (b < a.nb) atomicAdd(&run[e4 + i], f[i]);
+      }
   }
   __syncthreads();
   scan_experts(cnt, a.E, off, start, scan);
@@ -1168,8 +1540,31 @@ template <typename X, int C>
 cudaError_t run_score(const ScoreArgs& a, const PlaceArgs& p, int blocks, cudaStream_t s) {
   return a.groups > 1 ? run_score<X, C, true>(a, p, blocks, s) : run_score<X, C, false>(a, p, blocks, s);
 }
+// Eight lanes per token: for at least kManyTokens per block (the same work with a
+// longer way through it: XX).
+constexpr int kManyTokens = 32;
+template <typename X, int CL>
+cudaError_t run_many(ScoreArgs a, int blocks, bool* taken, cudaStream_t s) {
+  constexpr int kVec = CL * (int)sizeof(X) < 16 ? CL * (int)sizeof(X) : 16;
+  a.seg = a.group_size % CL ? 0 : a.group_size / CL;
+  for (a.seg_log = 0; 1 << a.seg_log < a.seg;) ++a.seg_log;
+  *taken = ((uintptr_t)a.logits & (kVec - 1)) == 0 && a.ld * sizeof(X) % kVec == 0 && a.E * sizeof(X) % kVec == 0 &&
+           (a.groups == 1 || (a.seg > 0 && !(a.seg & (a.seg - 1))));
+  if (!*taken) return cudaSuccess;
+  return a.groups > 1 ? launch_overlapped(score_many_kernel<X, CL, true>, blocks, kManyThreads, 0, s, a)
+                      : launch_overlapped(score_many_kernel<X, CL, false>, blocks, kManyThreads, 0, s, a);
+}
+
 template <typename X>
 cudaError_t run_score(const ScoreArgs& a, const PlaceArgs& p, int blocks, cudaStream_t s) {
+  if (a.per_block >= kManyTokens && blocks > 1 && a.k <= 8 && a.E <= 256) {
+    bool taken = false;
+    const cudaError_t e = a.E <= 32 ? run_many<X, 4>(a, blocks, &taken, s)
+                          : a.E <= 64 ? run_many<X, 8>(a, blocks, &taken, s)
+                          : a.E <= 128 ? run_many<X, 16>(a, blocks, &taken, s)
+                                       : run_many<X, 32>(a, blocks, &taken, s);
+    if (e != cudaSuccess || taken) return e;
+  }
   if (a.E <= 32) return run_score<X, 1>(a, p, blocks, s);
   if (a.E <= 64) return run_score<X, 2>(a, p, blocks, s);
   if (a.E <= 128) return run_score<X, 4>(a, p, blocks, s);
@@ -1183,7 +1578,7 @@ cudaError_t run_score(const ScoreArgs& a, const PlaceArgs& p, int blocks, cudaSt
 size_t router_workspace_bytes(const moe_router_dims& d) {
   const int per = tokens_per_block(d.T);
   const size_t nb = ((size_t)d.T + per - 1) / per;
-  return 16 + nb * d.E * sizeof(int32_t);
+  return 16 + nb * padded4(d.E) * sizeof(int32_t);
 }
 
 cudaError_t launch_router(const moe_router_dims& d, const void* logits, const float* bias, const moe_route_out& o,

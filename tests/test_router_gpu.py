@@ -106,7 +106,17 @@ CASES = [
     (611, 257, 9, dict(score="sigmoid", renormalise=False)), (300, 512, 16, dict(groups=32, top_groups=5, group_top=1)),
     (97, 1000, 31, dict(score="sigmoid", groups=10, top_groups=7, group_top=2)), (40, 1024, 32, dict(score="sigmoid")),
     (700, 24, 2, dict(groups=12, top_groups=1, group_top=2, renormalise=False)),
+    # many tokens per block: eight lanes per token, in whole and part rows, and what it leaves to the others
+    (5003, 60, 6, {}), (4901, 128, 8, dict(renormalise=False)), (5003, 32, 8, dict(score="sigmoid", renormalise=False)),
+    (4999, 256, 8, dict(groups=4, top_groups=2, group_top=2)), (5001, 248, 7, dict(score="sigmoid")), (5000, 20, 1, {}),
+    (4903, 128, 5, dict(score="sigmoid", groups=8, top_groups=3, group_top=2)), (5000, 96, 9, {}),
+    (4905, 64, 3, dict(score="sigmoid", groups=2, top_groups=1, group_top=1)), (4870, 30, 4, {}),
 ]
+
+
+def _many(l, many):
+    """The same rows as often as blocks of many tokens need."""
+    return np.tile(l, (-(-5000 // len(l)), 1)) if many else l
 
 
 @pytest.mark.parametrize("T,E,k,how", CASES)
@@ -123,7 +133,8 @@ def test_router_matches_definition(T, E, k, how, biased, dtype, pad):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups", [1, 4])
-def test_close_values_are_chosen_in_64_bits(score, groups):
+@pytest.mark.parametrize("many", [False, True])
+def test_close_values_are_chosen_in_64_bits(score, groups, many):
     """Values apart by less than fp32 can tell: the bias makes up for the score's
     difference up to its own last bits."""
     rng = np.random.default_rng(11)
@@ -134,14 +145,15 @@ def test_close_values_are_chosen_in_64_bits(score, groups):
     l[1::2] = l[0]
     l[1::2] += rng.integers(0, 3, (T // 2, E)).astype(np.float32) * np.float32(2.0 ** -22)
     how = dict(score=score, groups=groups, top_groups=max(1, groups // 2), group_top=2 if groups > 1 else 1)
-    l, r, dg, dl = _run(l, bias, 6, **how)
+    l, r, dg, dl = _run(_many(l, many), bias, 6, **how)
     _check(l, bias, 6, r, dg, dl, **how)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [None, 0.0, 0.25])
 @pytest.mark.parametrize("groups", [1, 4])
-def test_ties_go_to_the_lower_index(score, bias, groups):
+@pytest.mark.parametrize("many", [False, True])
+def test_ties_go_to_the_lower_index(score, bias, groups, many):
     """Equal logits (a router of zeros, logits of few values) with equal biases."""
     rng = np.random.default_rng(5)
     l = rng.integers(0, 2, (300, 40)).astype(np.float32)
@@ -150,13 +162,32 @@ def test_ties_go_to_the_lower_index(score, bias, groups):
     l[60:70, ::2] = -0.0
     b = None if bias is None else np.full(40, bias, np.float32)
     how = dict(score=score, groups=groups, top_groups=max(1, groups // 2), group_top=2 if groups > 1 else 1)
-    l, r, dg, dl = _run(l, b, 7, **how)
+    l, r, dg, dl = _run(_many(l, many), b, 7, **how)
     _check(l, b, 7, r, dg, dl, **how)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("E", [32, 100, 256])
+@pytest.mark.parametrize("bias", [None, 0.25])
+def test_a_few_equal_logits(dtype, E, bias):
+    """Two to five equal values among others, at the front, inside and at the end of
+    the chosen, in any places."""
+    rng = np.random.default_rng(E)
+    l = np.stack([rng.permutation(E) for _ in range(5000)]).astype(np.float32) / 64 - 1
+    order = np.argsort(-l, 1)
+    for t in range(5000):
+        i, n = rng.integers(0, 8), rng.integers(2, 6)
+        l[t, order[t, i:i + n]] = l[t, order[t, i]]
+    b = None if bias is None else np.full(E, bias, np.float32)
+    how = dict(score="sigmoid")
+    l, r, dg, dl = _run(l, b, 6, dtype, **how)
+    _check(l, b, 6, r, dg, dl, **how)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
-def test_masked_experts(score, renorm):
+@pytest.mark.parametrize("many", [False, True])
+def test_masked_experts(score, renorm, many):
     """-inf and the type's lowest value in masked places, tokens with fewer
     experts than top_k, with none, and groups left empty; large logits."""
     rng = np.random.default_rng(6)
@@ -169,12 +200,9 @@ def test_masked_experts(score, renorm):
     how = dict(score=score, renormalise=renorm)
     for bias, more in ((None, {}), (rng.standard_normal(32).astype(np.float32), {}),
                        (None, dict(groups=4, top_groups=2, group_top=1))):
-        x, r, dg, dl = _run(l, bias, 4, **how, **more)
-        if bias is None:
-            _check(x, bias, 4, r, dg, dl, **how, **more)
-        else:
-            # (scores of the lowest value are 0 in 64 bits, like those of logits below -745)
-            _check(x, bias, 4, r, dg, dl, **how, **more)
+        # (scores of the lowest value are 0 in 64 bits, like those of logits below -745)
+        x, r, dg, dl = _run(_many(l, many), bias, 4, **how, **more)
+        _check(x, bias, 4, r, dg, dl, **how, **more)
         assert r.device_status() == 0
 
 
@@ -186,8 +214,8 @@ def test_bad_logits_are_reported():
     base = rng.standard_normal((50, 32)).astype(np.float32)
     b = (0.1 * rng.standard_normal(32)).astype(np.float32)
     for bad in ("row", "nan", "inf", "bias"):
-        for score in ("softmax", "sigmoid"):
-            l, bias = base.copy(), b.copy()
+        for score, many in (("softmax", False), ("sigmoid", False), ("softmax", True), ("sigmoid", True)):
+            l, bias = _many(base.copy(), many), b.copy()
             if bad == "row":
                 l[7] = -np.inf
             elif bad == "bias":
