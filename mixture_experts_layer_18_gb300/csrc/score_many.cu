@@ -1,0 +1,428 @@
+// score_many.cu - the router by scores (score_route.cu) for many tokens.
+#include "score_route.cuh"
+
+namespace moe {
+
+namespace {
+
+// Many tokens: eight lanes per token, four tokens per warp, so that what a token
+// takes besides its elements (rounds, gates, addresses) is paid once for four.
+// E <= 8 CL, top_k <= 8, a group is a power of two of lanes or all there is; rows by
+// vectors.  Of fp32 logits a key's index is that within the lane, which leaves more bits
+// to the value.
+__device__ __forceinline__ uint32_t max8(uint32_t v) {          // over a token's lanes
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// As order(), for up to 16 candidates of each of four tokens: lane sl of a token
+// has candidates sl and sl + 8 (n: how many the token has).  Returns the lane's
+// expert in that order, -1 to all lanes of a token whose order is not known.
+template <typename X, int CL>
+__device__ __noinline__ int order8(const ScoreArgs& a, const X* row, int e0, int e1, float l0, float l1, float b0, float b1,
+                                   int n, float top, float inv, int* slot) {
+  const int e[2] = {e0, e1};
+  const float l[2] = {l0, l1}, b[2] = {b0, b1};
+  const int sl = threadIdx.x & 7, first = threadIdx.x & 24;
+  const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
+  float v[2];
+  bool on[2];
+  int better[2] = {0, 0};
+  bool unsure = false;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    on[r] = sl + 8 * r < n && l[r] > -INFINITY;
+    v[r] = !on[r] || by_logit ? l[r] : score_of(a, l[r], top, inv) + b[r];
+  }
+  const int most = (int)__reduce_max_sync(kAll, (unsigned)n);
+  for (int i = 0; i < most; ++i) {
+    const int at = first + (i & 7);
+    const float ov = __shfl_sync(kAll, i < 8 ? v[0] : v[1], at), ol = __shfl_sync(kAll, i < 8 ? l[0] : l[1], at);
+    const float ob = __shfl_sync(kAll, i < 8 ? b[0] : b[1], at);
+    const int oe = __shfl_sync(kAll, i < 8 ? e[0] : e[1], at);
+    const bool other = ol > -INFINITY;
+    if (i >= n) continue;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (sl + 8 * r >= n || oe == e[r]) continue;
+      const float gap = near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(v[r]), fabsf(ov)));
+      if ((ol == l[r] && ob == b[r]) || (!on[r] && !other)) better[r] += oe < e[r];
+      else if (!on[r] || !other) better[r] += other;               // masked ones last
+      else if (by_logit || fabsf(ov - v[r]) > gap) better[r] += ov > v[r] || (ov == v[r] && oe < e[r]);
+      else unsure = true;
+    }
+  }
+  unsigned open = __ballot_sync(kAll, unsure);
+  if (open) {
+    Pair scale{};
+    if (!a.sigmoid) {
+      for (int t = 0; t < 32; t += 8)                        // a token at a time, by the whole warp
+        if (open >> t & 0xffu) {
+          const X* r = reinterpret_cast<const X*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(row), t));
+          const Pair p = softmax_scale(a, r, __shfl_sync(kAll, top, t));
+          if (first == t) scale = p;
+        }
+    }
+    const Exact x0 = exact_value(a.sigmoid, l[0], b[0], top, scale), x1 = exact_value(a.sigmoid, l[1], b[1], top, scale);
+    better[0] = better[1] = 0;
+    unsure = false;
+    for (int i = 0; i < most; ++i) {
+      const int at = first + (i & 7);
+      const float oh = __shfl_sync(kAll, i < 8 ? x0.u.h : x1.u.h, at), olow = __shfl_sync(kAll, i < 8 ? x0.u.l : x1.u.l, at);
+      const float oo = __shfl_sync(kAll, i < 8 ? x0.off : x1.off, at), ol = __shfl_sync(kAll, i < 8 ? l[0] : l[1], at);
+      const float ob = __shfl_sync(kAll, i < 8 ? b[0] : b[1], at), ov = __shfl_sync(kAll, i < 8 ? v[0] : v[1], at);
+      const int oe = __shfl_sync(kAll, i < 8 ? e[0] : e[1], at);
+      const bool other = ol > -INFINITY;
+      if (i >= n) continue;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (sl + 8 * r >= n || oe == e[r]) continue;
+        const Exact& x = r ? x1 : x0;
+        const float gap = near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(v[r]), fabsf(ov)));
+        const float d = (oh - x.u.h) + (olow - x.u.l);
+        if ((ol == l[r] && ob == b[r]) || (!on[r] && !other)) better[r] += oe < e[r];
+        else if (!on[r] || !other) better[r] += other;
+        else if (by_logit || fabsf(ov - v[r]) > gap) better[r] += ov > v[r] || (ov == v[r] && oe < e[r]);
+        else if (fabsf(d) > oo + x.off) better[r] += d > 0.f;
+        else unsure = true;
+      }
+    }
+    open = __ballot_sync(kAll, unsure);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    if (sl + 8 * r < n) slot[first * 2 + better[r]] = e[r];
+  __syncwarp();
+  return open >> first & 0xffu ? -1 : sl < n ? slot[first * 2 + sl] : 0;
+}
+
+// A lane's best keys, the largest first (more are looked for again when these are
+// taken: 0.6 times a token with three of 16 kept, with four of 32 and half of the groups gone).
+template <int CL>
+struct BestKeys {
+  static constexpr int K = CL > 16 ? 4 : 3;
+  uint32_t m[K];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < K; ++i) m[i] = 0;
+  }
+  __device__ __forceinline__ void insert(uint32_t k) {
+#pragma unroll
+    for (int i = K - 1; i > 0; --i) m[i] = max(m[i], min(m[i - 1], k));
+    m[0] = max(m[0], k);
+  }
+  __device__ __forceinline__ void pop(const uint32_t (&key)[CL]) {
+    const uint32_t last = m[0];
+#pragma unroll
+    for (int i = 0; i + 1 < K; ++i) m[i] = m[i + 1];
+    m[K - 1] = 0;
+    if (m[0] == 0) {
+#pragma unroll
+      for (int q = 0; q < CL; ++q)
+        if (key[q] < last) m[0] = max(m[0], key[q]);
+    }
+  }
+};
+
+template <int CL>
+constexpr int kManyThreads = CL > 16 ? 512 : 640;
+
+template <typename X, int CL, bool GROUPED>
+__global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const __grid_constant__ ScoreArgs a) {
+  constexpr bool kLossless = sizeof(X) == 2;            // a bf16 logit is all leading bits:
+  constexpr uint32_t kIndex = (kLossless ? 8 : 1) * CL - 1;    // a key then holds the expert's index, else that in the lane
+  constexpr float kLead = (kIndex + 1) * 0x1p-23f;      // what it takes from the value, relative to it
+  constexpr int V = CL * (int)sizeof(X) < 16 ? CL : 16 / (int)sizeof(X);
+  __shared__ int hist[8 * CL];
+  __shared__ __align__(16) float bias[8 * (CL + 4)];    // (rows of lanes apart by 4 banks)
+  __shared__ uint2 slots[kManyThreads<CL> / 32][33];
+  __shared__ int units;
+  let_next_start();
+  for (int e = threadIdx.x; e < 8 * CL; e += kManyThreads<CL>) hist[e] = 0;
+  if (threadIdx.x == 0) units = 0;
+  wait_for_previous();
+  bool bad = false, unused = false;
+  const bool by_logit = !a.bias && (!GROUPED || a.group_top == 1);
+  for (int e = threadIdx.x; e < 8 * CL; e += kManyThreads<CL>) {
+    float b = 0.f;
+    if (a.bias && e < a.E) {
+      b = bias_of(a, e);
+      if (!(fabsf(a.bias[e]) < INFINITY)) bad = true;
+    }
+    bias[e / CL * (CL + 4) + e % CL] = b;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, sl = lane & 7, first = lane & 24;
+  const unsigned below = ((1u << sl) - 1u) << first;
+  uint2* slot = slots[threadIdx.x >> 5];
+  int* slot_e = reinterpret_cast<int*>(slot);           // [4 tokens][16]
+  const float* my_bias = bias + sl * (CL + 4);
+  const uint32_t index0 = kIndex - (kLossless ? sl * CL : 0);   // a key's index of the lane's first expert
+  float bias_most = 0.f;
+  if (a.bias) {
+#pragma unroll
+    for (int q = 0; q < CL; ++q) bias_most = fmaxf(bias_most, fabsf(my_bias[q]));
+    bias_most = __uint_as_float(max8(__float_as_uint(bias_most)));
+  }
+  auto leading = [](uint32_t key) {
+    const uint32_t k = key & ~kIndex;
+    return k > 0x007fffffu ? value_of(k) : -INFINITY;   // (-inf, and none)
+  };
+  const int64_t t0 = (int64_t)blockIdx.x * a.per_block, t1 = min((int64_t)a.T, t0 + a.per_block);
+  for (;;) {
+    // warps take the block's tokens as they come: one that has to look closer delays no others
+    int unit = 0;
+    if (lane == 0) unit = atomicAdd(&units, 1);
+    const int64_t tb = t0 + (int64_t)__shfl_sync(kAll, unit, 0) * 4;
+    if (tb >= t1) break;
+    const int64_t t = min(tb + (lane >> 3), t1 - 1);    // (past the end: the last token again, not stored)
+    const bool mine_on = tb + (lane >> 3) < t1;
+    const X* row = static_cast<const X*>(a.logits) + t * a.ld;
+    float u[CL];
+    rows::F2 finite = rows::f2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < CL / V; ++i) {
+      const int e = sl * CL + i * V;
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (e < a.E) {
+        if constexpr (V * sizeof(X) == 16) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + e));
+          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + e));
+          w[0] = x.x; w[1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        u[i * V + j] = sizeof(X) == 4 ? __uint_as_float(w[j & 3]) : j & 1 ? bf16_hi(w[(j / 2) & 3]) : bf16_lo(w[(j / 2) & 3]);
+    }
+#pragma unroll
+    for (int q = 0; q < CL; q += 2)                     // NaN after an infinity or a NaN
+      finite = rows::fma2(rows::f2(u[q], u[q + 1]), rows::f2(0.f, 0.f), finite);
+    const bool plain = !__any_sync(kAll, rows::sum2(finite) != 0.f) && a.E == 8 * CL;
+    if (!plain) {
+#pragma unroll
+      for (int q = 0; q < CL; ++q) {
+        const bool there = sl * CL + q < a.E;
+        if (there && !(u[q] < INFINITY)) bad = true;    // NaN and +inf read as -inf
+        if (!there || !(u[q] < INFINITY)) u[q] = -INFINITY;
+      }
+    }
+    float top = 0.f, sum = 1.f;
+    if (!a.sigmoid && (!by_logit || !a.renorm)) {
+      float m = u[0];
+#pragma unroll
+      for (int q = 1; q < CL; ++q) m = fmaxf(m, u[q]);
+      top = value_of(max8(key_of(m)));
+      top = top > -INFINITY ? top : 0.f;
+      sum = 0.f;
+      if (by_logit) {
+#pragma unroll
+        for (int q = 0; q < CL; ++q) sum += fast_exp(u[q] - top);
+      } else {                                          // (a masked expert is marked by -1)
+#pragma unroll
+        for (int q = 0; q < CL; ++q) {
+          const float x = fast_exp(u[q] - top);
+          sum += x;
+          u[q] = !plain && !(u[q] > -INFINITY) ? -1.f : x;
+        }
+      }
+      sum = sum8(sum);
+    }
+    const float inv = a.sigmoid ? 1.f : __fdividef(1.f, sum);
+    // the keys; what is no expert counts as a masked one behind them
+    uint32_t key[CL];
+    BestKeys<CL> best;
+    best.clear();
+    auto take = [&](int q, float v) {
+      key[q] = (key_of(v) & ~kIndex) | (index0 - q);
+      best.insert(key[q]);
+    };
+    auto biased = [&](auto score) {
+#pragma unroll
+      for (int i = 0; i < CL; i += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(my_bias + i);
+        take(i, score(u[i], b.x));
+        take(i + 1, score(u[i + 1], b.y));
+        take(i + 2, score(u[i + 2], b.z));
+        take(i + 3, score(u[i + 3], b.w));
+      }
+    };
+    if (by_logit) {
+#pragma unroll
+      for (int q = 0; q < CL; ++q) take(q, u[q]);
+    } else if (!plain) {
+      biased([&](float x, float b) {
+        const float s = a.sigmoid ? __fdividef(1.f, 1.f + fast_exp(-x)) : x * inv;
+        return (a.sigmoid ? x > -INFINITY : x >= 0.f) ? s + b : -INFINITY;
+      });
+    } else if (a.sigmoid) {
+      biased([&](float x, float b) { return __fdividef(1.f, 1.f + fast_exp(-x)) + b; });
+    } else {
+      biased([&](float x, float b) { return x * inv + b; });
+    }
+    bool again = false;                                 // (the same in a token's lanes)
+    if (GROUPED) {
+      uint32_t g1 = best.m[0], g2 = best.m[1];
+      for (int o = 1; o < a.seg; o <<= 1) {
+        const uint32_t n1 = __shfl_xor_sync(kAll, g1, o), n2 = __shfl_xor_sync(kAll, g2, o);
+        g2 = max(min(g1, n1), max(g2, n2));
+        g1 = max(g1, n1);
+      }
+      const int own = sl >> a.seg_log;
+      float mine = -INFINITY;
+      if (own < a.groups) mine = a.group_top == 1 ? leading(g1) : leading(g1) + leading(g2);
+      int better = 0;
+      for (int g = 0; g < a.groups; ++g) {
+        const float v = __shfl_sync(kAll, mine, first + (g << a.seg_log));
+        better += v > mine || (v == mine && g < own);
+      }
+      bool stays = own < a.groups && better < a.top_groups;
+      if (a.top_groups < a.groups) {
+        const float lo = -value_of(max8(stays ? key_of(-mine) : 0x007fffffu));   // (-inf)
+        const float hi = value_of(max8(own < a.groups && !stays ? key_of(mine) : 0x007fffffu));
+        // (a value is up to kLead of itself above its leading bits)
+        const float most = bias_most + (a.sigmoid ? 1.f : inv);
+        const float gap = by_logit ? 0.f : 2.f * near_of<CL>(a.sigmoid, inv, 2.f * most) + 2.f * kLead * most;
+        again = hi > -INFINITY && !(lo - hi > gap || (by_logit && kLossless));
+        if (a.seg == 1 && a.sigmoid && !by_logit && __any_sync(kAll, again)) {
+          // a lane's own best, if no third one comes near the last of them
+          const float last = leading(a.group_top == 1 ? best.m[0] : best.m[1]);
+          const float next = leading(a.group_top == 1 ? best.m[1] : best.m[2]);
+          const bool live = own < a.groups && last > -INFINITY;
+          bool unsure = live && next > -INFINITY && !(last - next > near_of<CL>(a.sigmoid, inv, last) + kLead * fabsf(last));
+          const int q0 = (index0 - (best.m[0] & kIndex)) & (CL - 1), q1 = (index0 - (best.m[1] & kIndex)) & (CL - 1);
+          const bool two = live && a.group_top == 2;
+          const bool s = better_groups(a, live ? logit(a, row, sl * CL + q0, &unused) : 0.f, live ? my_bias[q0] : 0.f,
+                                       two ? logit(a, row, sl * CL + q1, &unused) : 0.f, two ? my_bias[q1] : 0.f, live, own,
+                                       first, 0, top, Pair{}, &unsure);
+          const unsigned open = __ballot_sync(kAll, unsure);
+          if (again && !(open >> first & 0xffu)) {
+            stays = s;
+            again = false;
+          }
+        }
+      }
+      if (!stays) best.clear();
+    }
+    // rounds of a maximum over the token's lanes: k, and more while the next may be as good as the k-th
+    uint32_t sel = 0;
+    int n = 0;
+    float last = -INFINITY;
+    bool stop = false;
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t m = max8(best.m[0]);
+      if (i >= a.k) {
+        const float v = leading(m);
+        const float gap = by_logit ? 0.f : near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(v))) + kLead * fabsf(v);
+        stop = stop || (by_logit && kLossless) || !(v > -INFINITY) || last - v > gap;
+        if (!__any_sync(kAll, !stop)) break;
+      } else if (i == a.k - 1) {
+        last = leading(m);
+      }
+      const unsigned who = __ballot_sync(kAll, best.m[0] == m);
+      if (!stop) {
+        ++n;
+        if (sl == i) sel = m;
+        if (best.m[0] == m && !(who & below)) {         // (of equal ones the first lane)
+          slot_e[first * 2 + i] = (kLossless ? 0 : sl * CL) + (int)(kIndex - (m & kIndex));
+          best.pop(key);
+        }
+      }
+    }
+    __syncwarp();
+    int e = sl < n ? slot_e[first * 2 + sl] : 0;
+    float l = sl < n ? logit(a, row, e, &unused) : -INFINITY;
+    if (!(by_logit && kLossless)) {
+      // (equal keys of two lanes came by their place in the lane: masked ones are chosen again)
+      if (!kLossless && !(last > -INFINITY)) again = true;
+      // is the order of neighbours certain?
+      const float v = leading(sel), pv = __shfl_up_sync(kAll, v, 1, 8), pl = __shfl_up_sync(kAll, l, 1, 8);
+      const float b = sl < n ? bias[e / CL * (CL + 4) + e % CL] : 0.f, pb = __shfl_up_sync(kAll, b, 1, 8);
+      const float gap = by_logit ? 0.f : near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(pv), fabsf(v))) + kLead * fabsf(v);
+      const int pe = __shfl_up_sync(kAll, e, 1, 8);
+      const bool close = sl > 0 && v > -INFINITY && !(pv - v > gap) && !(pl == l && pb == b && pe < e);
+      bool open = again || n == 16;              // (16: there may be more)
+      if (__any_sync(kAll, close || n > a.k || open)) {
+        const int e2 = sl + 8 < n ? slot_e[first * 2 + sl + 8] : 0;
+        const float l2 = sl + 8 < n ? logit(a, row, e2, &unused) : -INFINITY;
+        const float b2 = sl + 8 < n ? bias[e2 / CL * (CL + 4) + e2 % CL] : 0.f;
+        e = order8<X, CL>(a, row, e, e2, l, l2, b, b2, n, top, inv, slot_e);
+        open = open || e < 0;
+        const unsigned left = __ballot_sync(kAll, open);
+        for (int o = 0; o < 32; o += 8)                  // what is left, a token at a time by the whole warp
+          if (left >> o & 0xffu) {
+            const X* r = reinterpret_cast<const X*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(row), o));
+            const int x = choose32<X, (CL + 3) / 4, GROUPED>(a, r, slot);
+            const int ex = __shfl_sync(kAll, x, sl);
+            if (first == o) e = ex;
+          }
+        if (sl < a.k) l = logit(a, row, e, &unused);
+      }
+    }
+    __syncwarp();                                       // (the slots are written again)
+    if (sl >= a.k) l = -INFINITY;
+    // gates, as above
+    const bool none = !(__ballot_sync(kAll, l > -INFINITY) >> first & 0xffu);
+    float w = !(l > -INFINITY) ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - top);
+    if (a.renorm) {
+      const bool small = !(__ballot_sync(kAll, l > -60.f) >> first & 0xffu);
+      if (!a.sigmoid || __any_sync(kAll, small)) {
+        const float x = a.sigmoid ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;
+        const float m = value_of(max8(key_of(x)));
+        if (!a.sigmoid || small) w = l > -INFINITY ? expf(x - m) : 0.f;
+      }
+      w = w / sum8(w);
+    } else if (!a.sigmoid) {
+      w = w / sum;
+    }
+    if (none && mine_on) bad = true;
+    if (mine_on && sl < a.k) {
+      a.idx[t * a.k + sl] = e;
+      a.gate[t * a.k + sl] = none ? 0.f : a.scale * w;
+      atomicAdd(&hist[e], 1);
+    }
+  }
+  if (bad) report(a.status, MOE_ERR_BAD_INPUT);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kManyThreads<CL>) a.hist[(int64_t)blockIdx.x * padded4(a.E) + e] = hist[e];
+}
+
+// Eight lanes per token: for at least kManyTokens per block (the same work with a
+// longer way through it: XX).
+constexpr int kManyTokens = 32;
+template <typename X, int CL>
+cudaError_t run_many(ScoreArgs a, int blocks, bool* taken, cudaStream_t s) {
+  constexpr int kVec = CL * (int)sizeof(X) < 16 ? CL * (int)sizeof(X) : 16;
+  a.seg = a.group_size % CL ? 0 : a.group_size / CL;
+  for (a.seg_log = 0; 1 << a.seg_log < a.seg;) ++a.seg_log;
+  *taken = ((uintptr_t)a.logits & (kVec - 1)) == 0 && a.ld * sizeof(X) % kVec == 0 && a.E * sizeof(X) % kVec == 0 &&
+           (a.groups == 1 || (a.seg > 0 && !(a.seg & (a.seg - 1))));
+  if (!*taken) return cudaSuccess;
+  return a.groups > 1 ? launch_overlapped(score_many_kernel<X, CL, true>, blocks, kManyThreads<CL>, 0, s, a)
+                      : launch_overlapped(score_many_kernel<X, CL, false>, blocks, kManyThreads<CL>, 0, s, a);
+}
+
+}  // namespace
+
+template <typename X>
+cudaError_t launch_score_many(const ScoreArgs& a, int blocks, bool* taken, cudaStream_t s) {
+  *taken = false;
+  if (a.per_block < kManyTokens || blocks < 2 || a.k > 8 || a.E > 256) return cudaSuccess;
+  return a.E <= 32 ? run_many<X, 4>(a, blocks, taken, s)
+         : a.E <= 64 ? run_many<X, 8>(a, blocks, taken, s)
+         : a.E <= 128 ? run_many<X, 16>(a, blocks, taken, s)
+                      : run_many<X, 32>(a, blocks, taken, s);
+}
+template cudaError_t launch_score_many<float>(const ScoreArgs&, int, bool*, cudaStream_t);
+template cudaError_t launch_score_many<__nv_bfloat16>(const ScoreArgs&, int, bool*, cudaStream_t);
+
+}  // namespace moe
