@@ -132,7 +132,7 @@ struct BestKeys {
 };
 
 template <int CL>
-constexpr int kManyThreads = CL > 16 ? 512 : 640;
+constexpr int kManyThreads = CL > 16 ? 512 : 736;
 
 template <typename X, int CL, bool GROUPED>
 __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const __grid_constant__ ScoreArgs a) {

@@ -44,28 +44,32 @@ struct PlaceArgs {
 };
 
 constexpr int kPerThread = 8;
-__device__ __forceinline__ void place_tokens(const PlaceArgs& a, int64_t t0, int64_t t1, int* run, uint32_t* bits) {
+__device__ __forceinline__ void place_tokens(const PlaceArgs& a, const int32_t* all_idx, int64_t t0, int64_t t1, int* run,
+                                             uint32_t* bits) {
   const int round = 32 * a.words;
   for (int64_t base = t0; base < t1; base += round) {
     const int n = (int)min((int64_t)round, t1 - base), words = (n + 31) >> 5;
     for (int i = threadIdx.x; i < words * a.E; i += blockDim.x) bits[i] = 0;
     __syncthreads();
-    const int32_t* idx = a.idx + base * a.k;
+    const int32_t* idx = all_idx + base * a.k;
     const int m = n * a.k;                                     // (at most kPerThread per thread)
     int e[kPerThread];
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       const int i = threadIdx.x + j * blockDim.x;
-      e[j] = i < m ? idx[i] : -1;
+      e[j] = -1;
+      if (i < m) e[j] = idx[i];
     }
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
+      if (j * (int)blockDim.x >= m) break;
       const int t = (int)((threadIdx.x + j * blockDim.x) * a.inv_k >> 32);
       if (e[j] >= 0) atomicOr(&bits[(t >> 5) * a.E + e[j]], 1u << (t & 31));
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
+      if (j * (int)blockDim.x >= m) break;
       if (e[j] < 0) continue;
       const int i = threadIdx.x + j * blockDim.x, t = (int)(i * a.inv_k >> 32);
       int row = run[e[j]] + __popc(bits[(t >> 5) * a.E + e[j]] & ((1u << (t & 31)) - 1u));
@@ -139,13 +143,12 @@ __device__ __forceinline__ void no_assignment(const PlaceArgs& a, int64_t r0, in
   }
 }
 
-// Rows without an assignment up to row `end`: those behind each expert's, and behind the last.
-__device__ __forceinline__ void fill_rows(const PlaceArgs& a, const int* cnt, const int* start, int64_t end, int b,
-                                          int nb) {
+// Rows without an assignment: those behind each expert's (a warp per expert), and behind the last.
+__device__ __forceinline__ void fill_rows(const PlaceArgs& a, const int* cnt, const int* start, int b, int nb) {
   const int w = threadIdx.x >> 5, nw = blockDim.x >> 5, lane = threadIdx.x & 31;
   for (int e = b * nw + w; e < a.E; e += nb * nw)
     for (int r = start[e] + cnt[e] + lane; r < start[e + 1]; r += 32) a.assign_of[r] = -1;
-  no_assignment(a, start[a.E], end, b, nb);
+  no_assignment(a, start[a.E], a.max_rows, b, nb);
 }
 
 // Threads of a block at most: the keys of wider rows take more registers.
@@ -161,6 +164,7 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
   __shared__ uint2 slots[32][33];
   __shared__ int2 scan[32];
   extern __shared__ uint32_t dyn[];
+  int* chosen = reinterpret_cast<int*>(dyn) + (3 + p.words) * a.E + 2;    // [T][k], with p.nb 1
   let_next_start();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
@@ -182,6 +186,8 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
     return k > 0x007fffffu ? value_of(k) : -INFINITY;   // (-inf, and none)
   };
   int64_t t = t0 + (threadIdx.x >> 5);
+  Logits<X, C> next;
+  if (t < t1) next.load(static_cast<const X*>(a.logits) + t * a.ld, a.E, a.vec);
   float bias[C], bias_most = 0.f;
   bool bad = false, unused = false;
 #pragma unroll
@@ -197,8 +203,6 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
     }
     bias_most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(bias_most)));
   }
-  Logits<X, C> next;
-  if (t < t1) next.load(static_cast<const X*>(a.logits) + t * a.ld, a.E, a.vec);
   for (; t < t1; t += nw) {
     const X* row = static_cast<const X*>(a.logits) + t * a.ld;
     const Logits<X, C> raw = next;
@@ -395,6 +399,7 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
     if (none) bad = true;
     if (lane < a.k) {
       a.idx[t * a.k + lane] = sel_e;
+      if (p.nb == 1) chosen[t * a.k + lane] = sel_e;
       a.gate[t * a.k + lane] = none ? 0.f : a.scale * w;
       atomicAdd(&hist[sel_e], 1);
     }
@@ -414,9 +419,10 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
       p.offsets[e] = off[e];
       p.padded[e] = start[e];
     }
+    // (no row has its assignment before place_tokens' barriers)
+    no_assignment(p, 0, gridDim.x > 1 ? p.sure : p.max_rows, 0, 1);
     __syncthreads();
-    place_tokens(p, 0, a.T, run, reinterpret_cast<uint32_t*>(run + a.E));
-    fill_rows(p, hist, start, gridDim.x > 1 ? p.sure : p.max_rows, 0, 1);
+    place_tokens(p, chosen, 0, a.T, run, reinterpret_cast<uint32_t*>(run + a.E));
   } else {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * padded4(a.E) + e] = hist[e];
   }
@@ -476,13 +482,13 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const __grid_const
       a.padded[i] = start[i];
     }
   if (b >= a.nb) {
-    fill_rows(a, cnt, start, a.max_rows, b - a.nb, gridDim.x - a.nb);
+    fill_rows(a, cnt, start, b - a.nb, gridDim.x - a.nb);
     return;
   }
   for (int i = threadIdx.x; i < a.E; i += blockDim.x) run[i] += start[i];
   __syncthreads();
   const int64_t t0 = (int64_t)b * a.per_block;
-  place_tokens(a, t0, min((int64_t)a.T, t0 + a.per_block), run, dyn);
+  place_tokens(a, a.idx, t0, min((int64_t)a.T, t0 + a.per_block), run, dyn);
 }
 
 // -------------------------------------------------------------- backward
@@ -606,7 +612,7 @@ cudaError_t run_score(ScoreArgs a, const PlaceArgs& p, int blocks, cudaStream_t 
   const int warps = blocks == 1 ? a.T : a.per_block, most = kRouteThreads<C>;
   if (blocks == 1) {
     const int threads = warps < 8 ? 256 : 32 * warps > most ? most : 32 * warps;
-    const int smem = ((3 + p.words) * a.E + 2) * 4;
+    const int smem = ((3 + p.words) * a.E + 2 + a.T * a.k) * 4;
     return launch_overlapped(score_route_kernel<X, C, GROUPED>, 1 + (unsigned)((p.max_rows - p.sure) / 4096),
                              threads, smem, s, a, p);
   }
@@ -654,8 +660,8 @@ cudaError_t launch_router(const moe_router_dims& d, const void* logits, const fl
     const cudaError_t e = d.type == MOE_TYPE_BF16 ? run_score<__nv_bfloat16>(a, p, nb, s) : run_score<float>(a, p, nb, s);
     if (e != cudaSuccess || nb == 1) return e;
   }
-  const int64_t fill = ((int64_t)kAlign * d.E + 8191) / 8192;
-  return launch_overlapped(place_kernel, nb + (unsigned)fill, kPlaceThreads, words * d.E * 4, s, p);
+  const int fill = (d.E + kPlaceThreads / 32 - 1) / (kPlaceThreads / 32);      // (a warp per expert)
+  return launch_overlapped(place_kernel, (unsigned)(nb + fill), kPlaceThreads, words * d.E * 4, s, p);
 }
 
 cudaError_t launch_router_backward(const moe_router_dims& d, const moe_route_out& o, const void* logits,
