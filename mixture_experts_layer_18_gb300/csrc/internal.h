@@ -194,7 +194,7 @@ cudaError_t launch_layer_norm_backward(const NormDesc& d, const void* dy, const 
 // score_route.cu
 size_t router_workspace_bytes(const moe_router_dims& d);
 cudaError_t launch_router(const moe_router_dims& d, const void* logits, const float* bias, const moe_route_out& o,
-                          int32_t* hist, int32_t* status, cudaStream_t s);
+                          uint16_t* hist, int32_t* status, cudaStream_t s);
 cudaError_t launch_router_backward(const moe_router_dims& d, const moe_route_out& o, const void* logits,
                                    const float* dgate, void* dlogits, int32_t* status, cudaStream_t s);
 cudaError_t launch_balance_bias(const int32_t* counts, int E, float rate, const float* bias, float* out,

@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
   }
   if (bad) report(a.status, MOE_ERR_BAD_INPUT);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kManyThreads<CL>) a.hist[(int64_t)blockIdx.x * padded4(a.E) + e] = hist[e];
+  for (int e = threadIdx.x; e < a.E; e += kManyThreads<CL>) a.hist[(int64_t)blockIdx.x * padded4(a.E) + e] = (uint16_t)hist[e];
 }
 
 // Eight lanes per token: for at least kManyTokens per block (the same work with a

@@ -32,7 +32,7 @@ namespace {
 // and expert, set in any order, counted up to the token's own.
 struct PlaceArgs {
   const int32_t* idx;
-  const int32_t* hist;       // [nb][padded4(E)]
+  const uint16_t* hist;      // [nb][padded4(E)]
   int T, k, E, nb, per_block, words;
   int64_t max_rows, sure;    // rows at or past `sure` belong to no expert, whatever the routing
   int32_t* counts;
@@ -47,10 +47,9 @@ constexpr int kPerThread = 8;
 __device__ __forceinline__ void place_tokens(const PlaceArgs& a, const int32_t* all_idx, int64_t t0, int64_t t1, int* run,
                                              uint32_t* bits) {
   const int round = 32 * a.words;
+  int* first = reinterpret_cast<int*>(bits) + a.words * a.E;   // [words][E]: the row of a word's first assignment
   for (int64_t base = t0; base < t1; base += round) {
     const int n = (int)min((int64_t)round, t1 - base), words = (n + 31) >> 5;
-    for (int i = threadIdx.x; i < words * a.E; i += blockDim.x) bits[i] = 0;
-    __syncthreads();
     const int32_t* idx = all_idx + base * a.k;
     const int m = n * a.k;                                     // (at most kPerThread per thread)
     int e[kPerThread];
@@ -60,6 +59,8 @@ __device__ __forceinline__ void place_tokens(const PlaceArgs& a, const int32_t* 
       e[j] = -1;
       if (i < m) e[j] = idx[i];
     }
+    for (int i = threadIdx.x; i < words * a.E; i += blockDim.x) bits[i] = 0;
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       if (j * (int)blockDim.x >= m) break;
@@ -67,29 +68,32 @@ __device__ __forceinline__ void place_tokens(const PlaceArgs& a, const int32_t* 
       if (e[j] >= 0) atomicOr(&bits[(t >> 5) * a.E + e[j]], 1u << (t & 31));
     }
     __syncthreads();
+    for (int x = threadIdx.x; x < a.E; x += blockDim.x) {
+      int row = run[x];
+#pragma unroll 4
+      for (int w = 0; w < words; ++w) {
+        first[w * a.E + x] = row;
+        row += __popc(bits[w * a.E + x]);
+      }
+      run[x] = row;
+    }
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       if (j * (int)blockDim.x >= m) break;
       if (e[j] < 0) continue;
-      const int i = threadIdx.x + j * blockDim.x, t = (int)(i * a.inv_k >> 32);
-      int row = run[e[j]] + __popc(bits[(t >> 5) * a.E + e[j]] & ((1u << (t & 31)) - 1u));
-#pragma unroll 4
-      for (int w = 0; w < t >> 5; ++w) row += __popc(bits[w * a.E + e[j]]);
+      const int i = threadIdx.x + j * blockDim.x, t = (int)(i * a.inv_k >> 32), at = (t >> 5) * a.E + e[j];
+      const int row = first[at] + __popc(bits[at] & ((1u << (t & 31)) - 1u));
       a.row_of[base * a.k + i] = row;
       a.assign_of[row] = (int)(base * a.k + i);
     }
-    __syncthreads();
-    if (base + round < t1) {
-      for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-        for (int w = 0; w < words; ++w) run[e] += __popc(bits[w * a.E + e]);
-      __syncthreads();
-    }
+    if (base + round < t1) __syncthreads();                    // (bits are written again)
   }
 }
 
-// Exclusive sums over the experts of their counts and of these rounded up to
-// kAlign: off and start [E + 1] in shared memory, by the whole block (sm: 32).
-__device__ __forceinline__ void scan_experts(const int* cnt, int E, int* off, int* start, int2* sm) {
+// Exclusive sums over the experts of their counts (off, where `both`) and of these
+// rounded up to kAlign (start): [E + 1] in shared memory, by the whole block (sm: 32).
+__device__ __forceinline__ void scan_experts(const int* cnt, int E, bool both, int* off, int* start, int2* sm) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int2 before = make_int2(0, 0);
   for (int c0 = 0; c0 < E; c0 += blockDim.x) {
@@ -99,10 +103,14 @@ __device__ __forceinline__ void scan_experts(const int* cnt, int E, int* off, in
     if (w < used) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kAll, x, o), v = __shfl_up_sync(kAll, y, o);
-        if (lane >= o) {
-          x += u;
-          y += v;
+        const int v = __shfl_up_sync(kAll, y, o);
+        if (lane >= o) y += v;
+      }
+      if (both) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(kAll, x, o);
+          if (lane >= o) x += u;
         }
       }
       if (lane == 31) sm[w] = make_int2(x, y);
@@ -110,13 +118,13 @@ __device__ __forceinline__ void scan_experts(const int* cnt, int E, int* off, in
     __syncthreads();
     if (w < used) {
       int2 all = lane < used ? sm[lane] : make_int2(0, 0), mine = lane < w ? all : make_int2(0, 0);
-      all.x = __reduce_add_sync(kAll, all.x);
       all.y = __reduce_add_sync(kAll, all.y);
-      mine.x = __reduce_add_sync(kAll, mine.x);
       mine.y = __reduce_add_sync(kAll, mine.y);
-      if (e < E) {
-        off[e] = before.x + mine.x + x - n;
-        start[e] = before.y + mine.y + y - p;
+      if (e < E) start[e] = before.y + mine.y + y - p;
+      if (both) {
+        all.x = __reduce_add_sync(kAll, all.x);
+        mine.x = __reduce_add_sync(kAll, mine.x);
+        if (e < E) off[e] = before.x + mine.x + x - n;
       }
       before.x += all.x;
       before.y += all.y;
@@ -164,7 +172,7 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
   __shared__ uint2 slots[32][33];
   __shared__ int2 scan[32];
   extern __shared__ uint32_t dyn[];
-  int* chosen = reinterpret_cast<int*>(dyn) + (3 + p.words) * a.E + 2;    // [T][k], with p.nb 1
+  int* chosen = reinterpret_cast<int*>(dyn) + (3 + 2 * p.words) * a.E + 2;    // [T][k], with p.nb 1
   let_next_start();
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
@@ -410,7 +418,7 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
     int* off = reinterpret_cast<int*>(dyn);
     int* start = off + a.E + 1;
     int* run = start + a.E + 1;
-    scan_experts(hist, a.E, off, start, scan);
+    scan_experts(hist, a.E, true, off, start, scan);
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
       if (e < a.E) {
         run[e] = start[e];
@@ -424,7 +432,7 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
     __syncthreads();
     place_tokens(p, chosen, 0, a.T, run, reinterpret_cast<uint32_t*>(run + a.E));
   } else {
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * padded4(a.E) + e] = hist[e];
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(int64_t)blockIdx.x * padded4(a.E) + e] = (uint16_t)hist[e];
   }
 }
 
@@ -448,19 +456,20 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const __grid_const
   const int e4 = threadIdx.x % four * 4;
   if (slice < slices) {
     int4 total = make_int4(0, 0, 0, 0), before = total;
-    const int4* h = reinterpret_cast<const int4*>(a.hist) + threadIdx.x % four;
+    const uint2* h = reinterpret_cast<const uint2*>(a.hist) + threadIdx.x % four;
     for (int i0 = slice; i0 < a.nb; i0 += 10 * slices) {       // ten loads at once, whatever is left
-      int4 c[10];
+      uint2 c[10];
 #pragma unroll
       for (int j = 0; j < 10; ++j) {
         const int i = i0 + j * slices;
-        c[j] = i < a.nb ? h[i * four] : make_int4(0, 0, 0, 0);
+        c[j] = i < a.nb ? h[(int64_t)i * four] : make_uint2(0, 0);
       }
 #pragma unroll
       for (int j = 0; j < 10; ++j) {
-        total.x += c[j].x; total.y += c[j].y; total.z += c[j].z; total.w += c[j].w;
+        const int4 d = make_int4(c[j].x & 0xffff, c[j].x >> 16, c[j].y & 0xffff, c[j].y >> 16);
+        total.x += d.x; total.y += d.y; total.z += d.z; total.w += d.w;
         if (i0 + j * slices < b) {
-          before.x += c[j].x; before.y += c[j].y; before.z += c[j].z; before.w += c[j].w;
+          before.x += d.x; before.y += d.y; before.z += d.z; before.w += d.w;
         }
       }
     }
@@ -474,7 +483,7 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const __grid_const
       }
   }
   __syncthreads();
-  scan_experts(cnt, a.E, off, start, scan);
+  scan_experts(cnt, a.E, b == 0, off, start, scan);
   if (b == 0)
     for (int i = threadIdx.x; i <= a.E; i += blockDim.x) {
       if (i < a.E) a.counts[i] = cnt[i];
@@ -585,18 +594,18 @@ __global__ void __launch_bounds__(256) balance_bias_kernel(const int32_t* counts
 
 // Blocks of the router: one of up to 32 warps per SM for many tokens, of four
 // tokens (a warp each) for few; one block that places its tokens too for at most
-// kFusedTokens.
+// kFusedTokens.  (More than 65535 would not fit the histograms' 16 bits.)
 constexpr int kMostBlocks = 152, kFusedTokens = 32;
 int tokens_per_block(int T) {
   const int per = (int)(((int64_t)T + kMostBlocks - 1) / kMostBlocks);
-  return T <= kFusedTokens ? kFusedTokens : per < 4 ? 4 : per;
+  return T <= kFusedTokens ? kFusedTokens : per < 4 ? 4 : per > 65535 ? 65535 : per;
 }
 
 // Words of 32 tokens that a round of the placement takes by blocks of `threads`:
-// what a block has, up to 28 KB of bits and kPerThread assignments per thread.
+// what a block has, up to 28 KB of bits and rows, and kPerThread assignments per thread.
 int place_words(int per_block, int E, int k, int threads) {
   int n = (per_block + 31) / 32;
-  if (n > 7168 / E) n = 7168 / E;
+  if (n > 3584 / E) n = 3584 / E;
   if (n > threads * kPerThread / (32 * k)) n = threads * kPerThread / (32 * k);
   return n;
 }
@@ -612,7 +621,7 @@ cudaError_t run_score(ScoreArgs a, const PlaceArgs& p, int blocks, cudaStream_t 
   const int warps = blocks == 1 ? a.T : a.per_block, most = kRouteThreads<C>;
   if (blocks == 1) {
     const int threads = warps < 8 ? 256 : 32 * warps > most ? most : 32 * warps;
-    const int smem = ((3 + p.words) * a.E + 2 + a.T * a.k) * 4;
+    const int smem = ((3 + 2 * p.words) * a.E + 2 + a.T * a.k) * 4;
     return launch_overlapped(score_route_kernel<X, C, GROUPED>, 1 + (unsigned)((p.max_rows - p.sure) / 4096),
                              threads, smem, s, a, p);
   }
@@ -641,11 +650,11 @@ cudaError_t run_score(const ScoreArgs& a, const PlaceArgs& p, int blocks, cudaSt
 size_t router_workspace_bytes(const moe_router_dims& d) {
   const int per = tokens_per_block(d.T);
   const size_t nb = ((size_t)d.T + per - 1) / per;
-  return 16 + nb * padded4(d.E) * sizeof(int32_t);
+  return 16 + nb * padded4(d.E) * sizeof(uint16_t);
 }
 
 cudaError_t launch_router(const moe_router_dims& d, const void* logits, const float* bias, const moe_route_out& o,
-                          int32_t* hist, int32_t* status, cudaStream_t s) {
+                          uint16_t* hist, int32_t* status, cudaStream_t s) {
   const int per = tokens_per_block(d.T);
   const int nb = (int)(((int64_t)d.T + per - 1) / per);
   const int64_t max_rows = (int64_t)d.T * d.top_k + (int64_t)kAlign * d.E;
@@ -661,7 +670,7 @@ cudaError_t launch_router(const moe_router_dims& d, const void* logits, const fl
     if (e != cudaSuccess || nb == 1) return e;
   }
   const int fill = (d.E + kPlaceThreads / 32 - 1) / (kPlaceThreads / 32);      // (a warp per expert)
-  return launch_overlapped(place_kernel, (unsigned)(nb + fill), kPlaceThreads, words * d.E * 4, s, p);
+  return launch_overlapped(place_kernel, (unsigned)(nb + fill), kPlaceThreads, 2 * words * d.E * 4, s, p);
 }
 
 cudaError_t launch_router_backward(const moe_router_dims& d, const moe_route_out& o, const void* logits,

@@ -20,7 +20,7 @@ struct ScoreArgs {
   float scale;
   int32_t* idx;
   float* gate;
-  int32_t* hist;            // [blocks][padded4(E)]
+  uint16_t* hist;           // [blocks][padded4(E)]
   int32_t* status;
 };
 

@@ -142,7 +142,7 @@ moe_status moe_router(const moe_router_dims* d, const void* logits, const float*
       ws_bytes < router_workspace_bytes(*d) || !aligned_or_null(bias, 4))
     return MOE_ERR_INVALID_ARG;
   if (d->T > 0 && !aligned(logits, type_bytes(d->type))) return MOE_ERR_INVALID_ARG;
-  return cuda_status(launch_router(*d, logits, bias, *o, static_cast<int32_t*>(ws), dev_status,
+  return cuda_status(launch_router(*d, logits, bias, *o, static_cast<uint16_t*>(ws), dev_status,
                                    static_cast<cudaStream_t>(stream)));
 }
 
