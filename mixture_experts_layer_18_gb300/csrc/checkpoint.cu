@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const __grid_consta
   let_next_start();
   wait_for_previous();
   const int lane = threadIdx.x & 31;
-  const int rows = a.padded_offsets[a.E];
+  const int rows = (int)min((int64_t)a.padded_offsets[a.E], a.n_assign + (int64_t)kAlign * a.E);
   const int nx = (a.H + kUnit - 1) / kUnit, nh = (2 * a.I + kUnit - 1) / kUnit;
   const int64_t ux = a.X ? (int64_t)a.T * nx : 0, all = ux + a.n_assign * nh;
   for (int64_t u = global_warp(); u < all; u += grid_warps()) {
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(const __grid_con
   let_next_start();
   wait_for_previous();
   const int lane = threadIdx.x & 31;
-  const int rows = a.padded_offsets[a.E];
+  const int rows = (int)min((int64_t)a.padded_offsets[a.E], a.n_assign + (int64_t)kAlign * a.E);
   X* x_perm = static_cast<X*>(a.x_perm);
   X* h13 = static_cast<X*>(a.h13);
   X* act = static_cast<X*>(a.act);

@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(kBlock<L, kThreads>, CPT <= 16 ? 768 / kBlock<
   }
   Weights<X, CPT, L, SHIFT, TH> gam;
   gam.load(lane, a.gamma, a.wtype, 1.f, reinterpret_cast<float4*>(dyn + (RES ? 2 : 1) * Str::RING));
-  const float inv = 1.f / (float)a.H;
   int st = 0, par = 0;
   for (uint32_t base = blockIdx.x * ROWS; base < T; base += stride, row += stride) {
     F2 x[CPT / 2];
@@ -119,7 +118,7 @@ __global__ void __launch_bounds__(kBlock<L, kThreads>, CPT <= 16 ? 768 / kBlock<
     float s[1] = {sum2(add2(acc, acc2))};
     row_sums<1, L>(s, group, sm[par]);
     par ^= 1;
-    const float r = inv_sqrt(s[0] * inv + a.eps);
+    const float r = inv_sqrt_exact(s[0] / (float)a.H + a.eps);
     const bool live = row < T;
     if (RES && a.h && live) store_row(lane, static_cast<X*>(a.h) + (int64_t)row * a.ld_h, x);
     F2 g[CPT / 2];
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(1024) rms_rows_kernel(const RmsArgs a) {
     for (int i = 0; i < V; ++i) s[0] += v[i] * v[i];
   }
   row_sums<1, 1024>(s, 0, sm);
-  const float r = inv_sqrt(s[0] / (float)a.H + a.eps);
+  const float r = inv_sqrt_exact(s[0] / (float)a.H + a.eps);
   if (threadIdx.x == 0 && a.rstd) a.rstd[row] = r;
   auto part = [&](int c, float (&v)[V]) {        // stores h and y of V columns; v: y
     sum_of(c, v);

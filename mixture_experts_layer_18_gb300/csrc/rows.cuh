@@ -123,6 +123,13 @@ __device__ __forceinline__ float inv_sqrt(float v) {
   return v > 0.f && v <= 3.402823466e38f ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
 }
 
+// The same within half an ulp: the step's residual 1 - v r r is exact to 2^-40.
+__device__ __forceinline__ float inv_sqrt_exact(float v) {
+  const float r = rsqrtf(v), t = v * r;
+  const float e = fmaf(-fmaf(v, r, -t), r, fmaf(-t, r, 1.f));
+  return v > 0.f && v <= 3.402823466e38f ? fmaf(0.5f * r, e, r) : r;
+}
+
 // ------------------------------------------------------------------ rows
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

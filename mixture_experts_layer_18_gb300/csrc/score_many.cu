@@ -193,10 +193,10 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
       uint32_t w[4] = {0, 0, 0, 0};
       if (e < a.E) {
         if constexpr (V * sizeof(X) == 16) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + e));
+          const uint4 x = *reinterpret_cast<const uint4*>(row + e);
           w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
         } else {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + e));
+          const uint2 x = *reinterpret_cast<const uint2*>(row + e);
           w[0] = x.x; w[1] = x.y;
         }
       }

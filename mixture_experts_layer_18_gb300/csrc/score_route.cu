@@ -539,7 +539,10 @@ __global__ void __launch_bounds__(256) score_route_backward_kernel(const __grid_
     float d;
     if (a.sigmoid || a.renorm) {
       d = a.renorm ? w * (dw - inner / a.scale) : w * dw;
-      if (a.sigmoid && e >= 0) d *= 1.f / (1.f + expf(to_f(row[e])));      // 1 - s
+      if (a.sigmoid && e >= 0) {
+        const float v = to_f(row[e]);
+        d *= v < INFINITY ? 1.f / (1.f + expf(v)) : 1.f;                     // 1 - s
+      }
       if (a.vec) {
         for (int c = lane; c < a.E * (int)sizeof(X) / 16; c += 32) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
       } else {

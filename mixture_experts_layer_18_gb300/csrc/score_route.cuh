@@ -178,13 +178,13 @@ struct Logits {
         if (e0 + i * (kVec / (int)sizeof(X)) >= E) continue;
         const X* p = row + e0 + i * (kVec / (int)sizeof(X));
         if constexpr (kVec == 16) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+          const uint4 v = *reinterpret_cast<const uint4*>(p);
           w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         } else if constexpr (kVec == 8) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
           w[0] = v.x; w[N - 1] = v.y;
         } else {
-          w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          w[0] = *reinterpret_cast<const uint32_t*>(p);
         }
       }
     } else {

@@ -229,6 +229,47 @@ def test_bad_logits_are_reported():
                 assert r.topk_idx[7].tolist() == [0, 1, 2, 3] and not r.gate[7].any() and not dl[7].any()
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("many", [False, True])
+def test_bad_logits_that_are_chosen(renorm, many):
+    """NaN and +inf among fewer finite logits than top_k: chosen as masked ones, gate and
+    gradient 0, and the gradient of the others is that of -inf in their place."""
+    from mixture_experts_layer_18_gb300 import MOE_ERR_BAD_INPUT
+    rng = np.random.default_rng(17)
+    l = np.full((20, 16), -np.inf, np.float32)
+    l[:, :2] = rng.standard_normal((20, 2))
+    l[::2, 2], l[::3, 3] = np.nan, np.inf
+    l = _many(l, many)
+    for score in ("softmax", "sigmoid"):
+        x, r, dg, dl = _run(l, None, 4, score=score, renormalise=renorm)
+        _check(x, None, 4, r, dg, dl, score=score, renormalise=renorm)
+        assert r.device_status() == MOE_ERR_BAD_INPUT
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T", [3, 900, 5000])
+@pytest.mark.parametrize("off,pad", [(1, 0), (2, 2), (3, 5), (4, 8), (8, 0)])
+def test_rows_at_any_address(dtype, T, off, pad):
+    """Logits whose rows start anywhere, gradients of an odd place too."""
+    import torch
+    from mixture_experts_layer_18_gb300.training import Router
+    rng = np.random.default_rng(off)
+    dt, E, k = getattr(torch, dtype), 128, 8
+    buf = torch.full((T, off + E + pad), 99.0, dtype=dt, device="cuda")
+    x = buf[:, off:off + E]
+    x.copy_(_device(rng.standard_normal((T, E)).astype(np.float32)))
+    b = (1e-3 * rng.integers(-50, 50, E)).astype(np.float32)
+    dg = rng.standard_normal((T, k)).astype(np.float32)
+    flat = torch.full((T * E + 16,), 7.0, dtype=dt, device="cuda")
+    dl = flat[off:off + T * E].view(T, E)
+    r = Router(T, E, k, score="sigmoid", dtype=dt)
+    r.forward(x, _device(b))
+    r.backward(x, _device(dg), dl)
+    torch.cuda.synchronize()
+    _check(x.float().cpu().numpy(), b, k, r, dg, dl, score="sigmoid")
+    assert (flat[:off] == 7.0).all() and (flat[off + T * E:] == 7.0).all()
+
+
 def test_no_tokens():
     import torch
     from mixture_experts_layer_18_gb300.training import Router
