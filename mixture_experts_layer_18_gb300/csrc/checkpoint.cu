@@ -84,7 +84,12 @@ struct CkptArgs {
   int32_t* status;
 };
 
-constexpr int kPieces = 4;                 // steps of 256 columns in a unit
+// Steps of 256 columns in a warp's unit of work: of a row to save or to decode; of
+// a token's row to restore (stored k times); of each half of h13 to restore.
+// (16384 tokens, H 2048, I 768, 8 of 128: save 117 us with 4, 136 with 2 and 141 with 8;
+// restore 233 with 2 and 3, 241 with 4 and 3, 276 with 4 and 2, which leaves half of a
+// unit idle.)
+constexpr int kPieces = 4, kTokenPieces = 2, kHalfPieces = 3;
 constexpr int kUnit = 256 * kPieces;
 
 // A row's codes of the columns [c0, c0 + kUnit).
@@ -154,8 +159,8 @@ __global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(const __grid_con
   X* x_perm = static_cast<X*>(a.x_perm);
   X* h13 = static_cast<X*>(a.h13);
   X* act = static_cast<X*>(a.act);
-  constexpr int kStep = 2;                 // steps of 256 columns of each half of h13 in a unit
-  const int nx = (a.H + kUnit - 1) / kUnit, nh = (a.I + 256 * kStep - 1) / (256 * kStep);
+  const int nx = (a.H + 256 * kTokenPieces - 1) / (256 * kTokenPieces);
+  const int nh = (a.I + 256 * kHalfPieces - 1) / (256 * kHalfPieces);
   const int64_t up = (int64_t)a.E * kAlign, ux = up + (int64_t)a.T * nx, all = ux + a.n_assign * nh;
   for (int64_t u = global_warp(); u < all; u += grid_warps()) {
     if (u < up) {                          // the i-th row behind an expert's, as the forward leaves it
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(const __grid_con
     }
     if (u < ux) {
       const int64_t t = (u - up) / nx;
-      const int c0 = (int)(u - up - t * nx) * kUnit;
+      const int c0 = (int)(u - up - t * nx) * (256 * kTokenPieces);
       int my = -1;                         // lane j < k: the row of slot j
       if (lane < a.k) {
         my = a.row_of_assign[t * a.k + lane];
@@ -178,25 +183,25 @@ __global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(const __grid_con
           my = -1;
         }
       }
-      uint2 q[kPieces];
-      int s[kPieces];
+      uint2 q[kTokenPieces];
+      int s[kTokenPieces];
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      for (int i = 0; i < kTokenPieces; ++i) {
         const int c = c0 + i * 256 + lane * 8;
         if (c < a.H) {
           q[i] = *reinterpret_cast<const uint2*>(a.x_q + t * a.H + c);
           s[i] = a.x_s[t * (a.H >> 5) + (c >> 5)];
         }
       }
-      float v[kPieces][8];
+      float v[kTokenPieces][8];
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) decode8(q[i], s[i], v[i]);
+      for (int i = 0; i < kTokenPieces; ++i) decode8(q[i], s[i], v[i]);
       for (int j = 0; j < a.k; ++j) {
         const int r = __shfl_sync(kAll, my, j);
         if (r < 0) continue;
         X* d = x_perm + (int64_t)r * a.H;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
+        for (int i = 0; i < kTokenPieces; ++i) {
           const int c = c0 + i * 256 + lane * 8;
           if (c < a.H) store8(d + c, v[i]);
         }
@@ -209,14 +214,14 @@ __global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(const __grid_con
       if (lane == 0) report(a.status, MOE_ERR_BAD_INDEX);
       continue;
     }
-    const int c0 = (int)(u - ux - n * nh) * (256 * kStep);
+    const int c0 = (int)(u - ux - n * nh) * (256 * kHalfPieces);
     const float g = a.gate ? a.gate[n] : 1.f;
     const uint8_t* hq = a.h_q + n * 2 * a.I;
     const uint8_t* hs = a.h_s + n * (2 * a.I >> 5);
-    uint2 q[kStep][2];
-    int s[kStep][2];
+    uint2 q[kHalfPieces][2];
+    int s[kHalfPieces][2];
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) {
+    for (int i = 0; i < kHalfPieces; ++i) {
       const int c = c0 + i * 256 + lane * 8;
 #pragma unroll
       for (int p = 0; p < 2; ++p)
@@ -226,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_restore_kernel(const __grid_con
         }
     }
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) {
+    for (int i = 0; i < kHalfPieces; ++i) {
       const int c = c0 + i * 256 + lane * 8;
       if (c >= a.I) continue;
       float x[8], v[8];
@@ -281,9 +286,11 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const uint8_t* q, cons
   }
 }
 
-// Blocks for `units` warps' worth of work: at most eight per SM.
-unsigned blocks_for(int64_t units) {
-  const int64_t need = (units + kThreads / 32 - 1) / (kThreads / 32), most = (int64_t)sm_count() * 8;
+// Blocks for `units` warps' worth of work: at most `per_sm` per SM.  (Saving reads
+// most: eight, all there is room for; writing more it goes faster with blocks that come
+// and go: restoring as above 492 us with eight and H 4096, I 1536, 458 with 64.)
+unsigned blocks_for(int64_t units, int per_sm) {
+  const int64_t need = (units + kThreads / 32 - 1) / (kThreads / 32), most = (int64_t)sm_count() * per_sm;
   return (unsigned)(need < 1 ? 1 : need < most ? need : most);
 }
 
@@ -299,24 +306,26 @@ cudaError_t launch_checkpoint_save(const CheckpointDesc& d, cudaStream_t s) {
   const CkptArgs a = ckpt_args(d);
   const int64_t units = (d.X ? (int64_t)d.T * ((d.H + kUnit - 1) / kUnit) : 0) +
                         a.n_assign * ((2 * d.I + kUnit - 1) / kUnit);
-  return d.elem_bytes == 2 ? launch_overlapped(ckpt_save_kernel<__nv_bfloat16>, blocks_for(units), kThreads, 0, s, a)
-                           : launch_overlapped(ckpt_save_kernel<float>, blocks_for(units), kThreads, 0, s, a);
+  const unsigned grid = blocks_for(units, 8);
+  return d.elem_bytes == 2 ? launch_overlapped(ckpt_save_kernel<__nv_bfloat16>, grid, kThreads, 0, s, a)
+                           : launch_overlapped(ckpt_save_kernel<float>, grid, kThreads, 0, s, a);
 }
 
 cudaError_t launch_checkpoint_restore(const CheckpointDesc& d, cudaStream_t s) {
   if (d.T == 0) return cudaSuccess;
   const CkptArgs a = ckpt_args(d);
-  const int64_t units = (int64_t)d.E * kAlign + (int64_t)d.T * ((d.H + kUnit - 1) / kUnit) +
-                        a.n_assign * ((d.I + 511) / 512);
-  return d.elem_bytes == 2
-             ? launch_overlapped(ckpt_restore_kernel<__nv_bfloat16>, blocks_for(units), kThreads, 0, s, a)
-             : launch_overlapped(ckpt_restore_kernel<float>, blocks_for(units), kThreads, 0, s, a);
+  const int64_t units = (int64_t)d.E * kAlign +
+                        (int64_t)d.T * ((d.H + 256 * kTokenPieces - 1) / (256 * kTokenPieces)) +
+                        a.n_assign * ((d.I + 256 * kHalfPieces - 1) / (256 * kHalfPieces));
+  const unsigned grid = blocks_for(units, 64);
+  return d.elem_bytes == 2 ? launch_overlapped(ckpt_restore_kernel<__nv_bfloat16>, grid, kThreads, 0, s, a)
+                           : launch_overlapped(ckpt_restore_kernel<float>, grid, kThreads, 0, s, a);
 }
 
 cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* sf, int R, int C, int64_t ld, int type, void* dst,
                               cudaStream_t s) {
   if (R == 0) return cudaSuccess;
-  const unsigned grid = blocks_for((int64_t)R * ((C + kUnit - 1) / kUnit));
+  const unsigned grid = blocks_for((int64_t)R * ((C + kUnit - 1) / kUnit), 64);
   const int es = type == MOE_TYPE_BF16 ? 2 : 4;
   const bool vec = ((uintptr_t)dst & 15) == 0 && (R == 1 || ld * es % 16 == 0);
   if (es == 2)
