@@ -260,3 +260,31 @@ def test_bad_rows_are_reported():
         L.clear_status()
         call()
         assert L.device_status() == 0
+
+
+def test_activations_past_32_bits():
+    """More than 2^31 elements of h13: the last tokens' rows are their own."""
+    import torch
+    from mixture_experts_layer_18_gb300.layer import MoELayer
+    T, H, E, I, k = 300_000, 64, 4, 2048, 2
+    L = MoELayer(T, H, E, I, k, backward=False)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    L.route(torch.randn((T, E), generator=g, device="cuda"))
+    n = int(L.padded_offsets[-1])
+    rows = L.row_of_assign[-40:].long()
+    L.h13.zero_()
+    part = torch.randn((40, 2 * I), generator=g, device="cuda").bfloat16()
+    L.h13[rows] = part
+    X = torch.randn((T, H), generator=g, device="cuda").bfloat16()
+    ck = L.checkpoint()
+    L.save(ck, X)
+    L.h13.fill_(3.0)
+    L.act.fill_(3.0)
+    L.restore(ck)
+    torch.cuda.synchronize()
+    assert L.device_status() == 0
+    want = M.dequantize_mxfp8(*M.quantize_mxfp8(_f64(part), 1), 1)
+    assert np.array_equal(_f64(L.h13[rows]), want)
+    assert not L.h13[:n].index_fill(0, rows, 0).any() and not L.act[:n].index_fill(0, rows, 0).any()
+    x = M.dequantize_mxfp8(*M.quantize_mxfp8(_f64(X[-20:]), 1), 1)
+    assert np.array_equal(_f64(L.x_perm[rows]), x.repeat(k, 0))

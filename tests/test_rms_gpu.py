@@ -286,3 +286,29 @@ def test_captured_and_same_every_time():
     n.forward(x, w, io["y"], residual=r, h=io["h"], encoded=m, stream=s)
     s.synchronize()
     assert torch.equal(io["h"], 2 * first[1])
+
+
+def test_elements_past_32_bits():
+    """More than 2^32 elements of rows and codes: the last rows are their own."""
+    import torch
+    from mixture_experts_layer_18_gb300.training import MXRows, RMSNorm
+    T, H = 2_100_000, 2048
+    g = torch.Generator(device="cuda").manual_seed(3)
+    tail = torch.randn((64, H), generator=g, device="cuda").bfloat16()
+    x = torch.ones((T, H), dtype=torch.bfloat16, device="cuda")
+    x[-64:] = tail
+    n, small, m, ms = RMSNorm(T, H), RMSNorm(64, H), MXRows(T, H), MXRows(64, H)
+    y, ys = torch.empty_like(x), torch.empty_like(tail)
+    n.forward(x, None, y, encoded=m)
+    small.forward(tail, None, ys, encoded=ms)
+    assert torch.equal(y[-64:], ys) and torch.equal(m.codes[-64:], ms.codes) and torch.equal(m.scales[-64:], ms.scales)
+    assert (y[:-64:1000] == 1.0).all()
+    back, bs = torch.empty_like(x), torch.empty_like(tail)
+    m.decode(back)
+    ms.decode(bs)
+    assert torch.equal(back[-64:], bs)
+    del back, m
+    dx, dxs = torch.empty_like(x), torch.empty_like(tail)
+    n.backward(y, x, None, dx)
+    small.backward(ys, tail, None, dxs)
+    assert torch.equal(dx[-64:], dxs)

@@ -283,21 +283,58 @@ def test_no_tokens():
     assert not r.counts.any() and not r.offsets.any() and not r.padded_offsets.any() and (r.assign_of_row == -1).all()
 
 
-def test_many_tokens_are_placed_in_order():
-    """More assignments per block than one round of the permutation takes."""
-    rng = np.random.default_rng(8)
-    l = rng.standard_normal((70001, 16)).astype(np.float32)
-    l[:, 3] += 3
-    x = _device(l)
+@pytest.mark.parametrize("T,E,k", [(70001, 16, 4), (200_003, 300, 9), (10_300_000, 8, 2)])
+def test_many_tokens_are_placed_in_order(T, E, k):
+    """More assignments per block than one round of the permutation takes; more tokens
+    per block than 16 bits count."""
     import torch
     from mixture_experts_layer_18_gb300.training import Router
-    r = Router(70001, 16, 4)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn((T, E), generator=g, device="cuda")
+    x[:, 3] += 3
+    r = Router(T, E, k)
     r.forward(x)
-    idx = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :4].cpu().numpy()
-    assert np.array_equal(r.topk_idx.cpu().numpy(), idx)
-    m = M.permute(idx, 16)
-    assert np.array_equal(r.row_of_assign.cpu().numpy(), m["row_of_assign"])
-    assert np.array_equal(r.counts.cpu().numpy(), m["counts"])
+    idx = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(r.topk_idx.long(), idx)
+    flat = idx.reshape(-1)
+    order = torch.sort(flat, stable=True).indices
+    counts = torch.bincount(flat, minlength=E)
+    start = torch.nn.functional.pad(((counts + 127) // 128 * 128).cumsum(0), (1, 0))
+    first = torch.nn.functional.pad(counts.cumsum(0), (1, 0))
+    e = flat[order]
+    row = start[e] + torch.arange(T * k, device="cuda") - first[e]
+    want = torch.empty_like(row)
+    want[order] = row
+    assert torch.equal(r.row_of_assign.long(), want) and torch.equal(r.counts.long(), counts)
+    back = torch.full((T * k + 128 * E,), -1, device="cuda")
+    back[want] = torch.arange(T * k, device="cuda")
+    assert torch.equal(r.assign_of_row.long(), back)
+    assert torch.equal(r.padded_offsets.long(), start) and torch.equal(r.offsets.long(), first)
+
+
+def test_logits_past_32_bits():
+    """More than 2^32 bytes and 2^31 elements of logits and gradients: the last rows are their own."""
+    import torch
+    from mixture_experts_layer_18_gb300.training import Router
+    T, E, k = 2_200_001, 1000, 4
+    x = torch.zeros((T, E), device="cuda")
+    x[:, 5] = 1.0
+    rng = np.random.default_rng(9)
+    tail = rng.standard_normal((40, E)).astype(np.float32)
+    x[-40:] = _device(tail)
+    r = Router(T, E, k, renormalise=False)
+    r.forward(x)
+    dg = torch.ones((T, k), device="cuda")
+    dl = torch.empty_like(x)
+    r.backward(x, dg, dl)
+    torch.cuda.synchronize()
+    idx, gate = O.route_by_scores(tail, None, k, renormalise=False)
+    assert np.array_equal(r.topk_idx[-40:].cpu().numpy(), idx)
+    assert (r.topk_idx[:-40] == torch.tensor([5, 0, 1, 2], device="cuda")).all()
+    assert np.abs(r.gate[-40:].double().cpu().numpy() - gate).max() <= 200 * U
+    want = O.route_by_scores_backward(tail, idx, gate, np.ones((40, k)), "softmax", False, 1.0)
+    assert np.abs(dl[-40:].double().cpu().numpy() - want).max() <= 400 * U
+    assert int(r.counts.sum()) == T * k
 
 
 def test_the_softmax_router_is_the_layers():
