@@ -51,7 +51,7 @@ __device__ __noinline__ int order8(const ScoreArgs& a, const X* row, int e0, int
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       if (sl + 8 * r >= n || oe == e[r]) continue;
-      const float gap = near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(v[r]), fabsf(ov)));
+      const float gap = near_pair<CL>(a.sigmoid, inv, v[r], b[r], ov, ob);
       if ((ol == l[r] && ob == b[r]) || (!on[r] && !other)) better[r] += oe < e[r];
       else if (!on[r] || !other) better[r] += other;               // masked ones last
       else if (by_logit || fabsf(ov - v[r]) > gap) better[r] += ov > v[r] || (ov == v[r] && oe < e[r]);
@@ -84,7 +84,7 @@ __device__ __noinline__ int order8(const ScoreArgs& a, const X* row, int e0, int
       for (int r = 0; r < 2; ++r) {
         if (sl + 8 * r >= n || oe == e[r]) continue;
         const Exact& x = r ? x1 : x0;
-        const float gap = near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(v[r]), fabsf(ov)));
+        const float gap = near_pair<CL>(a.sigmoid, inv, v[r], b[r], ov, ob);
         const float d = (oh - x.u.h) + (olow - x.u.l);
         if ((ol == l[r] && ob == b[r]) || (!on[r] && !other)) better[r] += oe < e[r];
         else if (!on[r] || !other) better[r] += other;
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
       // is the order of neighbours certain?
       const float v = leading(sel), pv = __shfl_up_sync(kAll, v, 1, 8), pl = __shfl_up_sync(kAll, l, 1, 8);
       const float b = sl < n ? bias[e / CL * (CL + 4) + e % CL] : 0.f, pb = __shfl_up_sync(kAll, b, 1, 8);
-      const float gap = by_logit ? 0.f : near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(pv), fabsf(v))) + kLead * fabsf(v);
+      const float gap = by_logit ? 0.f : near_pair<CL>(a.sigmoid, inv, pv, pb, v, b) + 2.f * kLead * fabsf(v);
       const int pe = __shfl_up_sync(kAll, e, 1, 8);
       const bool close = sl > 0 && v > -INFINITY && !(pv - v > gap) && !(pl == l && pb == b && pe < e);
       bool open = again || n == 16;              // (16: there may be more)

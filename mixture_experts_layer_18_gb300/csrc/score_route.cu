@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
       float b = 0.f;
       if (a.bias && sel) b = bias_of(a, sel_e);
       const float pb = __shfl_up_sync(kAll, b, 1);
-      const float gap = by_logit ? 0.f : near_of<C>(a.sigmoid, inv, fmaxf(fabsf(pv), fabsf(v))) + kLead * fabsf(v);
+      const float gap = by_logit ? 0.f : near_pair<C>(a.sigmoid, inv, pv, pb, v, b) + 2.f * kLead * fabsf(v);
       const bool close = lane > 0 && v > -INFINITY && !(pv - v > gap) && !(pl == l && pb == b);
       if (again || n == 32) {
         sel_e = choose32<X, C, GROUPED>(a, row, slot);

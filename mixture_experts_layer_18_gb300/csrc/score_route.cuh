@@ -217,6 +217,18 @@ __device__ __forceinline__ float near_of(bool sigmoid, float s, float u) {
   return (sigmoid ? 10 * 0x1p-24f : (64 + 2 * C) * 0x1p-24f * s) + 0x1p-23f * fabsf(u);
 }
 
+// The same for two values (u, b) and (v, c) whose biases are known.  The softmax' sum
+// is off by 28 + C for both alike, which moves their scores' difference, at most that of
+// the biases and their own, by as much relative to it; 7 relative to each score and 1.8
+// to the largest are their own.
+template <int C>
+__device__ __forceinline__ float near_pair(bool sigmoid, float s, float u, float b, float v, float c) {
+  const float w = fmaxf(fabsf(u), fabsf(v));
+  if (sigmoid) return near_of<C>(true, 1.f, w);
+  return 0x1p-24f * ((30 + C) * (fabsf(b - c) + fabsf(u - v)) + 7.5f * (fabsf(u - b) + fabsf(v - c)) + 2.f * s) +
+         0x1p-23f * w;
+}
+
 // The best two keys of a lane with their places (of equal ones the first).
 template <int C>
 struct BestTwo {
@@ -379,7 +391,7 @@ __device__ __noinline__ int order(const ScoreArgs& a, const X* row, int e, float
     const float ov = __shfl_sync(kAll, v, i), ol = __shfl_sync(kAll, l, i), ob = __shfl_sync(kAll, b, i);
     const int oe = __shfl_sync(kAll, e, i);
     const bool other = ol > -INFINITY;
-    const float gap = by_logit ? 0.f : near_of<C>(a.sigmoid, inv, fmaxf(fabsf(v), fabsf(ov)));
+    const float gap = by_logit ? 0.f : near_pair<C>(a.sigmoid, inv, v, b, ov, ob);
     if (oe == e) continue;
     if ((ol == l && ob == b) || (!on && !other)) better += oe < e;
     else if (!on || !other) better += other;               // masked ones last
