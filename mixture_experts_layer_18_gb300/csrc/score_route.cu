@@ -6,20 +6,30 @@
 //   best groups stay; the k largest u in them are chosen (ties: the lower
 //   index), and gate_j = scale s_j, or scale s_j / sum of the chosen s.
 //
-// The choice is that of u in 64 bits, whatever the GPU, found in three steps:
+// The choice is that of u in 64 bits, whatever the GPU, found in steps:
 //   - keys of 32 bits that hold the leading bits of u in fp32 and the expert's
-//     index, all different, so that a round of the choice is one warp maximum
-//     (about 250 instructions a token where comparing values and indices took 750);
-//   - where two values that the choice turns on are not told apart by these bits and
-//     the error of fp32 (near_of): the token's values in full fp32, and those that
-//     are still too close as pairs of fp32 numbers (choose32);
-//   - where more than a warp's worth of values are too close, or pairs of fp32 numbers
-//     do not tell: all of the token in 64 bits (choose64).  fp64 for every value would
-//     take 30 times the time that the logits take from HBM.
+//     index, so that a round of the choice is one maximum over the lanes (comparing
+//     values and indices took 750 instructions a token of 128 experts; 290 now);
+//   - where these bits and the error of fp32 (near_of, near_pair) leave it open, the
+//     candidates in full fp32, and those that are still too close in pairs of fp32
+//     numbers (order; a few tokens in a thousand with 256 sigmoid scores, one in a
+//     thousand in pairs);
+//   - more candidates than fit: the row's values again with all bits (choose32);
+//   - what pairs do not tell (equal sums of different parts): the row in 64 bits
+//     (choose64).  This GPU's fp64 takes 43 us for a row of 256.
 // Without a bias u orders as the logits do, which are compared themselves.
 //
 // One warp per token, C neighbouring experts per lane, so that a group is a
-// segment of lanes and the logits arrive in vectors.
+// segment of lanes and the logits arrive in vectors; for many tokens eight lanes
+// per token (score_many.cu).  Then a second launch gives the assignments their rows
+// (for at most kFusedTokens the same one does).
+//
+// Measured (GB300, fp32 logits, top 8, with the permutation): 1 token of 256 experts
+// in 8 groups 5.5 us; 1500 tokens 15 us; 16384 tokens 24 us; 65536 tokens of 128 experts,
+// softmax with a bias, 40 us (logits from HBM: 5 us).  The choice is bound by
+// instructions (62% of the issue slots with 65536 tokens, 41% with 16384, where a
+// block has 27 warps' worth of tokens for 16 warps), the permutation (6 us) by its
+// chain of dependent steps, 4000 cycles of it the other blocks' histograms.
 #include "score_route.cuh"
 
 namespace moe {
@@ -509,7 +519,7 @@ struct ScoreBwdArgs {
   void* dlogits;
   int64_t ld;
   int T, E, k, sigmoid, renorm, vec;
-  float scale;
+  float inv_scale;
   int32_t* status;
 };
 
@@ -538,7 +548,8 @@ __global__ void __launch_bounds__(256) score_route_backward_kernel(const __grid_
     const float inner = warp_sum(w * dw);
     float d;
     if (a.sigmoid || a.renorm) {
-      d = a.renorm ? w * (dw - inner / a.scale) : w * dw;
+      // (rounded product by product: of one expert alone this is what rounding leaves of 0)
+      d = a.renorm ? w * __fsub_rn(dw, __fmul_rn(inner, a.inv_scale)) : w * dw;
       if (a.sigmoid && e >= 0) {
         const float v = to_f(row[e]);
         d *= v < INFINITY ? 1.f / (1.f + expf(v)) : 1.f;                     // 1 - s
@@ -681,7 +692,7 @@ cudaError_t launch_router_backward(const moe_router_dims& d, const moe_route_out
   if (d.T == 0) return cudaSuccess;
   const int vec = ((uintptr_t)dlogits & 15) == 0 && d.E * (d.type == MOE_TYPE_BF16 ? 2 : 4) % 16 == 0;
   const ScoreBwdArgs a{logits, o.topk_idx, o.gate, dgate, dlogits, d.ld, d.T, d.E, d.top_k,
-                       d.score == MOE_SCORE_SIGMOID, d.renormalise != 0, vec, d.scale, status};
+                       d.score == MOE_SCORE_SIGMOID, d.renormalise != 0, vec, 1.f / d.scale, status};
   const int blocks = (d.T - 1) / 8 + 1, most = kMostBlocks * 8;
   const int grid = blocks < most ? blocks : most;
   return d.type == MOE_TYPE_BF16

@@ -1,6 +1,6 @@
-// score_route.cuh - what the router by scores does for one token, whole warp by whole warp: scores,
-// the order of close values, the choice from all bits; shared by its two kernels
-// (score_route.cu: a warp per token; score_many.cu: eight lanes per token).
+// score_route.cuh - what the two kernels of the router by scores share
+// (score_route.cu: a warp per token; score_many.cu: eight lanes per token): scores and
+// their errors, the order of close values, the choice from all bits by a whole warp.
 #pragma once
 
 #include "rows.cuh"

@@ -40,7 +40,7 @@ bool router_ok(const moe_router_dims* d) {
   if (d->groups < 1 || d->groups > 32 || d->E % d->groups || d->top_groups < 1 || d->top_groups > d->groups) return false;
   const int size = d->E / d->groups;
   if (d->group_top < 1 || d->group_top > 2 || d->group_top > size || d->top_k > d->top_groups * size) return false;
-  if (!(std::isfinite(d->scale) && d->scale > 0.f)) return false;
+  if (!(d->scale >= 0x1p-64f && d->scale <= 0x1p64f)) return false;
   return (int64_t)d->T * d->top_k + (int64_t)kAlign * d->E < ((int64_t)1 << 31);
 }
 

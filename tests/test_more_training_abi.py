@@ -29,7 +29,7 @@ def _route(**kw):
     dict(T=-1), dict(E=0), dict(E=1025, ld=1025), dict(top_k=0), dict(top_k=33, E=64, ld=64, groups=1, top_groups=1),
     dict(ld=31), dict(type=2), dict(score=2), dict(score=-1), dict(groups=0), dict(groups=5), dict(groups=64, E=64, ld=64),
     dict(top_groups=0), dict(top_groups=5), dict(group_top=0), dict(group_top=3), dict(groups=32, group_top=2),
-    dict(top_k=17), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan),
+    dict(top_k=17), dict(scale=0.0), dict(scale=2.0 ** -65), dict(scale=2.0 ** 65), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan),
     dict(T=1 << 29, top_k=4)])
 def test_router_dims_refused(bad):
     d = _router(**bad)
