@@ -9,9 +9,9 @@ namespace {
 
 // Many tokens: eight lanes per token, four tokens per warp, so that what a token
 // takes besides its elements (rounds, gates, addresses) is paid once for four.
-// E <= 8 CL, top_k <= 8, a group is a power of two of lanes or all there is; rows by
-// vectors.  Of fp32 logits a key's index is that within the lane, which leaves more bits
-// to the value.
+// A group has a power of two of the eight lanes (all of them without groups), and a
+// lane up to CL neighbouring experts of its group; top_k <= 8.  Of fp32 logits a key's
+// index is that within the lane, which leaves more bits to the value.
 __device__ __forceinline__ uint32_t max8(uint32_t v) {          // over a token's lanes
 #pragma unroll
   for (int o = 4; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
   constexpr float kLead = (kIndex + 1) * 0x1p-23f;      // what it takes from the value, relative to it
   constexpr int V = CL * (int)sizeof(X) < 16 ? CL : 16 / (int)sizeof(X);
   __shared__ int hist[8 * CL];
-  __shared__ __align__(16) float bias[8 * (CL + 4)];    // (rows of lanes apart by 4 banks)
+  __shared__ float biases[8 * CL];                      // by expert,
+  __shared__ __align__(16) float bias[8 * (CL + 4)];    // and by lane (rows apart by 4 banks)
   __shared__ uint2 slots[kManyThreads<CL> / 32][33];
   __shared__ int units;
   let_next_start();
@@ -154,13 +155,20 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
   wait_for_previous();
   bool bad = false, unused = false;
   const bool by_logit = !a.bias && (!GROUPED || a.group_top == 1);
-  for (int e = threadIdx.x; e < 8 * CL; e += kManyThreads<CL>) {
+  // the first expert of a lane, and how many it has (the last of a group's lanes may have fewer or none)
+  auto first_of = [&](int l) { return (l >> a.seg_log) * a.group_size + (l & (a.seg - 1)) * CL; };
+  auto count_of = [&](int l) {
+    return l >> a.seg_log < a.groups ? max(0, min(CL, a.group_size - (l & (a.seg - 1)) * CL)) : 0;
+  };
+  for (int i = threadIdx.x; i < 8 * CL; i += kManyThreads<CL>) {
+    const int l = i / CL, q = i % CL, e = first_of(l) + q;
     float b = 0.f;
-    if (a.bias && e < a.E) {
+    if (a.bias && q < count_of(l)) {
       b = bias_of(a, e);
       if (!(fabsf(a.bias[e]) < INFINITY)) bad = true;
     }
-    bias[e / CL * (CL + 4) + e % CL] = b;
+    bias[l * (CL + 4) + q] = b;
+    if (q < count_of(l)) biases[e] = b;
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, sl = lane & 7, first = lane & 24;
@@ -168,6 +176,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
   uint2* slot = slots[threadIdx.x >> 5];
   int* slot_e = reinterpret_cast<int*>(slot);           // [4 tokens][16]
   const float* my_bias = bias + sl * (CL + 4);
+  const int e0 = first_of(sl), count = count_of(sl);
   const uint32_t index0 = kIndex - (kLossless ? sl * CL : 0);   // a key's index of the lane's first expert
   float bias_most = 0.f;
   if (a.bias) {
@@ -191,31 +200,36 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
     const X* row = static_cast<const X*>(a.logits) + t * a.ld;
     float u[CL];
     rows::F2 finite = rows::f2(0.f, 0.f);
+    if (a.vec) {
 #pragma unroll
-    for (int i = 0; i < CL / V; ++i) {
-      const int e = sl * CL + i * V;
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (e < a.E) {
-        if constexpr (V * sizeof(X) == 16) {
-          const uint4 x = *reinterpret_cast<const uint4*>(row + e);
-          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(row + e);
-          w[0] = x.x; w[1] = x.y;
+      for (int i = 0; i < CL / V; ++i) {
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (i * V < count) {
+          if constexpr (V * sizeof(X) == 16) {
+            const uint4 x = *reinterpret_cast<const uint4*>(row + e0 + i * V);
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(row + e0 + i * V);
+            w[0] = x.x; w[1] = x.y;
+          }
         }
-      }
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        u[i * V + j] = sizeof(X) == 4 ? __uint_as_float(w[j & 3]) : j & 1 ? bf16_hi(w[(j / 2) & 3]) : bf16_lo(w[(j / 2) & 3]);
+        for (int j = 0; j < V; ++j)
+          u[i * V + j] = sizeof(X) == 4 ? __uint_as_float(w[j & 3])
+                                        : j & 1 ? bf16_hi(w[(j / 2) & 3]) : bf16_lo(w[(j / 2) & 3]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < CL; ++q) u[q] = q < count ? to_f(row[e0 + q]) : 0.f;
     }
 #pragma unroll
     for (int q = 0; q < CL; q += 2)                     // NaN after an infinity or a NaN
       finite = rows::fma2(rows::f2(u[q], u[q + 1]), rows::f2(0.f, 0.f), finite);
-    const bool plain = !__any_sync(kAll, rows::sum2(finite) != 0.f) && a.E == 8 * CL;
+    const bool plain = !__any_sync(kAll, rows::sum2(finite) != 0.f || count < CL);
     if (!plain) {
 #pragma unroll
       for (int q = 0; q < CL; ++q) {
-        const bool there = sl * CL + q < a.E;
+        const bool there = q < count;
         if (there && !(u[q] < INFINITY)) bad = true;    // NaN and +inf read as -inf
         if (!there || !(u[q] < INFINITY)) u[q] = -INFINITY;
       }
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
       sum = sum8(sum);
     }
     const float inv = a.sigmoid ? 1.f : __fdividef(1.f, sum);
-    // the keys; what is no expert counts as a masked one behind them
+    // the keys; a place without an expert counts as a masked one
     uint32_t key[CL];
     BestKeys<CL> best;
     best.clear();
@@ -305,8 +319,8 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
           bool unsure = live && next > -INFINITY && !(last - next > near_of<CL>(a.sigmoid, inv, last) + kLead * fabsf(last));
           const int q0 = (index0 - (best.m[0] & kIndex)) & (CL - 1), q1 = (index0 - (best.m[1] & kIndex)) & (CL - 1);
           const bool two = live && a.group_top == 2;
-          const bool s = better_groups(a, live ? logit(a, row, sl * CL + q0, &unused) : 0.f, live ? my_bias[q0] : 0.f,
-                                       two ? logit(a, row, sl * CL + q1, &unused) : 0.f, two ? my_bias[q1] : 0.f, live, own,
+          const bool s = better_groups(a, live ? logit(a, row, e0 + q0, &unused) : 0.f, live ? my_bias[q0] : 0.f,
+                                       two ? logit(a, row, e0 + q1, &unused) : 0.f, two ? my_bias[q1] : 0.f, live, own,
                                        first, 0, top, Pair{}, &unsure);
           const unsigned open = __ballot_sync(kAll, unsure);
           if (again && !(open >> first & 0xffu)) {
@@ -337,7 +351,8 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
         ++n;
         if (sl == i) sel = m;
         if (best.m[0] == m && !(who & below)) {         // (of equal ones the first lane)
-          slot_e[first * 2 + i] = (kLossless ? 0 : sl * CL) + (int)(kIndex - (m & kIndex));
+          // (no expert: one that is none came after masked ones, and the token is done again)
+          slot_e[first * 2 + i] = min(e0 + (int)((index0 - (m & kIndex)) & (CL - 1)), a.E - 1);
           best.pop(key);
         }
       }
@@ -345,12 +360,13 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
     __syncwarp();
     int e = sl < n ? slot_e[first * 2 + sl] : 0;
     float l = sl < n ? logit(a, row, e, &unused) : -INFINITY;
-    if (!(by_logit && kLossless)) {
-      // (equal keys of two lanes came by their place in the lane: masked ones are chosen again)
-      if (!kLossless && !(last > -INFINITY)) again = true;
+    // (equal keys of two lanes came by their place in the lane, and places without an
+    // expert count as masked ones: masked ones are chosen again)
+    if (!(last > -INFINITY)) again = true;
+    if (!(by_logit && kLossless) || __any_sync(kAll, again)) {
       // is the order of neighbours certain?
       const float v = leading(sel), pv = __shfl_up_sync(kAll, v, 1, 8), pl = __shfl_up_sync(kAll, l, 1, 8);
-      const float b = sl < n ? bias[e / CL * (CL + 4) + e % CL] : 0.f, pb = __shfl_up_sync(kAll, b, 1, 8);
+      const float b = sl < n ? biases[e] : 0.f, pb = __shfl_up_sync(kAll, b, 1, 8);
       const float gap = by_logit ? 0.f : near_pair<CL>(a.sigmoid, inv, pv, pb, v, b) + 2.f * kLead * fabsf(v);
       const int pe = __shfl_up_sync(kAll, e, 1, 8);
       const bool close = sl > 0 && v > -INFINITY && !(pv - v > gap) && !(pl == l && pb == b && pe < e);
@@ -358,7 +374,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
       if (__any_sync(kAll, close || n > a.k || open)) {
         const int e2 = sl + 8 < n ? slot_e[first * 2 + sl + 8] : 0;
         const float l2 = sl + 8 < n ? logit(a, row, e2, &unused) : -INFINITY;
-        const float b2 = sl + 8 < n ? bias[e2 / CL * (CL + 4) + e2 % CL] : 0.f;
+        const float b2 = sl + 8 < n ? biases[e2] : 0.f;
         e = order8<X, CL>(a, row, e, e2, l, l2, b, b2, n, top, inv, slot_e);
         open = open || e < 0;
         const unsigned left = __ballot_sync(kAll, open);
@@ -405,13 +421,11 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
 // block 18 / 20, 20 tokens 16.5 / 15; 128 experts, 40 tokens 18.5 / 18.4).
 constexpr int kManyTokens = 32;
 template <typename X, int CL>
-cudaError_t run_many(ScoreArgs a, int blocks, bool* taken, cudaStream_t s) {
+cudaError_t run_many(ScoreArgs a, int blocks, cudaStream_t s) {
   constexpr int kVec = CL * (int)sizeof(X) < 16 ? CL * (int)sizeof(X) : 16;
-  a.seg = a.group_size % CL ? 0 : a.group_size / CL;
-  for (a.seg_log = 0; 1 << a.seg_log < a.seg;) ++a.seg_log;
-  *taken = ((uintptr_t)a.logits & (kVec - 1)) == 0 && a.ld * sizeof(X) % kVec == 0 && a.E * sizeof(X) % kVec == 0 &&
-           (a.groups == 1 || (a.seg > 0 && !(a.seg & (a.seg - 1))));
-  if (!*taken) return cudaSuccess;
+  // by vectors: rows and groups start on their boundaries
+  a.vec = ((uintptr_t)a.logits & (kVec - 1)) == 0 && a.ld * sizeof(X) % kVec == 0 &&
+          a.group_size * sizeof(X) % kVec == 0;
   return a.groups > 1 ? launch_overlapped(score_many_kernel<X, CL, true>, blocks, kManyThreads<CL>, 0, s, a)
                       : launch_overlapped(score_many_kernel<X, CL, false>, blocks, kManyThreads<CL>, 0, s, a);
 }
@@ -419,15 +433,19 @@ cudaError_t run_many(ScoreArgs a, int blocks, bool* taken, cudaStream_t s) {
 }  // namespace
 
 template <typename X>
-cudaError_t launch_score_many(const ScoreArgs& a, int blocks, bool* taken, cudaStream_t s) {
+cudaError_t launch_score_many(ScoreArgs a, int blocks, bool* taken, cudaStream_t s) {
   *taken = false;
-  if (a.per_block < kManyTokens || blocks < 2 || a.k > 8 || a.E > 256) return cudaSuccess;
-  return a.E <= 32 ? run_many<X, 4>(a, blocks, taken, s)
-         : a.E <= 64 ? run_many<X, 8>(a, blocks, taken, s)
-         : a.E <= 128 ? run_many<X, 16>(a, blocks, taken, s)
-                      : run_many<X, 32>(a, blocks, taken, s);
+  if (a.per_block < kManyTokens || blocks < 2 || a.k > 8 || a.groups > 8) return cudaSuccess;
+  for (a.seg = 8, a.seg_log = 3; a.groups * a.seg > 8; a.seg /= 2) --a.seg_log;
+  const int n = (a.group_size + a.seg - 1) / a.seg;      // experts of a lane
+  if (n > 32) return cudaSuccess;
+  *taken = true;
+  return n <= 4 ? run_many<X, 4>(a, blocks, s)
+         : n <= 8 ? run_many<X, 8>(a, blocks, s)
+         : n <= 16 ? run_many<X, 16>(a, blocks, s)
+                   : run_many<X, 32>(a, blocks, s);
 }
-template cudaError_t launch_score_many<float>(const ScoreArgs&, int, bool*, cudaStream_t);
-template cudaError_t launch_score_many<__nv_bfloat16>(const ScoreArgs&, int, bool*, cudaStream_t);
+template cudaError_t launch_score_many<float>(ScoreArgs, int, bool*, cudaStream_t);
+template cudaError_t launch_score_many<__nv_bfloat16>(ScoreArgs, int, bool*, cudaStream_t);
 
 }  // namespace moe

@@ -15,7 +15,7 @@ struct ScoreArgs {
   int64_t ld;
   int T, E, k, per_block;
   int groups, group_size, top_groups, group_top;
-  int seg, seg_log;         // lanes of a group where it is 2^seg_log whole lanes, else 0
+  int seg, seg_log;         // lanes of a group where it has 2^seg_log, else 0
   int sigmoid, renorm, vec;
   float scale;
   int32_t* idx;
@@ -621,6 +621,6 @@ __device__ __noinline__ int choose32(const ScoreArgs& a, const X* row, uint2* sl
 // Where a token count is large and the sizes fit: the choice, gates and
 // histograms by eight lanes per token; *taken: whether they did.
 template <typename X>
-cudaError_t launch_score_many(const ScoreArgs& a, int blocks, bool* taken, cudaStream_t s);
+cudaError_t launch_score_many(ScoreArgs a, int blocks, bool* taken, cudaStream_t s);
 
 }  // namespace moe

@@ -111,6 +111,10 @@ CASES = [
     (4999, 256, 8, dict(groups=4, top_groups=2, group_top=2)), (5001, 248, 7, dict(score="sigmoid")), (5000, 20, 1, {}),
     (4903, 128, 5, dict(score="sigmoid", groups=8, top_groups=3, group_top=2)), (5000, 96, 9, {}),
     (4905, 64, 3, dict(score="sigmoid", groups=2, top_groups=1, group_top=1)), (4870, 30, 4, {}),
+    (5003, 160, 6, dict(score="sigmoid", groups=8, top_groups=3, group_top=2, scale=2.5)), (5000, 250, 8, {}),
+    (4903, 35, 5, dict(groups=5, top_groups=3, group_top=1, renormalise=False)),
+    (5005, 14, 2, dict(groups=7, top_groups=2, group_top=2)), (4999, 99, 7, dict(score="sigmoid", groups=3, top_groups=2, group_top=2)),
+    (5001, 513, 3, {}), (4997, 320, 8, dict(groups=16, top_groups=5, group_top=2)),
 ]
 
 
@@ -186,19 +190,20 @@ def test_a_few_equal_logits(dtype, E, bias):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [32, 40])
 @pytest.mark.parametrize("many", [False, True])
-def test_masked_experts(score, renorm, many):
+def test_masked_experts(score, renorm, many, E):
     """-inf and the type's lowest value in masked places, tokens with fewer
     experts than top_k, with none, and groups left empty; large logits."""
     rng = np.random.default_rng(6)
-    l = rng.standard_normal((200, 32)).astype(np.float32)
-    l[:60][rng.random((60, 32)) < 0.5] = -np.inf
+    l = rng.standard_normal((200, E)).astype(np.float32)
+    l[:60][rng.random((60, E)) < 0.5] = -np.inf
     l[60:90, 8:] = -np.inf
     l[90:100, 2:] = -np.inf
-    l[100:130][rng.random((30, 32)) < 0.5] = np.finfo(np.float32).min
+    l[100:130][rng.random((30, E)) < 0.5] = np.finfo(np.float32).min
     l[130:150] *= 200
     how = dict(score=score, renormalise=renorm)
-    for bias, more in ((None, {}), (rng.standard_normal(32).astype(np.float32), {}),
+    for bias, more in ((None, {}), (rng.standard_normal(E).astype(np.float32), {}),
                        (None, dict(groups=4, top_groups=2, group_top=1))):
         # (scores of the lowest value are 0 in 64 bits, like those of logits below -745)
         x, r, dg, dl = _run(_many(l, many), bias, 4, **how, **more)
