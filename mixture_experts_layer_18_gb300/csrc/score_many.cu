@@ -23,6 +23,19 @@ __device__ __forceinline__ float sum8(float v) {
   return v;
 }
 
+// softmax_scale of the tokens with a lane in `open`, a token at a time by the whole warp.
+template <typename X>
+__device__ __forceinline__ Pair softmax_scales(const ScoreArgs& a, const X* row, float top, unsigned open) {
+  Pair scale{};
+  for (int t = 0; t < 32; t += 8)
+    if (open >> t & 0xffu) {
+      const X* r = reinterpret_cast<const X*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(row), t));
+      const Pair p = softmax_scale(a, r, __shfl_sync(kAll, top, t));
+      if ((threadIdx.x & 24) == t) scale = p;
+    }
+  return scale;
+}
+
 // As order(), for up to 16 candidates of each of four tokens: lane sl of a token
 // has candidates sl and sl + 8 (n: how many the token has).  Returns the lane's
 // expert in that order, -1 to all lanes of a token whose order is not known.
@@ -62,15 +75,7 @@ __device__ __noinline__ int order8(const ScoreArgs& a, const X* row, int e0, int
   }
   unsigned open = __ballot_sync(kAll, unsure);
   if (open) {
-    Pair scale{};
-    if (!a.sigmoid) {
-      for (int t = 0; t < 32; t += 8)                        // a token at a time, by the whole warp
-        if (open >> t & 0xffu) {
-          const X* r = reinterpret_cast<const X*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(row), t));
-          const Pair p = softmax_scale(a, r, __shfl_sync(kAll, top, t));
-          if (first == t) scale = p;
-        }
-    }
+    const Pair scale = a.sigmoid ? Pair{} : softmax_scales(a, row, top, open);
     const Exact x0 = exact_value(a.sigmoid, l[0], b[0], top, scale), x1 = exact_value(a.sigmoid, l[1], b[1], top, scale);
     better[0] = better[1] = 0;
     unsure = false;
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
         const float most = bias_most + (a.sigmoid ? 1.f : inv);
         const float gap = by_logit ? 0.f : 2.f * near_of<CL>(a.sigmoid, inv, 2.f * most) + 2.f * kLead * most;
         again = hi > -INFINITY && !(lo - hi > gap || (by_logit && kLossless));
-        if (a.seg == 1 && a.sigmoid && !by_logit && __any_sync(kAll, again)) {
+        if (a.seg == 1 && !by_logit && __any_sync(kAll, again)) {
           // a lane's own best, if no third one comes near the last of them
           const float last = leading(a.group_top == 1 ? best.m[0] : best.m[1]);
           const float next = leading(a.group_top == 1 ? best.m[1] : best.m[2]);
@@ -319,9 +324,10 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
           bool unsure = live && next > -INFINITY && !(last - next > near_of<CL>(a.sigmoid, inv, last) + kLead * fabsf(last));
           const int q0 = (index0 - (best.m[0] & kIndex)) & (CL - 1), q1 = (index0 - (best.m[1] & kIndex)) & (CL - 1);
           const bool two = live && a.group_top == 2;
+          const Pair scale = a.sigmoid ? Pair{} : softmax_scales(a, row, top, __ballot_sync(kAll, again));
           const bool s = better_groups(a, live ? logit(a, row, e0 + q0, &unused) : 0.f, live ? my_bias[q0] : 0.f,
                                        two ? logit(a, row, e0 + q1, &unused) : 0.f, two ? my_bias[q1] : 0.f, live, own,
-                                       first, 0, top, Pair{}, &unsure);
+                                       first, 0, top, scale, &unsure);
           const unsigned open = __ballot_sync(kAll, unsure);
           if (again && !(open >> first & 0xffu)) {
             stays = s;
