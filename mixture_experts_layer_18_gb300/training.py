@@ -203,7 +203,7 @@ class RMSNorm(_Op):
         self.rstd = torch.empty(T, dtype=torch.float32, device=self.device) if backward else None
         self.ws = torch.empty(need if backward else 0, dtype=torch.uint8, device=self.device)
         self._keep(self.rstd, self.ws)
-        self._rstd = _ptr(self.rstd)
+        self._rstd, self._ws, self._width = _ptr(self.rstd), (self.ws.data_ptr(), self.ws.numel()), self.shape[1:]
 
     def _dims(self, *lds):
         """As LayerNorm's."""
@@ -213,21 +213,21 @@ class RMSNorm(_Op):
                                                          TYPES[self.weight_dtype], self.eps))
         return known[1]
 
-    def _rows_or_none(self, name, t):
-        return (None, self.H) if t is None else self._rows(name, t, self.shape, self.dtype)
-
     def forward(self, x, gamma, y=None, residual=None, h=None, encoded=None, stream=None):
         """h = x + residual, y = h / rms(h) * gamma; gamma may be None (1).  Of h
         (only with a residual), y and encoded (an MXRows: y in 8 bits) those that
         are given are written."""
-        x, ld_x = self._rows("x", x, self.shape, self.dtype)
-        residual, ld_r = self._rows_or_none("residual", residual)
-        h, ld_h = self._rows_or_none("h", h)
-        y, ld_y = self._rows_or_none("y", y)
-        gamma = self._fits_or_none("gamma", gamma, self.shape[1:], self.weight_dtype)
+        shape, dt, H = self.shape, self.dtype, self.H
+        if residual is None and h is not None:
+            _require(False, "RMSNorm: h is x itself without a residual")
+        x, ld_x = self._rows("x", x, shape, dt)
+        residual, ld_r = (None, H) if residual is None else self._rows("residual", residual, shape, dt)
+        h, ld_h = (None, H) if h is None else self._rows("h", h, shape, dt)
+        y, ld_y = (None, H) if y is None else self._rows("y", y, shape, dt)
+        if gamma is not None:
+            gamma = self._fits("gamma", gamma, self._width, self.weight_dtype)
         q, scales = (None, None) if encoded is None else encoded._pointers("encoded", self)
-        _require(h is None or residual is not None, "RMSNorm: h is x itself without a residual")
-        rc = moe_rms_norm(self._dims(ld_x, ld_r, ld_h, ld_y, self.H, self.H), x, residual, gamma, h, y, q, scales,
+        rc = moe_rms_norm(self._dims(ld_x, ld_r, ld_h, ld_y, H, H), x, residual, gamma, h, y, q, scales,
                           self._rstd, self._current(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_rms_norm")
@@ -236,15 +236,17 @@ class RMSNorm(_Op):
         """dx (of x and of residual) and dgamma (None leaves it out) of the last
         forward, whose sum is h; dh: the gradient that reaches h on other ways."""
         _require(self.rstd is not None, "RMSNorm: built with backward=False")
-        dy, ld_dy = self._rows("dy", dy, self.shape, self.dtype)
-        h, ld_h = self._rows("h", h, self.shape, self.dtype)
-        dh, ld_dh = self._rows_or_none("dh", dh)
-        dx, ld_dx = self._rows("dx", dx, self.shape, self.dtype)
-        gamma = self._fits_or_none("gamma", gamma, self.shape[1:], self.weight_dtype)
-        dgamma = self._fits_or_none("dgamma", dgamma, self.shape[1:], self.weight_dtype)
-        rc = moe_rms_norm_backward(self._dims(self.H, self.H, ld_h, ld_dy, ld_dh, ld_dx), dy, h, dh, gamma,
-                                   self._rstd, dx, dgamma, self.ws.data_ptr(), self.ws.numel(),
-                                   self._current(stream))
+        shape, dt, H = self.shape, self.dtype, self.H
+        dy, ld_dy = self._rows("dy", dy, shape, dt)
+        h, ld_h = self._rows("h", h, shape, dt)
+        dh, ld_dh = (None, H) if dh is None else self._rows("dh", dh, shape, dt)
+        dx, ld_dx = self._rows("dx", dx, shape, dt)
+        if gamma is not None:
+            gamma = self._fits("gamma", gamma, self._width, self.weight_dtype)
+        if dgamma is not None:
+            dgamma = self._fits("dgamma", dgamma, self._width, self.weight_dtype)
+        rc = moe_rms_norm_backward(self._dims(H, H, ld_h, ld_dy, ld_dh, ld_dx), dy, h, dh, gamma, self._rstd, dx,
+                                   dgamma, *self._ws, self._current(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_rms_norm_backward")
 
@@ -269,18 +271,18 @@ class MXRows(_Op):
         self.codes, self.scales = torch.empty((rows, cols), **u8), torch.empty((rows, cols // 32), **u8)
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
         self._keep(self.codes, self.scales, self.status)
-        self._at = (_ptr(self.codes), _ptr(self.scales))
+        self._at, self._shape = (_ptr(self.codes), _ptr(self.scales)), torch.Size((rows, cols))
 
     def _pointers(self, name, op):
         """The addresses, for an operator whose rows they are to be."""
-        if (self.rows, self.cols) != (op.T, op.H) or self.index != op.index:
+        if self.rows != op.T or self.cols != op.H or self.index != op.index:
             raise MoEError(MOE_ERR_INVALID_ARG, f"{name}: expected [{op.T}, {op.H}] on {op.device}; got "
                                                 f"[{self.rows}, {self.cols}] on {self.device}")
         return self._at
 
     def encode(self, x, stream=None):
         """From bfloat16 rows that start on 16-byte boundaries."""
-        x, ld = self._rows("x", x, (self.rows, self.cols), torch.bfloat16)
+        x, ld = self._rows("x", x, self._shape, torch.bfloat16)
         _require(ld < 1 << 31, "MXRows: rows less than 2^31 elements apart")
         rc = moe_quantize_mxfp8(x, self.rows, self.cols, ld, 1, None, 0, *self._at, self.status.data_ptr(),
                                 self._current(stream))
@@ -290,9 +292,11 @@ class MXRows(_Op):
     def decode(self, out, stream=None):
         """The values into bfloat16 or float32 rows."""
         dtype = getattr(out, "dtype", None)
-        _require(dtype in TYPES, "MXRows: float32 or bfloat16")
-        out, ld = self._rows("out", out, (self.rows, self.cols), dtype)
-        rc = moe_dequantize_mxfp8(*self._at, self.rows, self.cols, ld, TYPES[dtype], out, self._current(stream))
+        kind = TYPES.get(dtype)
+        if kind is None:
+            _require(False, "MXRows: float32 or bfloat16")
+        out, ld = self._rows("out", out, self._shape, dtype)
+        rc = moe_dequantize_mxfp8(*self._at, self.rows, self.cols, ld, kind, out, self._current(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_dequantize_mxfp8")
 
@@ -330,6 +334,7 @@ class Router(_Op):
         self._keep(*arrays, self.ws, self.status)
         self.route_out = moe_route_out(*map(_ptr, arrays))
         self._shape, self._counts, self._status = torch.Size((T, E)), self.counts.data_ptr(), self.status.data_ptr()
+        self._experts, self._chosen = torch.Size((E,)), torch.Size((T, top_k))
         self._ws = (self.ws.data_ptr(), need)
 
     def _dims(self, ld):
@@ -342,7 +347,8 @@ class Router(_Op):
     def forward(self, logits, bias=None, stream=None):
         """logits [T, E] (a slice of a wider buffer too); bias [E] float32 or None."""
         logits, ld = self._rows("logits", logits, self._shape, self.dtype)
-        bias = self._fits_or_none("bias", bias, self._shape[1:], torch.float32)
+        if bias is not None:
+            bias = self._fits("bias", bias, self._experts, torch.float32)
         rc = moe_router(self._dims(ld), logits, bias, self.route_out, *self._ws, self._status,
                         self._current(stream))
         if rc != MOE_OK:
@@ -351,7 +357,7 @@ class Router(_Op):
     def backward(self, logits, dgate, dlogits, stream=None):
         """dlogits [T, E] of the last forward's logits, from dgate [T, top_k]."""
         logits, ld = self._rows("logits", logits, self._shape, self.dtype)
-        dgate = self._fits("dgate", dgate, (self.T, self.k), torch.float32)
+        dgate = self._fits("dgate", dgate, self._chosen, torch.float32)
         dlogits = self._fits("dlogits", dlogits, self._shape, self.dtype)
         rc = moe_router_backward(self._dims(ld), self.route_out, logits, dgate, dlogits, self._status,
                                  self._current(stream))
@@ -361,9 +367,8 @@ class Router(_Op):
     def update_bias(self, bias, rate, out=None, stream=None):
         """Moves the bias by ``rate`` towards an even load, by the last forward's
         counts: in place, or into ``out``."""
-        shape = self._shape[1:]
-        bias = self._fits("bias", bias, shape, torch.float32)
-        out = bias if out is None else self._fits("out", out, shape, torch.float32)
+        bias = self._fits("bias", bias, self._experts, torch.float32)
+        out = bias if out is None else self._fits("out", out, self._experts, torch.float32)
         rc = moe_balance_bias(self.E, self._counts, rate, bias, out, self._current(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_balance_bias")
