@@ -1,5 +1,5 @@
-// score_many.cu - the router by scores (score_route.cu) for many tokens: 24 us for 16384
-// tokens of 256 experts in groups and 40 for 65536 of 128, with the permutation, where a
+// score_many.cu - the router by scores (score_route.cu) for many tokens: 23 us for 16384
+// tokens of 256 experts in groups and 36 for 65536 of 128, with the permutation, where a
 // warp per token took 36 and 69.
 #include "score_route.cuh"
 
@@ -8,10 +8,12 @@ namespace moe {
 namespace {
 
 // Many tokens: eight lanes per token, four tokens per warp, so that what a token
-// takes besides its elements (rounds, gates, addresses) is paid once for four.
+// takes besides its elements (order, gates, addresses) is paid once for four.
 // A group has a power of two of the eight lanes (all of them without groups), and a
-// lane up to CL neighbouring experts of its group; top_k <= 8.  Of fp32 logits a key's
-// index is that within the lane, which leaves more bits to the value.
+// lane up to CL neighbouring experts of its group; top_k <= 8.  A lane puts its keys
+// in order by eights and keeps the best eight, and the lanes' lists are merged in three
+// steps: 10 % less time than a maximum over the lanes for each of the chosen, whose
+// rounds wait for one another (65536 tokens of 128 experts: 36.1 us instead of 39.1).
 __device__ __forceinline__ uint32_t max8(uint32_t v) {          // over a token's lanes
 #pragma unroll
   for (int o = 4; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
@@ -110,44 +112,43 @@ __device__ __noinline__ int order8(const ScoreArgs& a, const X* row, int e0, int
   return open >> first & 0xffu ? -1 : sl < n ? slot[first * 2 + sl] : 0;
 }
 
-// A lane's best keys, the largest first (more are looked for again when these are
-// taken: 0.6 times a token with three of 16 kept, with four of 32 and half of the groups gone).
-template <int CL>
-struct BestKeys {
-  static constexpr int K = CL > 16 ? 4 : 3;
-  uint32_t m[K];
-  __device__ __forceinline__ void clear() {
+// Eight keys in descending order: by a merge exchange network (19 exchanges),
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+__device__ __forceinline__ void sort8(uint32_t (&k)[8]) {
+  exchange(k[0], k[1]); exchange(k[2], k[3]); exchange(k[4], k[5]); exchange(k[6], k[7]);
+  exchange(k[0], k[2]); exchange(k[1], k[3]); exchange(k[4], k[6]); exchange(k[5], k[7]);
+  exchange(k[1], k[2]); exchange(k[5], k[6]);
+  exchange(k[0], k[4]); exchange(k[1], k[5]); exchange(k[2], k[6]); exchange(k[3], k[7]);
+  exchange(k[2], k[4]); exchange(k[3], k[5]);
+  exchange(k[1], k[2]); exchange(k[3], k[4]); exchange(k[5], k[6]);
+}
+// and the best eight of two such lists: one against the other backwards leaves them
+// as a list that rises and falls, which three rounds of exchanges put in order.
+__device__ __forceinline__ void merge8(uint32_t (&k)[8], const uint32_t (&other)[8]) {
 #pragma unroll
-    for (int i = 0; i < K; ++i) m[i] = 0;
-  }
-  __device__ __forceinline__ void insert(uint32_t k) {
+  for (int i = 0; i < 8; ++i) k[i] = max(k[i], other[7 - i]);
 #pragma unroll
-    for (int i = K - 1; i > 0; --i) m[i] = max(m[i], min(m[i - 1], k));
-    m[0] = max(m[0], k);
-  }
-  __device__ __forceinline__ void pop(const uint32_t (&key)[CL]) {
-    const uint32_t last = m[0];
+  for (int o = 4; o; o >>= 1)
 #pragma unroll
-    for (int i = 0; i + 1 < K; ++i) m[i] = m[i + 1];
-    m[K - 1] = 0;
-    if (m[0] == 0) {
-#pragma unroll
-      for (int q = 0; q < CL; ++q)
-        if (key[q] < last) m[0] = max(m[0], key[q]);
-    }
-  }
-};
+    for (int i = 0; i < 8; ++i)
+      if (!(i & o)) exchange(k[i], k[i + o]);
+}
 
-// As many warps as the registers leave room for (65536 tokens of 128 experts: 41.5 us
-// with 736 threads, 43.3 with 640).
+// As many warps as the registers leave room for (5000 tokens of 256 experts: 16.8 us
+// with 512 threads, 18.0 with 576, 17.1 with 480; 65536 of 128: 36.0 with 736 or 800,
+// 36.2 with 640).
 template <int CL>
 constexpr int kManyThreads = CL > 16 ? 512 : 736;
 
 template <typename X, int CL, bool GROUPED>
 __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const __grid_constant__ ScoreArgs a) {
-  constexpr bool kLossless = sizeof(X) == 2;            // a bf16 logit is all leading bits:
-  constexpr uint32_t kIndex = (kLossless ? 8 : 1) * CL - 1;    // a key then holds the expert's index, else that in the lane
-  constexpr float kLead = (kIndex + 1) * 0x1p-23f;      // what it takes from the value, relative to it
+  constexpr uint32_t kIndex = 8 * CL - 1;               // the bits of a key that hold the expert's place
+  constexpr float kLead = 8.f * CL * 0x1p-23f;          // what they take from the value, relative to it
+  constexpr bool kLossless = sizeof(X) == 2;            // a bf16 logit is all leading bits
   constexpr int V = CL * (int)sizeof(X) < 16 ? CL : 16 / (int)sizeof(X);
   __shared__ int hist[8 * CL];
   __shared__ float biases[8 * CL];                      // by expert,
@@ -177,12 +178,15 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, sl = lane & 7, first = lane & 24;
-  const unsigned below = ((1u << sl) - 1u) << first;
   uint2* slot = slots[threadIdx.x >> 5];
-  int* slot_e = reinterpret_cast<int*>(slot);           // [4 tokens][16]
   const float* my_bias = bias + sl * (CL + 4);
   const int e0 = first_of(sl), count = count_of(sl);
-  const uint32_t index0 = kIndex - (kLossless ? sl * CL : 0);   // a key's index of the lane's first expert
+  const uint32_t index0 = kIndex - sl * CL;             // a key's place of the lane's first expert, downwards
+  // the expert of a key (of a masked one, which may be none: some expert)
+  auto expert = [&](uint32_t key) {
+    const int at = kIndex - (key & kIndex);
+    return min(first_of(at / CL) + at % CL, a.E - 1);
+  };
   float bias_most = 0.f;
   if (a.bias) {
 #pragma unroll
@@ -261,13 +265,20 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
       sum = sum8(sum);
     }
     const float inv = a.sigmoid ? 1.f : __fdividef(1.f, sum);
-    // the keys; a place without an expert counts as a masked one
-    uint32_t key[CL];
-    BestKeys<CL> best;
-    best.clear();
+    // the keys, the lane's best eight in order; a place without an expert counts as a masked one
+    uint32_t list[8] = {}, part[8];
     auto take = [&](int q, float v) {
-      key[q] = (key_of(v) & ~kIndex) | (index0 - q);
-      best.insert(key[q]);
+      const uint32_t key = (key_of(v) & ~kIndex) | (index0 - q);
+      if (q < 8) list[q & 7] = key;
+      else part[q & 7] = key;
+      if (q % 8 == 7 || q == CL - 1) {
+        if (q < 8) {
+          sort8(list);
+        } else {
+          sort8(part);
+          merge8(list, part);
+        }
+      }
     };
     auto biased = [&](auto score) {
 #pragma unroll
@@ -294,7 +305,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
     }
     bool again = false;                                 // (the same in a token's lanes)
     if (GROUPED) {
-      uint32_t g1 = best.m[0], g2 = best.m[1];
+      uint32_t g1 = list[0], g2 = list[1];
       for (int o = 1; o < a.seg; o <<= 1) {
         const uint32_t n1 = __shfl_xor_sync(kAll, g1, o), n2 = __shfl_xor_sync(kAll, g2, o);
         g2 = max(min(g1, n1), max(g2, n2));
@@ -317,17 +328,36 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
         const float gap = by_logit ? 0.f : 2.f * near_of<CL>(a.sigmoid, inv, 2.f * most) + 2.f * kLead * most;
         again = hi > -INFINITY && !(lo - hi > gap || (by_logit && kLossless));
         if (a.seg == 1 && !by_logit && __any_sync(kAll, again)) {
-          // a lane's own best, if no third one comes near the last of them
-          const float last = leading(a.group_top == 1 ? best.m[0] : best.m[1]);
-          const float next = leading(a.group_top == 1 ? best.m[1] : best.m[2]);
-          const bool live = own < a.groups && last > -INFINITY;
-          bool unsure = live && next > -INFINITY && !(last - next > near_of<CL>(a.sigmoid, inv, last) + kLead * fabsf(last));
-          const int q0 = (index0 - (best.m[0] & kIndex)) & (CL - 1), q1 = (index0 - (best.m[1] & kIndex)) & (CL - 1);
-          const bool two = live && a.group_top == 2;
+          // a lane's own best: those of its first three by their fp32 values, if no other
+          // comes near the last of them without being the same
+          float x[3], bx[3], f[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const bool on = own < a.groups && leading(list[i]) > -INFINITY;
+            const int q = (index0 - (list[i] & kIndex)) & (CL - 1);
+            x[i] = on ? logit(a, row, e0 + q, &unused) : 0.f;
+            bx[i] = on ? my_bias[q] : 0.f;
+            f[i] = on ? score_of(a, x[i], top, inv) + bx[i] : -INFINITY;
+          }
+          auto order = [&](int i, int j) {
+            if (!(f[j] > f[i])) return;
+            const float t = f[i], tx = x[i], tb = bx[i];
+            f[i] = f[j]; x[i] = x[j]; bx[i] = bx[j];
+            f[j] = t; x[j] = tx; bx[j] = tb;
+          };
+          order(1, 2);
+          order(0, 1);
+          order(1, 2);
+          const bool two = a.group_top == 2;
+          const float least = two ? f[1] : f[0], xl = two ? x[1] : x[0], bl = two ? bx[1] : bx[0];
+          const bool live = own < a.groups && least > -INFINITY;
+          auto apart = [&](float v, float lead) {
+            return !(v > -INFINITY) || least - v > near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(least), fabsf(v))) + lead * fabsf(v);
+          };
+          bool unsure = live && !((two || apart(f[1], 0.f) || (x[1] == xl && bx[1] == bl)) &&
+                                  (apart(f[2], 0.f) || (x[2] == xl && bx[2] == bl)) && apart(leading(list[3]), kLead));
           const Pair scale = a.sigmoid ? Pair{} : softmax_scales(a, row, top, __ballot_sync(kAll, again));
-          const bool s = better_groups(a, live ? logit(a, row, e0 + q0, &unused) : 0.f, live ? my_bias[q0] : 0.f,
-                                       two ? logit(a, row, e0 + q1, &unused) : 0.f, two ? my_bias[q1] : 0.f, live, own,
-                                       first, 0, top, scale, &unsure);
+          const bool s = better_groups(a, x[0], bx[0], x[1], bx[1], live, own, first, 0, top, scale, &unsure);
           const unsigned open = __ballot_sync(kAll, unsure);
           if (again && !(open >> first & 0xffu)) {
             stays = s;
@@ -335,53 +365,104 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
           }
         }
       }
-      if (!stays) best.clear();
-    }
-    // rounds of a maximum over the token's lanes: k, and more while the next may be as good as the k-th
-    uint32_t sel = 0;
-    int n = 0;
-    float last = -INFINITY;
-    bool stop = false;
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t m = max8(best.m[0]);
-      if (i >= a.k) {
-        const float v = leading(m);
-        const float gap = by_logit ? 0.f : near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(v))) + kLead * fabsf(v);
-        stop = stop || (by_logit && kLossless) || !(v > -INFINITY) || last - v > gap;
-        if (!__any_sync(kAll, !stop)) break;
-      } else if (i == a.k - 1) {
-        last = leading(m);
-      }
-      const unsigned who = __ballot_sync(kAll, best.m[0] == m);
-      if (!stop) {
-        ++n;
-        if (sl == i) sel = m;
-        if (best.m[0] == m && !(who & below)) {         // (of equal ones the first lane)
-          // (no expert: one that is none came after masked ones, and the token is done again)
-          slot_e[first * 2 + i] = min(e0 + (int)((index0 - (m & kIndex)) & (CL - 1)), a.E - 1);
-          best.pop(key);
-        }
+      if (!stays) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) list[i] = 0;
       }
     }
-    __syncwarp();
-    int e = sl < n ? slot_e[first * 2 + sl] : 0;
-    float l = sl < n ? logit(a, row, e, &unused) : -INFINITY;
-    // (equal keys of two lanes came by their place in the lane, and places without an
-    // expert count as masked ones: masked ones are chosen again)
+    // the token's best eight, the same in all its lanes, and how the k-th compares to the next
+    uint32_t best[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) best[i] = list[i];
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[i] = __shfl_xor_sync(kAll, best[i], o);
+      merge8(best, part);
+    }
+    auto next_below = [&](uint32_t key) {               // (a lane's list ends with its eighth)
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, list[i] < key ? list[i] : 0u);
+      return max8(m);
+    };
+    uint32_t sel = 0, kth = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (sl == i && i < a.k) sel = best[i];
+      if (i == a.k - 1) kth = best[i];
+    }
+    const float last = leading(kth);
+    int n = a.k, e = expert(sel);
+    float l = sl < a.k ? logit(a, row, e, &unused) : -INFINITY;
+    // (places without an expert count as masked ones: masked ones are chosen again)
     if (!(last > -INFINITY)) again = true;
     if (!(by_logit && kLossless) || __any_sync(kAll, again)) {
-      // is the order of neighbours certain?
-      const float v = leading(sel), pv = __shfl_up_sync(kAll, v, 1, 8), pl = __shfl_up_sync(kAll, l, 1, 8);
-      const float b = sl < n ? biases[e] : 0.f, pb = __shfl_up_sync(kAll, b, 1, 8);
-      const float gap = by_logit ? 0.f : near_pair<CL>(a.sigmoid, inv, pv, pb, v, b) + 2.f * kLead * fabsf(v);
-      const int pe = __shfl_up_sync(kAll, e, 1, 8);
-      const bool close = sl > 0 && v > -INFINITY && !(pv - v > gap) && !(pl == l && pb == b && pe < e);
-      bool open = again || n == 16;              // (16: there may be more)
-      if (__any_sync(kAll, close || n > a.k || open)) {
-        const int e2 = sl + 8 < n ? slot_e[first * 2 + sl + 8] : 0;
+      // is it certain, and the order of neighbours?  By the fp32 values of the chosen, and by
+      // the leading bits of the next
+      uint32_t next = next_below(kth);
+      float b = sl < a.k ? biases[e] : 0.f;
+      const float v = !(l > -INFINITY) || by_logit ? l : score_of(a, l, top, inv) + b;
+      const float kth_v = __shfl_sync(kAll, v, first + a.k - 1);
+      auto certain = [&](uint32_t key, float than) {
+        const float x = leading(key);
+        if (!(x > -INFINITY) || by_logit) return !(x > -INFINITY) || last > x;
+        return than - x > near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(than), fabsf(x))) + kLead * fabsf(x);
+      };
+      // (a lane whose eight are all among the chosen may have a ninth: the token's lanes
+      // look through that lane's experts once more, without those of its list.  One group
+      // of 32 experts and 8 of them chosen, so that each token does: 30 us for 16384
+      // instead of 23; 33 with that lane looking alone)
+      const unsigned owns = __ballot_sync(kAll, list[7] >= kth && list[7] != 0) >> first & 0xffu;
+      float ninth = -INFINITY;
+      if (__any_sync(kAll, owns != 0)) {
+        const int owner = owns ? __ffs(owns) - 1 : 0;
+        uint32_t in_list = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) in_list |= 1u << ((index0 - list[i]) & (CL - 1));
+        in_list = __shfl_sync(kAll, in_list, first + owner);
+        if (owns) {
+          const int from = first_of(owner), n_of = count_of(owner);
+          for (int q = sl; q < n_of; q += 8) {
+            const float x = logit(a, row, from + q, &unused);
+            const float s = by_logit || !(x > -INFINITY) ? x : score_of(a, x, top, inv) + bias[owner * (CL + 4) + q];
+            if (!(in_list >> q & 1)) ninth = fmaxf(ninth, s);
+          }
+        }
+        ninth = value_of(max8(key_of(ninth)));
+      }
+      const float pv = __shfl_up_sync(kAll, v, 1, 8), pl = __shfl_up_sync(kAll, l, 1, 8), pb = __shfl_up_sync(kAll, b, 1, 8);
+      const float gap = by_logit ? 0.f : near_pair<CL>(a.sigmoid, inv, pv, pb, v, b);
+      const bool close = sl > 0 && v > -INFINITY && !(pv - v > gap) && !(pl == l && pb == b);
+      const bool closes = __ballot_sync(kAll, close) >> first & 0xffu;
+      const float than = closes ? last : kth_v;          // (the k-th only if their order is known)
+      const bool full = ninth > -INFINITY &&
+             !(than - ninth > (by_logit ? 0.f : near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(than), fabsf(ninth)))));
+      const bool sure = certain(next, than) && !full;
+      if (__any_sync(kAll, closes || !sure || again)) {
+        // more candidates, as long as one may be as good as the k-th
+        uint32_t sel2 = 0, lowest = kth;
+        for (int i = a.k; i < 16; ++i) {
+          const bool more = !sure && !certain(next, last);
+          if (!__any_sync(kAll, more)) break;
+          if (more) {
+            ++n;
+            if (sl == i) sel = next;
+            if (sl == i - 8) sel2 = next;
+            lowest = next;
+          }
+          next = next_below(lowest);
+        }
+        // (16: there may be more; and a lane may have more than its list)
+        const bool ended = __ballot_sync(kAll, list[7] >= lowest && list[7] != 0) >> first & 0xffu;
+        bool open = again || n == 16 || (ended && (full || n > a.k));
+        e = expert(sel);
+        l = sl < n ? logit(a, row, e, &unused) : -INFINITY;
+        b = sl < n ? biases[e] : 0.f;
+        const int e2 = expert(sel2);
         const float l2 = sl + 8 < n ? logit(a, row, e2, &unused) : -INFINITY;
         const float b2 = sl + 8 < n ? biases[e2] : 0.f;
-        e = order8<X, CL>(a, row, e, e2, l, l2, b, b2, n, top, inv, slot_e);
+        e = order8<X, CL>(a, row, e, e2, l, l2, b, b2, n, top, inv, reinterpret_cast<int*>(slot));
         open = open || e < 0;
         const unsigned left = __ballot_sync(kAll, open);
         for (int o = 0; o < 32; o += 8)                  // what is left, a token at a time by the whole warp
@@ -424,7 +505,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
 
 // For at least kManyTokens per block; with fewer the longer way of a token through
 // its lanes counts (256 experts in groups, us here / with a warp per token: 33 tokens per
-// block 18 / 20, 20 tokens 16.5 / 15; 128 experts, 40 tokens 18.5 / 18.4).
+// block 17.5 / 20, 20 tokens 16.5 / 15; 128 experts, 40 tokens 18.5 / 18.4).
 constexpr int kManyTokens = 32;
 template <typename X, int CL>
 cudaError_t run_many(ScoreArgs a, int blocks, cudaStream_t s) {

@@ -25,8 +25,8 @@
 // (for at most kFusedTokens the same one does).
 //
 // Measured (GB300, fp32 logits, top 8, with the permutation): 1 token of 256 experts
-// in 8 groups 5.5 us; 1500 tokens 15 us; 16384 tokens 24 us; 65536 tokens of 128 experts,
-// softmax with a bias, 40 us (logits from HBM: 5 us).  The choice is bound by
+// in 8 groups 5.5 us; 1500 tokens 15 us; 16384 tokens 23 us; 65536 tokens of 128 experts,
+// softmax with a bias, 36 us (logits from HBM: 5 us).  The choice is bound by
 // instructions (62% of the issue slots with 65536 tokens, 41% with 16384, where a
 // block has 27 warps' worth of tokens for 16 warps), the permutation (6 us) by its
 // chain of dependent steps, 4000 cycles of it the other blocks' histograms.

@@ -211,6 +211,31 @@ def test_masked_experts(score, renorm, many, E):
         assert r.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,how", [(128, {}), (256, dict(score="sigmoid")), (128, dict(renormalise=False, groups=2, top_groups=1, group_top=2)),
+                                   (256, dict(score="sigmoid", groups=8, top_groups=4, group_top=2)),
+                                   (160, dict(score="softmax", groups=8, top_groups=1, group_top=1))])
+def test_the_best_lie_next_to_each_other(E, how, biased, dtype):
+    """The chosen, and sometimes those that are as good or nearly so, are neighbours."""
+    rng = np.random.default_rng(E + biased)
+    T, k, n = 5000, 8, 16
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    at = rng.integers(0, E // n, T)[:, None] * n + np.arange(n)
+    order = np.argsort(rng.random((T, n)), 1)
+    best = (5 + 0.25 * order).astype(np.float32)
+    near = rng.integers(0, 4, T)                                 # apart; one, two steps, or nothing between 8 and 9
+    eighth = np.float32(5 + 0.25 * (n - k))
+    ninth = {1: np.nextafter(eighth, np.float32(0)), 2: np.nextafter(np.nextafter(eighth, np.float32(0)), np.float32(0)), 3: eighth}
+    for c, v in ninth.items():
+        rows = np.where(near == c)[0]
+        best[rows, np.argmax(order[rows] == n - k - 1, 1)] = v
+    np.put_along_axis(l, at, best, 1)
+    bias = np.repeat(rng.integers(-60, 61, E // n) * 1e-3, n) if biased else None
+    l, r, dg, dl = _run(l, bias, k, dtype, **how)
+    _check(l, None if bias is None else bias.astype(np.float32), k, r, dg, dl, **how)
+
+
 def test_bad_logits_are_reported():
     """A token of masked experts only, NaN, +inf, a bias that is not finite: read
     as masked (as 0), reported, and the other tokens are as without them."""
