@@ -9,7 +9,8 @@
 // The choice is that of u in 64 bits, whatever the GPU, found in steps:
 //   - keys of 32 bits that hold the leading bits of u in fp32 and the expert's
 //     index, so that a round of the choice is one maximum over the lanes (comparing
-//     values and indices took 750 instructions a token of 128 experts; 290 now);
+//     values and indices took 750 instructions a token of 128 experts; 290 with keys, 240
+//     where lanes sort theirs, score_many.cu);
 //   - where these bits and the error of fp32 (near_of, near_pair) leave it open, the
 //     candidates in full fp32, and those that are still too close in pairs of fp32
 //     numbers (order; a few tokens in a thousand with 256 sigmoid scores, one in a
@@ -27,7 +28,7 @@
 // Measured (GB300, fp32 logits, top 8, with the permutation): 1 token of 256 experts
 // in 8 groups 5.5 us; 1500 tokens 15 us; 16384 tokens 23 us; 65536 tokens of 128 experts,
 // softmax with a bias, 36 us (logits from HBM: 5 us).  The choice is bound by
-// instructions (62% of the issue slots with 65536 tokens, 41% with 16384, where a
+// instructions (59% of the issue slots with 65536 tokens, 35% with 16384, where a
 // block has 27 warps' worth of tokens for 16 warps), the permutation (6 us) by its
 // chain of dependent steps, 4000 cycles of it the other blocks' histograms.
 #include "score_route.cuh"
