@@ -464,12 +464,12 @@ __device__ __noinline__ bool exact_groups(const ScoreArgs& a, const X* row, cons
                                           float top, float inv, bool* sure) {
   const int lane = threadIdx.x & 31;
   const unsigned below = (1u << lane) - 1u;
-  bool bad = false;
-  float v[3] = {-INFINITY, -INFINITY, -INFINITY};          // lane g: its best three, the last known by value
-  float lg[3] = {}, bg[3] = {};
+  bool bad = false, unsure = false;
+  float worst = -INFINITY, lg[2] = {}, bg[2] = {};         // lane g: its group's best one or two, the last of them by value
   for (int g = 0; g < a.groups; ++g) {
     uint32_t gone = 0;
-    for (int r = 0; r <= a.group_top; ++r) {
+    float first = -INFINITY, last = -INFINITY, ll = 0.f, bl = 0.f;
+    for (int r = 0; r < a.group_top; ++r) {
       uint32_t m = 0;
       int at = 0;
 #pragma unroll
@@ -485,21 +485,37 @@ __device__ __noinline__ bool exact_groups(const ScoreArgs& a, const X* row, cons
       const bool win = (who >> lane & 1u) && !(who & below);
       if (win) gone |= 1u << at;
       const int x = __shfl_sync(kAll, lane * C + at, who ? __ffs(who) - 1 : 0);
+      last = f ? value_of(f) : -INFINITY;
+      ll = f ? logit(a, row, x, &bad) : -INFINITY;
+      bl = f ? bias_of(a, x) : 0.f;
+      if (r == 0) first = last;
       if (lane == g) {
-        const float lx = f ? logit(a, row, x, &bad) : -INFINITY, bx = f ? bias_of(a, x) : 0.f;
-        if (r == 0) { v[0] = f ? value_of(f) : -INFINITY; lg[0] = lx; bg[0] = bx; }
-        else if (r == 1) { v[1] = f ? value_of(f) : -INFINITY; lg[1] = lx; bg[1] = bx; }
-        else { v[2] = f ? value_of(f) : -INFINITY; lg[2] = lx; bg[2] = bx; }
+        worst = last;
+        if (r == 0) { lg[0] = ll; bg[0] = bl; }
+        else { lg[1] = ll; bg[1] = bl; }
       }
     }
+    // Which are the best is certain if no other one comes close to the last of them (the first of two may),
+    // or if all that do are the same as it.  (Next to twins of it, a close one may lie above
+    // them that fp32 has below, or below them that it has among the best.)
+    auto close = [&](float w) {
+      return last > -INFINITY && w > -INFINITY &&
+             !(fabsf(last - w) > near_of<C>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(w))));
+    };
+    int count = 0;
+    bool other = false;
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      const int x = lane * C + q;
+      if (x < g * a.group_size || x >= (g + 1) * a.group_size || !key[q] || !close(value_of(key[q]))) continue;
+      ++count;
+      other = other || !(logit(a, row, x, &bad) == ll && bias_of(a, x) == bl);
+    }
+    count = __reduce_add_sync(kAll, count);
+    const bool mixed = __any_sync(kAll, other);
+    if (lane == g) unsure = mixed && count > (a.group_top == 2 && close(first) ? 2 : 1);
   }
-  // the group's best are certain if the next one lies apart or is the same
-  const int t = a.group_top;
-  const float last = t == 1 ? v[0] : v[1], next = t == 1 ? v[1] : v[2];
-  const float ll = t == 1 ? lg[0] : lg[1], bl = t == 1 ? bg[0] : bg[1], ln = t == 1 ? lg[1] : lg[2], bn = t == 1 ? bg[1] : bg[2];
-  bool unsure = lane < a.groups && next > -INFINITY && !(last - next > near_of<C>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(next)))) &&
-                !(ll == ln && bl == bn);
-  const bool live = lane < a.groups && last > -INFINITY;     // (a group with a masked one among its best counts as -inf)
+  const bool live = lane < a.groups && worst > -INFINITY;    // (a group with a masked one among its best counts as -inf)
   const bool stays = better_groups(a, lg[0], bg[0], lg[1], bg[1], live, lane, 0, 0, top,
                                    a.sigmoid ? Pair{} : softmax_scale(a, row, top), &unsure);
   *sure = !__any_sync(kAll, unsure);
