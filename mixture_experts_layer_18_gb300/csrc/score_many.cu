@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
         again = hi > -INFINITY && !(lo - hi > gap || (by_logit && kLossless));
         if (a.seg == 1 && !by_logit && __any_sync(kAll, again)) {
           // a lane's own best: those of its first three by their fp32 values, if no other
-          // comes near the last of them without being the same
+          // comes near the last of them without being the same, and no other at all where one of the best does
           float x[3], bx[3], f[3];
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
@@ -351,11 +351,13 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
           const bool two = a.group_top == 2;
           const float least = two ? f[1] : f[0], xl = two ? x[1] : x[0], bl = two ? bx[1] : bx[0];
           const bool live = own < a.groups && least > -INFINITY;
-          auto apart = [&](float v, float lead) {
-            return !(v > -INFINITY) || least - v > near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(least), fabsf(v))) + lead * fabsf(v);
+          auto apart = [&](float hi, float lo, float lead) {
+            return !(lo > -INFINITY) || hi - lo > near_of<CL>(a.sigmoid, inv, fmaxf(fabsf(hi), fabsf(lo))) + lead * fabsf(lo);
           };
-          bool unsure = live && !((two || apart(f[1], 0.f) || (x[1] == xl && bx[1] == bl)) &&
-                                  (apart(f[2], 0.f) || (x[2] == xl && bx[2] == bl)) && apart(leading(list[3]), kLead));
+          auto same = [&](int i) { return x[i] == xl && bx[i] == bl; };
+          const bool third = apart(least, f[2], 0.f);
+          bool unsure = live && !((two ? third || same(0) || apart(f[0], least, 0.f) : same(1) || apart(least, f[1], 0.f)) &&
+                                  (third || same(2)) && apart(least, leading(list[3]), kLead));
           const Pair scale = a.sigmoid ? Pair{} : softmax_scales(a, row, top, __ballot_sync(kAll, again));
           const bool s = better_groups(a, x[0], bx[0], x[1], bx[1], live, own, first, 0, top, scale, &unsure);
           const unsigned open = __ballot_sync(kAll, unsure);

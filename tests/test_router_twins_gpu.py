@@ -64,3 +64,19 @@ def test_groups_whose_best_are_twins(score, E, groups, top_groups, group_top, ma
         how = dict(score=score, groups=groups, top_groups=top_groups, group_top=group_top)
         x, r, dg, dl = _run(_many(l, many), bias, 4, **how)
         _check(x, bias, 4, r, dg, dl, **how)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,top_groups", [(64, 8, 3), (256, 8, 4), (60, 6, 2), (96, 3, 1), (320, 32, 9)])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("many", [False, True])
+def test_two_groups_with_a_close_one_next_to_twins(score, E, groups, top_groups, group_top, many):
+    """The same where the other groups have twins alone, whose best are certain."""
+    rng = np.random.default_rng(2 * E + groups + group_top)
+    size = E // groups
+    for each in (2, 3):
+        at = np.stack([g * size + rng.permutation(min(size, 7))[:each + 1] for g in range(groups)])
+        l, bias = _rows(rng, 600, E, score, at[:, 1:].reshape(-1), at[:2, 0])
+        how = dict(score=score, groups=groups, top_groups=top_groups, group_top=group_top)
+        x, r, dg, dl = _run(_many(l, many), bias, 4, **how)
+        _check(x, bias, 4, r, dg, dl, **how)
