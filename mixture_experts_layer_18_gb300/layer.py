@@ -64,19 +64,13 @@ class MoELayer:
                                   **u8)
         self.layout = moe_saved_layout_of(self.dims)
         self.saved = torch.empty(self.layout.total, **u8)
-        self._views = {}
         self.status = torch.zeros(4, **i32)
 
     # ------------------------------------------------------------- views
     def _view(self, offset, rows, cols):
-        """Rows of `saved`; made once for each buffer that is there."""
-        if self._views.get("of") is not self.saved:
-            self._views = {"of": self.saved}
-        known = self._views.get((offset, cols))
-        if known is None:
-            n = rows * cols * (4 if self.dtype == torch.float32 else 2)
-            known = self._views[(offset, cols)] = self.saved[offset:offset + n].view(self.dtype).view(rows, cols)
-        return known
+        """Rows of `saved` as it is now (a caller may replace its memory), a tensor of its own each time."""
+        n = rows * cols * (4 if self.dtype == torch.float32 else 2)
+        return self.saved[offset:offset + n].view(self.dtype).view(rows, cols)
 
     @property
     def x_perm(self):
