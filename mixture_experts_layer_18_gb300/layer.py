@@ -17,9 +17,12 @@ from . import (MOE_BF16, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_F32, MOE_
 
 MODES = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "fp8_bwd": MOE_FP8_BWD}
 
-
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# torch.cuda.current_device() without its first-call initialisation and
+# torch.cuda.current_stream(index).cuda_stream without the Stream object (3 us); a torch
+# without CUDA has neither, and its own calls say so
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _ptr(t):
@@ -27,7 +30,6 @@ def _ptr(t):
 
 
 def _stream(stream):
-    # (torch.cuda.current_stream() without the Stream object)
     return _current_stream(_current_device()) if stream is None else stream.cuda_stream
 
 

@@ -26,18 +26,12 @@ from . import (MOE_ERR_INVALID_ARG, MOE_INDEX_I32, MOE_INDEX_I64, MOE_OK, MOE_RE
                moe_quantize_mxfp8, moe_rms_dims, moe_rms_norm, moe_rms_norm_backward,
                moe_rms_norm_workspace_size, moe_route_out, moe_router, moe_router_backward,
                moe_router_dims, moe_router_workspace_size, moe_xent_dims)
-from .layer import _ptr
+from .layer import _current_device, _current_stream, _ptr
 
 TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
 INDEX_TYPES = {torch.int32: MOE_INDEX_I32, torch.int64: MOE_INDEX_I64}
 SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 REDUCTIONS = {"none": MOE_REDUCE_NONE, "sum": MOE_REDUCE_SUM, "mean": MOE_REDUCE_MEAN}
-
-
-# torch.cuda.current_stream(index).cuda_stream without the Stream object (3 us),
-# torch.cuda.current_device() without its first-call initialisation
-_current_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
 
 
 def _require(ok, what):

@@ -1,11 +1,14 @@
 """MoELayer's Python side on host tensors."""
 import gc
+import subprocess
+import sys
 import weakref
 
 import numpy as np
 import pytest
 import torch
 
+from conftest import ROOT
 from mixture_experts_layer_18_gb300 import layer
 
 
@@ -48,3 +51,13 @@ def test_views_hold_no_memory(L):
         replace(torch.empty(L.layout.total, dtype=torch.uint8))
         gc.collect()
         assert gone() is None
+
+
+def test_import_needs_no_cuda_in_torch():
+    """A torch built without CUDA lacks these two; its own message comes at the first call."""
+    code = ("import torch; del torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream\n"
+            "from mixture_experts_layer_18_gb300 import layer, training\n"
+            "assert training._current_device is layer._current_device is torch.cuda.current_device\n"
+            "assert callable(layer._current_stream) and training._current_stream is layer._current_stream\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
