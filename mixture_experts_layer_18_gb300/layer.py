@@ -66,6 +66,8 @@ class MoELayer:
                                   **u8)
         self.layout = moe_saved_layout_of(self.dims)
         self.saved = torch.empty(self.layout.total, **u8)
+        self._no_h13 = None          # address of `saved`, where the last forward kept no h13 in it
+        self._replays = False        # a forward that keeps h13 has been captured into a graph
         self.status = torch.zeros(4, **i32)
 
     # ------------------------------------------------------------- views
@@ -88,6 +90,7 @@ class MoELayer:
 
     @property
     def h13(self):
+        self._no_h13 = None          # (the caller may write it)
         return self._view(self.layout.h13, self.max_rows, 2 * self.I)
 
     @property
@@ -124,8 +127,9 @@ class MoELayer:
         return route.route_out
 
     def forward(self, X, W13, W2, Y, stream=None, save=None, route=None):
-        """save: None = the layer's setting; False = inference / checkpointed
-        first pass (h13 not kept); True = keep h13 for moe_backward.
+        """save: None = the layer's setting; False = inference, or a first pass
+        that is run again before its backward (h13 not kept, so that ``save``
+        refuses); True = keep h13 for ``backward`` or ``save``.
         route: a training.Router that holds the routing, in place of the
         layer's own (``route`` above)."""
         dims = self.dims
@@ -137,6 +141,15 @@ class MoELayer:
                          self.ws_fwd.numel(), _ptr(self.status), _stream(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_forward")
+        self._keeps_h13(dims.save_for_backward)
+
+    def _keeps_h13(self, kept):
+        """Notes for ``save`` whether `saved` holds this call's h13.  A captured call
+        runs when its graph is replayed, which is not seen here."""
+        if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+            self._replays = self._replays or bool(kept)
+        else:
+            self._no_h13 = None if kept else _ptr(self.saved)
 
     def backward(self, dY, W13, W2, dX, dW13, dW2, dgate, stream=None, route=None):
         rc = moe_backward(self.dims, _ptr(dY), _ptr(W13), _ptr(W2), self._route(route),
@@ -174,7 +187,10 @@ class MoELayer:
     def save(self, checkpoint, X=None, stream=None, route=None):
         """After ``forward``: X and h13 into the checkpoint, in 8 bits.  X None:
         ``checkpoint.x`` holds its codes already (RMSNorm.forward(encoded=) wrote
-        them).  Another forward may then use the layer's buffers."""
+        them).  Another forward may then use the layer's buffers.  Refused after a
+        forward that kept no h13 (save=False)."""
+        if self._no_h13 is not None and self._no_h13 == _ptr(self.saved) and not self._replays:
+            raise MoEError(MOE_ERR_INVALID_ARG, "save: the last forward kept no h13 (save=False)")
         rc = moe_checkpoint_save(self.dims, None if X is None else _ptr(X), self._route(route), _ptr(self.saved),
                                  self.saved.numel(), self._checkpoint(checkpoint, X), _ptr(self.status),
                                  _stream(stream))
@@ -188,6 +204,7 @@ class MoELayer:
                                     self.saved.numel(), _ptr(self.status), _stream(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_checkpoint_restore")
+        self._keeps_h13(True)
 
     # --------------------------------------------------------- allocation
     def empty_io(self):

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from conftest import ROOT
-from mixture_experts_layer_18_gb300 import layer
+from mixture_experts_layer_18_gb300 import MOE_ERR_INVALID_ARG, MoEError, layer, training
 
 
 @pytest.fixture
@@ -61,3 +61,66 @@ def test_import_needs_no_cuda_in_torch():
             "assert callable(layer._current_stream) and training._current_stream is layer._current_stream\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.fixture
+def calls(L, monkeypatch):
+    """L with a library that does nothing; the names of the calls that reach it."""
+    seen = []
+    for name in ("moe_forward", "moe_checkpoint_save", "moe_checkpoint_restore"):
+        monkeypatch.setattr(layer, name, lambda *a, name=name: seen.append(name) or 0)
+    monkeypatch.setattr(layer, "_stream", lambda s: 0)
+    monkeypatch.setattr(layer, "_current_device", lambda: None)
+
+    def device(self, _):
+        self.index, self.device = -1, torch.device("cpu")
+    monkeypatch.setattr(training._Op, "_device", device)
+    return seen
+
+
+def test_save_needs_the_forwards_h13(L, calls):
+    """After a forward that kept none, an earlier one's would go into the checkpoint."""
+    ck, X = L.checkpoint(), torch.zeros((4, 64), dtype=torch.bfloat16)
+
+    def refused():
+        calls.clear()
+        with pytest.raises(MoEError) as e:
+            L.save(ck, X)
+        return e.value.code == MOE_ERR_INVALID_ARG and not calls
+
+    def forward(save):
+        L.forward(X, X, X, X, save=save)
+    L.save(ck, X)                                # (what the caller wrote itself)
+    for again in (lambda: forward(True), lambda: forward(None), lambda: L.restore(ck), lambda: L.h13.fill_(1),
+                  lambda: setattr(L, "saved", torch.empty(L.layout.total, dtype=torch.uint8))):
+        forward(True)
+        L.save(ck, X)
+        forward(False)
+        assert refused() and refused()
+        again()
+        calls.clear()
+        L.save(ck, X)
+        assert calls == ["moe_checkpoint_save"]
+
+
+def test_save_after_captured_forwards(L, calls, monkeypatch):
+    """A captured call changes nothing yet; once one that keeps h13 has been captured, its replays may
+    have come after any other call."""
+    ck, X, capturing = L.checkpoint(), torch.zeros((4, 64), dtype=torch.bfloat16), [False]
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+
+    def forward(save, captured=False):
+        capturing[0] = captured
+        L.forward(X, X, X, X, save=save)
+        capturing[0] = False
+    forward(True)
+    forward(False, captured=True)
+    L.save(ck, X)
+    forward(False)
+    with pytest.raises(MoEError):
+        L.save(ck, X)
+    forward(True, captured=True)
+    L.save(ck, X)
+    forward(False)
+    L.save(ck, X)
