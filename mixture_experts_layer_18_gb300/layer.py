@@ -65,16 +65,44 @@ class MoELayer:
         self.ws_bwd = torch.empty(moe_workspace_size(self.dims, MOE_WS_BACKWARD) if backward else 0,
                                   **u8)
         self.layout = moe_saved_layout_of(self.dims)
-        self.saved = torch.empty(self.layout.total, **u8)
-        self._no_h13 = None          # address of `saved`, where the last forward kept no h13 in it
+        self._saved, self._views = torch.empty(self.layout.total, **u8), {}
+        self._no_h13 = None          # where the last forward kept no h13: address and version of `saved`
         self._replays = False        # a forward that keeps h13 has been captured into a graph
         self.status = torch.zeros(4, **i32)
 
     # ------------------------------------------------------------- views
+    @property
+    def saved(self):
+        """The buffer of saved activations, which may be replaced.  (Whoever takes it may
+        also replace its memory, or write it: no view is kept that would hold the old
+        one, and what it holds is not known.)"""
+        self._views, self._no_h13 = {}, None
+        return self._saved
+
+    @saved.setter
+    def saved(self, buffer):
+        self._views, self._saved, self._no_h13 = {}, buffer, None
+
+    @saved.deleter
+    def saved(self):
+        self._views = {}
+        del self._saved
+
     def _view(self, offset, rows, cols):
-        """Rows of `saved` as it is now (a caller may replace its memory), a tensor of its own each time."""
-        n = rows * cols * (4 if self.dtype == torch.float32 else 2)
-        return self.saved[offset:offset + n].view(self.dtype).view(rows, cols)
+        """Rows of `saved` as it is now, a tensor of its own each time.  (Made from one
+        that is kept while the memory stays: 1.1 us instead of 5.8.)"""
+        buffer, views = self._saved, self._views
+        at = (buffer.data_ptr(), buffer.numel(), self.dtype)
+        if views.get("at") != at:
+            views = self._views = {"at": at}
+        kept = views.get((offset, rows, cols))
+        if kept is None:
+            n = rows * cols * (4 if self.dtype == torch.float32 else 2)
+            kept = buffer[offset:offset + n].view(self.dtype).view(rows, cols)
+            if torch.is_inference_mode_enabled():        # (an inference tensor for good)
+                return kept
+            views[offset, rows, cols] = kept
+        return kept.view(rows, cols)
 
     @property
     def x_perm(self):
@@ -137,7 +165,7 @@ class MoELayer:
             dims = moe_dims(self.dims.T, self.dims.H, self.dims.E, self.dims.I, self.dims.top_k,
                             self.dims.mode, 1 if save else 0)
         rc = moe_forward(dims, _ptr(X), _ptr(W13), _ptr(W2), self._route(route), _ptr(Y),
-                         _ptr(self.saved), self.saved.numel(), _ptr(self.ws_fwd),
+                         _ptr(self._saved), self._saved.numel(), _ptr(self.ws_fwd),
                          self.ws_fwd.numel(), _ptr(self.status), _stream(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_forward")
@@ -145,15 +173,17 @@ class MoELayer:
 
     def _keeps_h13(self, kept):
         """Notes for ``save`` whether `saved` holds this call's h13.  A captured call
-        runs when its graph is replayed, which is not seen here."""
+        runs when its graph is replayed, which is not seen here; nor are writes to an
+        inference tensor."""
         if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
             self._replays = self._replays or bool(kept)
         else:
-            self._no_h13 = None if kept else _ptr(self.saved)
+            b = self._saved
+            self._no_h13 = None if kept or b.is_inference() else (b.data_ptr(), b._version)
 
     def backward(self, dY, W13, W2, dX, dW13, dW2, dgate, stream=None, route=None):
         rc = moe_backward(self.dims, _ptr(dY), _ptr(W13), _ptr(W2), self._route(route),
-                          _ptr(self.saved), self.saved.numel(), _ptr(dX), _ptr(dW13), _ptr(dW2),
+                          _ptr(self._saved), self._saved.numel(), _ptr(dX), _ptr(dW13), _ptr(dW2),
                           _ptr(dgate), _ptr(self.ws_bwd), self.ws_bwd.numel(),
                           _ptr(self.status), _stream(stream))
         if rc != MOE_OK:
@@ -188,11 +218,12 @@ class MoELayer:
         """After ``forward``: X and h13 into the checkpoint, in 8 bits.  X None:
         ``checkpoint.x`` holds its codes already (RMSNorm.forward(encoded=) wrote
         them).  Another forward may then use the layer's buffers.  Refused after a
-        forward that kept no h13 (save=False)."""
-        if self._no_h13 is not None and self._no_h13 == _ptr(self.saved) and not self._replays:
+        forward that kept no h13 (save=False), unless it was written otherwise:
+        by ``restore``, by torch, or by whoever looked at ``h13`` or ``saved`` since."""
+        if self._no_h13 and self._no_h13 == (self._saved.data_ptr(), self._saved._version) and not self._replays:
             raise MoEError(MOE_ERR_INVALID_ARG, "save: the last forward kept no h13 (save=False)")
-        rc = moe_checkpoint_save(self.dims, None if X is None else _ptr(X), self._route(route), _ptr(self.saved),
-                                 self.saved.numel(), self._checkpoint(checkpoint, X), _ptr(self.status),
+        rc = moe_checkpoint_save(self.dims, None if X is None else _ptr(X), self._route(route), _ptr(self._saved),
+                                 self._saved.numel(), self._checkpoint(checkpoint, X), _ptr(self.status),
                                  _stream(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_checkpoint_save")
@@ -200,8 +231,8 @@ class MoELayer:
     def restore(self, checkpoint, stream=None, route=None):
         """Before ``backward``: the saved activations of the checkpoint's
         forward, whose routing ``route`` (or the layer's own) still has to hold."""
-        rc = moe_checkpoint_restore(self.dims, self._checkpoint(checkpoint), self._route(route), _ptr(self.saved),
-                                    self.saved.numel(), _ptr(self.status), _stream(stream))
+        rc = moe_checkpoint_restore(self.dims, self._checkpoint(checkpoint), self._route(route), _ptr(self._saved),
+                                    self._saved.numel(), _ptr(self.status), _stream(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_checkpoint_restore")
         self._keeps_h13(True)

@@ -53,6 +53,43 @@ def test_views_hold_no_memory(L):
         assert gone() is None
 
 
+def test_views_after_other_ways_to_replace_the_memory(L):
+    """By a reference taken before, by size alone, in place; and without a buffer."""
+    buffer = L.saved
+    for n in VIEWS:
+        getattr(L, n)
+    buffer.data = torch.empty(L.layout.total, dtype=torch.uint8)
+    assert L.h13.data_ptr() == buffer.data_ptr() + L.layout.h13
+    buffer.data = buffer.data[:L.layout.act]
+    assert L.h13.data_ptr() == buffer.data_ptr() + L.layout.h13
+    with pytest.raises(RuntimeError):
+        L.act
+    del L.saved, buffer
+    with pytest.raises(AttributeError):
+        L.h13
+    L.saved = torch.zeros(L.layout.total, dtype=torch.uint8)
+    assert not L.h13.any()
+
+
+def test_views_seen_in_inference_mode_first(L):
+    """They do not make later ones inference tensors, which could not be written."""
+    with torch.inference_mode():
+        for n in VIEWS:
+            getattr(L, n)
+    for n in VIEWS:
+        getattr(L, n).fill_(1)
+    assert not L.h13.is_inference() and L.h13.eq(1).all()
+
+
+def test_views_share_the_buffer_and_nothing_else(L):
+    for n in VIEWS:
+        a, b = getattr(L, n), getattr(L, n)
+        a.fill_(2)
+        assert b.eq(2).all() and b._version == a._version == L.saved._version
+        a.requires_grad_()
+        assert not b.requires_grad and not getattr(L, n).requires_grad
+
+
 def test_import_needs_no_cuda_in_torch():
     """A torch built without CUDA lacks these two; its own message comes at the first call."""
     code = ("import torch; del torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream\n"
@@ -91,7 +128,10 @@ def test_save_needs_the_forwards_h13(L, calls):
     def forward(save):
         L.forward(X, X, X, X, save=save)
     L.save(ck, X)                                # (what the caller wrote itself)
-    for again in (lambda: forward(True), lambda: forward(None), lambda: L.restore(ck), lambda: L.h13.fill_(1),
+    buffer, h13 = L.saved, L.h13
+    for again in (lambda: forward(True), lambda: forward(None), lambda: L.restore(ck), lambda: h13.fill_(1),
+                  lambda: buffer[L.layout.h13:L.layout.act].zero_(), lambda: L.h13, lambda: L.saved,
+                  lambda: setattr(buffer, "data", torch.empty(L.layout.total, dtype=torch.uint8)),
                   lambda: setattr(L, "saved", torch.empty(L.layout.total, dtype=torch.uint8))):
         forward(True)
         L.save(ck, X)
