@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kManyThreads<CL>, 1) score_many_kernel(const _
     const bool none = !(__ballot_sync(kAll, l > -INFINITY) >> first & 0xffu);
     float w = !(l > -INFINITY) ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - top);
     if (a.renorm) {
-      const bool small = !(__ballot_sync(kAll, l > -60.f) >> first & 0xffu);
+      const bool small = __ballot_sync(kAll, l > -INFINITY && l < -87.f) >> first & 0xffu;
       if (!a.sigmoid || __any_sync(kAll, small)) {
         const float x = a.sigmoid ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;
         const float m = value_of(max8(key_of(x)));

@@ -398,8 +398,9 @@ __global__ void __launch_bounds__(kRouteThreads<C>) score_route_kernel(const __g
     const bool none = !__any_sync(kAll, l > -INFINITY);
     float w = !(l > -INFINITY) ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - top);
     if (a.renorm) {
-      // relative to the largest chosen score where sigmoids are small (their sum may be 0), and for the softmax
-      if (!a.sigmoid || !__any_sync(kAll, l > -60.f)) {
+      // relative to the largest chosen score for the softmax, and where a sigmoid leaves the range of
+      // fp32's normal numbers (below e^-87), which its gate need not do
+      if (!a.sigmoid || __any_sync(kAll, l > -INFINITY && l < -87.f)) {
         const float x = a.sigmoid ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;      // log s (+ a constant)
         const float m = value_of(__reduce_max_sync(kAll, key_of(x)));
         w = l > -INFINITY ? expf(x - m) : 0.f;
