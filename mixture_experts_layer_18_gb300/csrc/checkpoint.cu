@@ -89,9 +89,10 @@ struct CkptArgs {
 
 // Steps of 256 columns in a warp's unit of work: of a row to save or to decode; of
 // a token's row to restore (stored k times); of each half of h13 to restore.
-// (16384 tokens, H 2048, I 768, 8 of 128: save 117 us with 4, 136 with 2 and 141 with 8;
-// restore 233 with 2 and 3, 241 with 4 and 3, 276 with 4 and 2, which leaves half of a
-// unit idle.)
+// (16384 tokens, 8 of 128, H 2048.  Save: I 768 117 us with 4, 137 with 2, 141 with 8; I 512 77,
+// 99, 124; I 1024 136, 178, 171.  Restore with 2 steps of X and 3 of a half: I 768 220 us, I 512
+// 184, I 1024 276, I 1408 329; with 2 and 4 220, 182, 261, 329; 2 and 2 223, 178, 263, 330; 4
+// and 3 241, 209, 319, 371; 1 and 3 222, 181, 268, 329.)
 constexpr int kPieces = 4, kTokenPieces = 2, kHalfPieces = 3;
 constexpr int kUnit = 256 * kPieces;
 
@@ -291,7 +292,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const uint8_t* q, cons
 
 // Blocks for `units` warps' worth of work: at most `per_sm` per SM.  (Saving reads
 // most: eight, all there is room for; writing more it goes faster with blocks that come
-// and go: restoring as above 492 us with eight and H 4096, I 1536, 458 with 64.)
+// and go: restoring as above 457 us with eight and H 4096, I 1536, 440 with 64; H 2048, I 768
+// 230 and 220.)
 unsigned blocks_for(int64_t units, int per_sm) {
   const int64_t need = (units + kThreads / 32 - 1) / (kThreads / 32), most = (int64_t)sm_count() * per_sm;
   return (unsigned)(need < 1 ? 1 : need < most ? need : most);

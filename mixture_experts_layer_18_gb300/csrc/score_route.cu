@@ -28,9 +28,17 @@
 // Measured (GB300, fp32 logits, top 8, with the permutation): 1 token of 256 experts
 // in 8 groups 5.5 us; 1500 tokens 15 us; 16384 tokens 23 us; 65536 tokens of 128 experts,
 // softmax with a bias, 36 us (logits from HBM: 5 us).  The choice is bound by
-// instructions (59% of the issue slots with 65536 tokens, 35% with 16384, where a
-// block has 27 warps' worth of tokens for 16 warps), the permutation (6 us) by its
-// chain of dependent steps, 4000 cycles of it the other blocks' histograms.
+// instructions with 65536 tokens (59% of the issue slots); with 16384 of 256 experts by the
+// latency of what a warp does in turn and by its split (35%: a block has 27 units of four
+// tokens for 16 warps, which is what the registers leave room for, so some warps take two);
+// the permutation (6 us) by its chain of dependent steps, 4000 cycles of it the other
+// blocks' histograms.  What does not fit eight lanes per token, 16384 tokens: 384 experts,
+// sigmoid with a bias, 52 us; 512, top 10, softmax, 39; 1024 96; 256, top 16, 44.
+//
+// Values that fp32 cannot order cost more.  A third of 16384 tokens with logits of zero: 141
+// us instead of 23 in 8 groups of 256 experts, 36 instead of 15 without a bias (128
+// experts; both look at such a token by a whole warp, choose32), no difference without
+// groups and with a bias.
 #include "score_route.cuh"
 
 namespace moe {
@@ -610,7 +618,9 @@ __global__ void __launch_bounds__(256) balance_bias_kernel(const int32_t* counts
 
 // Blocks of the router: one of up to 32 warps per SM for many tokens, of four
 // tokens (a warp each) for few; one block that places its tokens too for at most
-// kFusedTokens.  (More than 65535 would not fit the histograms' 16 bits.)
+// kFusedTokens.  (More than 65535 would not fit the histograms' 16 bits.)  kMostBlocks is
+// this GPU's number of SMs: where fewer are at hand the last blocks run after the others, with
+// the same results; the workspace has room for that many on any device.
 constexpr int kMostBlocks = 152, kFusedTokens = 32;
 int tokens_per_block(int T) {
   const int per = (int)(((int64_t)T + kMostBlocks - 1) / kMostBlocks);

@@ -616,7 +616,9 @@ __device__ __noinline__ int choose32(const ScoreArgs& a, const X* row, uint2* sl
   if (by_logit) return sel_e;
   bool unused = false;
   const float l = sel.x ? logit(a, row, sel_e, &unused) : -INFINITY, b = sel.x ? bias_of(a, sel_e) : 0.f;
-  bool more = false;                       // close ones that found no place among the candidates
+  // (with all places taken others may be as close: known only if all that come close to the
+  // k-th, candidates or not, are the same as it, so that their order is that of their indices)
+  bool more = false;
   if (n == 32) {
     const float lk = __shfl_sync(kAll, l, a.k - 1), bk = __shfl_sync(kAll, b, a.k - 1);
 #pragma unroll
