@@ -33,6 +33,20 @@ def _stream(stream):
     return _current_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
+def _may_be_captured(stream):
+    """Whether a call on this stream (None: the current one) may have been captured
+    into a graph.  torch tells of the current stream only, and raises if it cannot tell
+    for another thread's or stream's capture."""
+    if not torch.cuda.is_initialized():
+        return False
+    if stream is not None and stream.cuda_stream != _current_stream(_current_device()):
+        return True
+    try:
+        return torch.cuda.is_current_stream_capturing()
+    except RuntimeError:
+        return True
+
+
 class MoELayer:
     """Buffers of one (T, H, E, I, top_k, mode) problem on one device."""
 
@@ -169,13 +183,13 @@ class MoELayer:
                          self.ws_fwd.numel(), _ptr(self.status), _stream(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_forward")
-        self._keeps_h13(dims.save_for_backward)
+        self._keeps_h13(dims.save_for_backward, stream)
 
-    def _keeps_h13(self, kept):
+    def _keeps_h13(self, kept, stream):
         """Notes for ``save`` whether `saved` holds this call's h13.  A captured call
         runs when its graph is replayed, which is not seen here; nor are writes to an
         inference tensor."""
-        if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+        if _may_be_captured(stream):
             self._replays = self._replays or bool(kept)
         else:
             b = self._saved
@@ -220,7 +234,8 @@ class MoELayer:
         them).  Another forward may then use the layer's buffers.  Refused after a
         forward that kept no h13 (save=False), unless it was written otherwise:
         by ``restore``, by torch, or by whoever looked at ``h13`` or ``saved`` since."""
-        if self._no_h13 and self._no_h13 == (self._saved.data_ptr(), self._saved._version) and not self._replays:
+        none = self._no_h13
+        if none and not self._replays and none[0] == self._saved.data_ptr() and none[1] == self._saved._version:
             raise MoEError(MOE_ERR_INVALID_ARG, "save: the last forward kept no h13 (save=False)")
         rc = moe_checkpoint_save(self.dims, None if X is None else _ptr(X), self._route(route), _ptr(self._saved),
                                  self._saved.numel(), self._checkpoint(checkpoint, X), _ptr(self.status),
@@ -235,7 +250,7 @@ class MoELayer:
                                     self._saved.numel(), _ptr(self.status), _stream(stream))
         if rc != MOE_OK:
             raise MoEError(rc, "moe_checkpoint_restore")
-        self._keeps_h13(True)
+        self._keeps_h13(True, stream)
 
     # --------------------------------------------------------- allocation
     def empty_io(self):

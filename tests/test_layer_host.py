@@ -164,3 +164,36 @@ def test_save_after_captured_forwards(L, calls, monkeypatch):
     L.save(ck, X)
     forward(False)
     L.save(ck, X)
+
+
+def test_save_after_forwards_on_other_streams(L, calls, monkeypatch):
+    """Which may be captured although the current one is not, or about which torch cannot tell."""
+    class Stream:
+        cuda_stream = 7
+    ck, X, current = L.checkpoint(), torch.zeros((4, 64), dtype=torch.bfloat16), [7]
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(layer, "_current_stream", lambda device: current[0])
+
+    def cannot_tell():
+        raise RuntimeError("a blocking stream is being captured")
+
+    def refused():
+        try:
+            L.save(ck, X)
+        except MoEError:
+            return True
+        return False
+    L.forward(X, X, X, X, stream=Stream, save=False)
+    assert refused()
+    L.forward(X, X, X, X, stream=Stream)
+    current[0] = 8
+    L.forward(X, X, X, X, stream=Stream, save=False)
+    assert not refused()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", cannot_tell)
+    L.forward(X, X, X, X, save=False)
+    assert not refused()
+    L.forward(X, X, X, X)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    L.forward(X, X, X, X, save=False)
+    assert not refused()
