@@ -35,7 +35,7 @@
 // blocks' histograms.  What does not fit eight lanes per token, 16384 tokens: 384 experts,
 // sigmoid with a bias, 52 us; 512, top 10, softmax, 39; 1024 96; 256, top 16, 44.
 //
-// Values that fp32 cannot order cost more.  A third of 16384 tokens with logits of zero: 141
+// Values that fp32 cannot order cost more.  A third of 16384 tokens with logits of zero: 134
 // us instead of 23 in 8 groups of 256 experts, 36 instead of 15 without a bias (128
 // experts; both look at such a token by a whole warp, choose32), no difference without
 // groups and with a bias.

@@ -464,18 +464,17 @@ __device__ __noinline__ bool exact_groups(const ScoreArgs& a, const X* row, cons
                                           float top, float inv, bool* sure) {
   const int lane = threadIdx.x & 31;
   const unsigned below = (1u << lane) - 1u;
-  bool bad = false, unsure = false;
+  bool bad = false;
   float worst = -INFINITY, lg[2] = {}, bg[2] = {};         // lane g: its group's best one or two, the last of them by value
+  uint32_t won = 0;                                        // this lane's experts among these
   for (int g = 0; g < a.groups; ++g) {
-    uint32_t gone = 0;
-    float first = -INFINITY, last = -INFINITY, ll = 0.f, bl = 0.f;
     for (int r = 0; r < a.group_top; ++r) {
       uint32_t m = 0;
       int at = 0;
 #pragma unroll
       for (int q = C - 1; q >= 0; --q) {
         const int x = lane * C + q;
-        if (x >= g * a.group_size && x < (g + 1) * a.group_size && !(gone >> q & 1u) && key[q] >= m && key[q]) {
+        if (x >= g * a.group_size && x < (g + 1) * a.group_size && !(won >> q & 1u) && key[q] >= m && key[q]) {
           m = key[q];
           at = q;
         }
@@ -483,38 +482,32 @@ __device__ __noinline__ bool exact_groups(const ScoreArgs& a, const X* row, cons
       const uint32_t f = __reduce_max_sync(kAll, m);
       const unsigned who = __ballot_sync(kAll, m == f && f);
       const bool win = (who >> lane & 1u) && !(who & below);
-      if (win) gone |= 1u << at;
+      if (win) won |= 1u << at;
       const int x = __shfl_sync(kAll, lane * C + at, who ? __ffs(who) - 1 : 0);
-      last = f ? value_of(f) : -INFINITY;
-      ll = f ? logit(a, row, x, &bad) : -INFINITY;
-      bl = f ? bias_of(a, x) : 0.f;
-      if (r == 0) first = last;
       if (lane == g) {
-        worst = last;
-        if (r == 0) { lg[0] = ll; bg[0] = bl; }
-        else { lg[1] = ll; bg[1] = bl; }
+        const float lx = f ? logit(a, row, x, &bad) : -INFINITY, bx = f ? bias_of(a, x) : 0.f;
+        worst = f ? value_of(f) : -INFINITY;
+        if (r == 0) { lg[0] = lx; bg[0] = bx; }
+        else { lg[1] = lx; bg[1] = bx; }
       }
     }
-    // Which are the best is certain if no other one comes close to the last of them (the first of two may),
-    // or if all that do are the same as it.  (Next to twins of it, a close one may lie above
-    // them that fp32 has below, or below them that it has among the best.)
-    auto close = [&](float w) {
-      return last > -INFINITY && w > -INFINITY &&
-             !(fabsf(last - w) > near_of<C>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(w))));
-    };
-    int count = 0;
-    bool other = false;
-#pragma unroll
-    for (int q = 0; q < C; ++q) {
-      const int x = lane * C + q;
-      if (x < g * a.group_size || x >= (g + 1) * a.group_size || !key[q] || !close(value_of(key[q]))) continue;
-      ++count;
-      other = other || !(logit(a, row, x, &bad) == ll && bias_of(a, x) == bl);
-    }
-    count = __reduce_add_sync(kAll, count);
-    const bool mixed = __any_sync(kAll, other);
-    if (lane == g) unsure = mixed && count > (a.group_top == 2 && close(first) ? 2 : 1);
   }
+  // Which are the best is certain if no other one comes close to the last of them, or if all
+  // that do, among the best too, are the same as it.  (Next to twins of it, a close one may lie
+  // above them that fp32 has below, or below them that it has among the best.)
+  const float lk = a.group_top == 1 ? lg[0] : lg[1], bk = a.group_top == 1 ? bg[0] : bg[1];
+  uint32_t more = 0, mixed = 0;                            // by group
+#pragma unroll 4
+  for (int q = 0; q < C; ++q) {
+    const int x = lane * C + q, g = min(x / a.group_size, a.groups - 1);
+    const float last = __shfl_sync(kAll, worst, g), ll = __shfl_sync(kAll, lk, g), bl = __shfl_sync(kAll, bk, g);
+    const float w = key[q] ? value_of(key[q]) : -INFINITY;
+    if (last > -INFINITY && w > -INFINITY && !(fabsf(last - w) > near_of<C>(a.sigmoid, inv, fmaxf(fabsf(last), fabsf(w))))) {
+      if (!(won >> q & 1u)) more |= 1u << g;
+      if (!(logit(a, row, x, &bad) == ll && bias_of(a, x) == bl)) mixed |= 1u << g;
+    }
+  }
+  bool unsure = (__reduce_or_sync(kAll, more) & __reduce_or_sync(kAll, mixed)) >> lane & 1u;
   const bool live = lane < a.groups && worst > -INFINITY;    // (a group with a masked one among its best counts as -inf)
   const bool stays = better_groups(a, lg[0], bg[0], lg[1], bg[1], live, lane, 0, 0, top,
                                    a.sigmoid ? Pair{} : softmax_scale(a, row, top), &unsure);
